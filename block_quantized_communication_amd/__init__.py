@@ -16,7 +16,16 @@ Functions (names follow the C ABI):
       out_dtype set : hop-2 mode, -> averaged values [chunk] of that dtype
 Each also accepts preallocated outputs (out=...) so that timed loops allocate
 nothing.
+
+Around the communication path (tensors need their element's alignment only):
+  TensorList(tensors)                        a list laid out once for grad_sumsq
+  grad_sumsq(tensors)                        -> sum of squares, f64 [1]
+  AdamW(params, grads, ...)                  the optimizer step over many tensors, states in 32 or 8 bits
+  state8_unpack / state8_pack                8-bit states to and from floats
+  embedding(ids, table, scale)               -> scaled rows; embedding_i8: from qwZ codes and scales
+  embedding_grad(ids, dy, rows, scale)       -> dense gradient of the table
 """
+import contextlib
 import ctypes
 import os
 
@@ -29,7 +38,39 @@ STATUS = {0: "ok", 1: "null pointer", 2: "bad size", 3: "bad block", 4: "misalig
           9: "output overlaps input"}
 
 EXPORTS = ("zpq_quant_i8", "zpq_dequant_i8", "zpq_quant_i8_tensor", "zpq_qgz_reorder_quant_i4",
-           "zpq_qgz_dequant_reduce_requant_i4", "zpq_status_str", "zpq_abi_version")
+           "zpq_qgz_dequant_reduce_requant_i4", "zpq_status_str", "zpq_abi_version",
+           "zpq_list_make", "zpq_grad_sumsq", "zpq_adamw_plan_make", "zpq_adamw_step",
+           "zpq_state8_unpack", "zpq_state8_pack", "zpq_embedding", "zpq_embedding_i8",
+           "zpq_embedding_grad_bytes", "zpq_embedding_grad")
+
+STATE_BLOCK = 256          # elements that share an exponent byte in 8-bit optimizer states
+SUMSQ_BYTES = 32768        # ZPQ_SUMSQ_BYTES
+
+
+class _List(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("elems", ctypes.c_int64), ("chunks", ctypes.c_int64),
+                ("count", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_double)]
+
+
+class _AdamwPlan(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("elems", ctypes.c_int64), ("chunks", ctypes.c_int64),
+                ("count", ctypes.c_int32), ("p_dtype", ctypes.c_int32),
+                ("g_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32), ("chunk_elems", ctypes.c_int32)]
+
+
+class _AdamwHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint64)]
 
 
 class ZpqError(RuntimeError):
@@ -56,8 +97,24 @@ def lib():
         L.zpq_qgz_reorder_quant_i4.argtypes = [vp, i32, i64, i32, i32, i32, vp, vp, vp]
         L.zpq_qgz_dequant_reduce_requant_i4.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp, i32,
                                                         f32, vp]
+        L.zpq_list_make.argtypes = [vp, vp, i32, i32, vp, i64, ctypes.POINTER(_List), vp]
+        L.zpq_grad_sumsq.argtypes = [ctypes.POINTER(_List), vp, i32, vp, i64, vp]
+        L.zpq_adamw_plan_make.argtypes = [ctypes.POINTER(_AdamwTensor), i32, i32, i32, i32, i32, vp,
+                                          i64, ctypes.POINTER(_AdamwPlan), vp]
+        L.zpq_adamw_step.argtypes = [ctypes.POINTER(_AdamwPlan), ctypes.POINTER(_AdamwHyper), vp, vp]
+        L.zpq_state8_unpack.argtypes = [vp, vp, i64, i32, vp, i32, vp]
+        L.zpq_state8_pack.argtypes = [vp, i32, i64, i32, vp, vp, vp]
+        L.zpq_embedding.argtypes = [vp, i32, i64, i64, i64, vp, i32, i64, i64, f32, vp, i32, i64, vp]
+        L.zpq_embedding_i8.argtypes = [vp, vp, i64, i64, i32, vp, i32, i64, i64, f32, vp, i32, i64,
+                                       vp]
+        L.zpq_embedding_grad_bytes.argtypes = [i64, i64, ctypes.POINTER(i64)]
+        L.zpq_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, i64, i64, f32, vp,
+                                         i32, i64, i32, vp, i64, vp]
         for f in (L.zpq_quant_i8, L.zpq_dequant_i8, L.zpq_quant_i8_tensor,
-                  L.zpq_qgz_reorder_quant_i4, L.zpq_qgz_dequant_reduce_requant_i4):
+                  L.zpq_qgz_reorder_quant_i4, L.zpq_qgz_dequant_reduce_requant_i4,
+                  L.zpq_list_make, L.zpq_grad_sumsq, L.zpq_adamw_plan_make, L.zpq_adamw_step,
+                  L.zpq_state8_unpack, L.zpq_state8_pack, L.zpq_embedding, L.zpq_embedding_i8,
+                  L.zpq_embedding_grad_bytes, L.zpq_embedding_grad):
             f.restype = ctypes.c_int
         L.zpq_status_str.argtypes = [ctypes.c_int]
         L.zpq_status_str.restype = ctypes.c_char_p
@@ -229,3 +286,335 @@ def qgz_dequant_reduce_requant_i4(in_codes, in_scales, n_src, chunk, block=128, 
 
 def abi_version():
     return int(lib().zpq_abi_version())
+
+
+# ---------------------------------------------------------------------------
+# Around the communication path: optimizer step, gradient norm, embedding.
+_here = contextlib.nullcontext()
+
+
+def _on(stream, device):
+    """(stream pointer, context): what a call allocates comes from the pool of
+    the stream that it runs on, so that freeing it is ordered with its use."""
+    torch = _torch()
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+        if device.index == torch.cuda.current_device():
+            return ctypes.c_void_p(s.cuda_stream), _here
+    else:
+        s = stream
+        if s.device != device:
+            raise ValueError(f"stream is on {s.device}, the tensors are on {device}")
+    return ctypes.c_void_p(s.cuda_stream), torch.cuda.stream(s)
+
+
+def _one_device(tensors, name):
+    """The tensors' common GPU; each must be contiguous and there."""
+    dev = None
+    for i, t in enumerate(tensors):
+        dev = _gpu(t, f"{name}[{i}]", dev)
+    return dev
+
+
+def _one_dtype(tensors, name):
+    kinds = {t.dtype for t in tensors}
+    if len(kinds) != 1:
+        raise ValueError(f"{name}: need tensors of one type, got {sorted(map(str, kinds))}")
+    return dtype_code(next(iter(kinds)))
+
+
+class TensorList:
+    """Tensors of one type on one GPU, laid out once for grad_sumsq.  Keeps the
+    tensors; their storage must not be replaced (set_, resize_) meanwhile."""
+
+    def __init__(self, tensors, stream=None):
+        torch = _torch()
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("tensors: need at least one")
+        self.device = _one_device(self.tensors, "tensors")
+        dt = _one_dtype(self.tensors, "tensors")
+        n = len(self.tensors)
+        ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        sizes = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
+        st, ctx = _on(stream, self.device)
+        with ctx:
+            self._table = torch.empty(n * 32 + 64, dtype=torch.uint8, device=self.device)
+            self._c = _List()
+            _check(lib().zpq_list_make(ptrs, sizes, n, dt, _ptr(self._table), self._table.numel(),
+                                       ctypes.byref(self._c), st), "zpq_list_make")
+
+
+def grad_sumsq(tensors, out=None, accumulate=False, stream=None):
+    """Sum of squares of all elements, in float64 -> out [1] (out[0] += with
+    accumulate: several lists, one norm).  tensors: a TensorList, or tensors."""
+    torch = _torch()
+    tl = tensors if isinstance(tensors, TensorList) else TensorList(tensors, stream=stream)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    st, ctx = _on(stream, tl.device)
+    with ctx:
+        if out is None:
+            out = torch.empty(1, dtype=torch.float64, device=tl.device)
+        _need(out, torch.float64, 1, "out", tl.device)
+        ws = torch.empty(SUMSQ_BYTES, dtype=torch.uint8, device=tl.device)
+        _check(lib().zpq_grad_sumsq(ctypes.byref(tl._c), _ptr(out), int(accumulate), _ptr(ws),
+                                    SUMSQ_BYTES, st), "zpq_grad_sumsq")
+    return out
+
+
+class AdamW:
+    """The AdamW step over many tensors in one launch.
+
+    params        tensors of one type (float32, or float16 / bfloat16 without a master copy), updated in place
+    grads         their gradients, of one type
+    copies        with float32 params: float16 or bfloat16 tensors that receive the new weights
+    weight_decay  one number, or one per tensor
+    state_bits    32 (float32 moments) or 8 (zpq.h, zpq_adamw_step)
+    exp_avg, exp_avg_sq
+                  existing moments, one per tensor: float32 tensors, or with 8 bits pairs (codes
+                  uint8 [n], exponents uint8 [ceil(n / 256)]); zeros are made where not given
+    seed          of the random rounding of 8-bit states
+
+    Tensors are kept and their addresses laid out once: storage must not be
+    replaced meanwhile; set_grads() takes other gradients."""
+
+    def __init__(self, params, grads, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+                 weight_decay=0.01, state_bits=32, exp_avg=None, exp_avg_sq=None, seed=0, stream=None):
+        torch = _torch()
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("params: need at least one tensor")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits: 8 or 32, got {state_bits}")
+        self.device = _one_device(self.params, "params")
+        self._pd = _one_dtype(self.params, "params")
+        self.state_bits, self.lr, self.betas, self.eps, self.seed = state_bits, lr, tuple(betas), eps, seed
+        count = len(self.params)
+        self.weight_decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * count
+        if len(self.weight_decay) != count:
+            raise ValueError(f"weight_decay: need {count} numbers, got {len(self.weight_decay)}")
+        self.copies = None if copies is None else list(copies)
+        self._cd = -1
+        if self.copies is not None:
+            self._match(self.copies, "copies")
+            self._cd = _one_dtype(self.copies, "copies")
+            if self._cd == ZPQ_F32 or self._pd != ZPQ_F32:
+                raise ValueError("copies: need float16 or bfloat16 tensors beside float32 params")
+        with _on(stream, self.device)[1]:
+            self.exp_avg = self._state(exp_avg, "exp_avg")
+            self.exp_avg_sq = self._state(exp_avg_sq, "exp_avg_sq")
+            self._table = torch.empty(count * 128 + 64, dtype=torch.uint8, device=self.device)
+        self.set_grads(grads, stream=stream)
+
+    def _match(self, tensors, name):
+        if len(tensors) != len(self.params):
+            raise ValueError(f"{name}: need {len(self.params)} tensors, got {len(tensors)}")
+        for i, (t, p) in enumerate(zip(tensors, self.params)):
+            _gpu(t, f"{name}[{i}]", self.device)
+            if t.numel() != p.numel():
+                raise ValueError(f"{name}[{i}]: need {p.numel()} elements, got {t.numel()}")
+
+    def _state(self, given, name):
+        torch = _torch()
+        if self.state_bits == 32:
+            if given is None:
+                return [torch.zeros(p.numel(), dtype=torch.float32, device=self.device) for p in self.params]
+            given = list(given)
+            self._match(given, name)
+            for i, t in enumerate(given):
+                _need(t, torch.float32, t.numel(), f"{name}[{i}]", self.device)
+            return given
+        if given is None:
+            zeros = lambda n: torch.zeros(n, dtype=torch.uint8, device=self.device)  # noqa: E731
+            return [(zeros(p.numel()), zeros(-(-p.numel() // STATE_BLOCK))) for p in self.params]
+        given = [tuple(x) for x in given]
+        if any(len(x) != 2 for x in given):
+            raise ValueError(f"{name}: need (codes, exponents) pairs with state_bits=8")
+        self._match([c for c, _ in given], name)
+        for i, (c, e) in enumerate(given):
+            _need(c, torch.uint8, c.numel(), f"{name}[{i}] codes", self.device)
+            _need(e, torch.uint8, -(-c.numel() // STATE_BLOCK), f"{name}[{i}] exponents", self.device)
+        return given
+
+    def set_grads(self, grads, stream=None):
+        """Take these gradients from the next call on."""
+        grads = list(grads)
+        self._match(grads, "grads")
+        gd = _one_dtype(grads, "grads")
+        count = len(self.params)
+        rows = (_AdamwTensor * count)()
+        for i, (r, p, g) in enumerate(zip(rows, self.params, grads)):
+            m, v = self.exp_avg[i], self.exp_avg_sq[i]
+            if self.state_bits == 8:
+                (m, me), (v, ve) = m, v
+                r.m_exp, r.v_exp = me.data_ptr(), ve.data_ptr()
+            r.p, r.g, r.m, r.v, r.n = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), p.numel()
+            if self.copies is not None:
+                r.copy = self.copies[i].data_ptr()
+            r.weight_decay = self.weight_decay[i]
+        st, ctx = _on(stream, self.device)
+        plan = _AdamwPlan()
+        with ctx:
+            _check(lib().zpq_adamw_plan_make(rows, count, self._pd, gd, self._cd, self.state_bits,
+                                             _ptr(self._table), self._table.numel(), ctypes.byref(plan), st),
+                   "zpq_adamw_plan_make")
+            self._plan, self.grads = plan, grads
+            self._list = TensorList(grads, stream=stream)
+
+    def grad_sumsq(self, out=None, accumulate=False, stream=None):
+        """Sum of squares of the gradients -> float64 [1] (see grad_sumsq)."""
+        return grad_sumsq(self._list, out=out, accumulate=accumulate, stream=stream)
+
+    def step(self, step, lr=None, grad_scale=1.0, sumsq=None, max_norm=None, stream=None):
+        """Step number `step` (from 1).  sumsq: float64 [1] on the GPU, the
+        squared norm of the unscaled gradients over all ranks; where it is not
+        finite nothing changes.  max_norm: clip the scaled gradients to it
+        (needs sumsq)."""
+        if sumsq is not None:
+            _need(sumsq, _torch().float64, 1, "sumsq", self.device)
+        elif max_norm is not None:
+            raise ValueError("max_norm needs sumsq")
+        h = _AdamwHyper(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, grad_scale,
+                        float("inf") if max_norm is None else max_norm, step, self.seed)
+        st, ctx = _on(stream, self.device)
+        with ctx:
+            _check(lib().zpq_adamw_step(ctypes.byref(self._plan), ctypes.byref(h), _ptr(sumsq), st),
+                   "zpq_adamw_step")
+
+
+def state8_unpack(codes, exps, moment, dtype=None, out=None, stream=None):
+    """Values of an 8-bit state of one tensor: moment 1 (exp_avg) or 2 (exp_avg_sq)."""
+    torch = _torch()
+    dev = _gpu(codes, "codes")
+    n = codes.numel()
+    _need(codes, torch.uint8, n, "codes", dev)
+    _need(exps, torch.uint8, -(-n // STATE_BLOCK), "exps", dev)
+    st, ctx = _on(stream, dev)
+    with ctx:
+        if out is None:
+            out = torch.empty(n, dtype=dtype or torch.float32, device=dev)
+        _need(out, out.dtype, n, "out", dev)
+        _check(lib().zpq_state8_unpack(_ptr(codes), _ptr(exps), n, moment, _ptr(out),
+                                       dtype_code(out.dtype), st), "zpq_state8_unpack")
+    return out
+
+
+def state8_pack(x, moment, out=None, stream=None):
+    """A float state as 8 bits, rounded to nearest -> (codes, exponents)."""
+    torch = _torch()
+    dev = _gpu(x, "x")
+    n = x.numel()
+    st, ctx = _on(stream, dev)
+    with ctx:
+        if out is None:
+            out = (torch.empty(n, dtype=torch.uint8, device=dev),
+                   torch.empty(-(-n // STATE_BLOCK), dtype=torch.uint8, device=dev))
+        codes, exps = out
+        _need(codes, torch.uint8, n, "codes", dev)
+        _need(exps, torch.uint8, -(-n // STATE_BLOCK), "exps", dev)
+        _check(lib().zpq_state8_pack(_ptr(x), dtype_code(x.dtype), n, moment, _ptr(codes), _ptr(exps),
+                                     st), "zpq_state8_pack")
+    return codes, exps
+
+
+def _ids(ids):
+    torch = _torch()
+    dev = _gpu(ids, "ids")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids: need int32 or int64, got {ids.dtype}")
+    return dev, ids.element_size()
+
+
+def _rows(t, name, device, rows=None, dim=None):
+    """t as rows: a 2-D tensor on `device` whose rows are contiguous (they may
+    lie further apart); returns the distance."""
+    if not t.is_cuda or t.device != device or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: need a 2-D tensor on {device} with contiguous rows, got "
+                         f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+    if (rows is not None and t.shape[0] != rows) or (dim is not None and t.shape[1] != dim):
+        raise ValueError(f"{name}: need {rows} x {dim}, got {tuple(t.shape)}")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap (strides {tuple(t.stride())})")
+    return ld
+
+
+def _lookup_out(ids, dim, out, dtype, dev):
+    """(out as given to the caller, out as rows)."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty(*ids.shape, dim, dtype=dtype, device=dev)
+        return out, out.view(-1, dim) if out.numel() else out.reshape(ids.numel(), dim)
+    return out, out if out.dim() == 2 else out.view(-1, out.shape[-1])
+
+
+def embedding(ids, table, scale=1.0, first=0, out_dtype=None, out=None, stream=None):
+    """scale * table[ids - first] -> [*ids.shape, dim]; zeros where ids - first is
+    not a row (padding, another shard's rows).  table [rows, dim]: float32,
+    float16 or bfloat16, rows may lie apart."""
+    dev, ib = _ids(ids)
+    ld = _rows(table, "table", dev)
+    rows, dim = table.shape
+    st, ctx = _on(stream, dev)
+    with ctx:
+        out, flat = _lookup_out(ids, dim, out, out_dtype or table.dtype, dev)
+        lo = _rows(flat, "out", dev, ids.numel(), dim)
+        _check(lib().zpq_embedding(_ptr(table), dtype_code(table.dtype), rows, dim, ld, _ptr(ids), ib,
+                                   ids.numel(), first, ctypes.c_float(scale), _ptr(flat),
+                                   dtype_code(flat.dtype), lo, st), "zpq_embedding")
+    return out
+
+
+def embedding_i8(ids, codes, scales, rows, dim, block=256, scale=1.0, first=0, out_dtype=None, out=None,
+                 stream=None):
+    """The same from a table as qwZ gathers it: int8 codes and one float32 scale
+    per block of them (at least rows * dim; padding after it is not read)."""
+    torch = _torch()
+    dev, ib = _ids(ids)
+    _gpu(codes, "codes", dev)
+    _gpu(scales, "scales", dev)
+    if codes.dtype != torch.int8 or codes.numel() < rows * dim:
+        raise ValueError(f"codes: need {rows * dim} elements of int8, got {codes.numel()} of {codes.dtype}")
+    if scales.dtype != torch.float32 or (block > 0 and scales.numel() < -(-rows * dim // block)):
+        raise ValueError(f"scales: need {-(-rows * dim // max(block, 1))} elements of float32, got "
+                         f"{scales.numel()} of {scales.dtype}")
+    st, ctx = _on(stream, dev)
+    with ctx:
+        out, flat = _lookup_out(ids, dim, out, out_dtype or torch.float16, dev)
+        lo = _rows(flat, "out", dev, ids.numel(), dim)
+        _check(lib().zpq_embedding_i8(_ptr(codes), _ptr(scales), rows, dim, block, _ptr(ids), ib,
+                                      ids.numel(), first, ctypes.c_float(scale), _ptr(flat),
+                                      dtype_code(flat.dtype), lo, st), "zpq_embedding_i8")
+    return out
+
+
+def embedding_grad(ids, dy, rows, scale=1.0, first=0, padding=None, out_dtype=None, out=None,
+                   accumulate=False, stream=None):
+    """Dense gradient of the lookup: row r gets scale * the sum of dy over the
+    tokens with ids - first == r (added to out with accumulate) -> [rows, dim].
+    Ids outside and `padding` count for nothing.  The same ids give the same
+    order of additions."""
+    torch = _torch()
+    dev, ib = _ids(ids)
+    if dy.dim() != 2:
+        _gpu(dy, "dy", dev)
+        dy = dy.view(-1, dy.shape[-1])
+    flat = dy
+    n, dim = ids.numel(), flat.shape[1]
+    ld = _rows(flat, "dy", dev, n, dim)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    need = ctypes.c_int64()
+    _check(lib().zpq_embedding_grad_bytes(n, dim, ctypes.byref(need)), "zpq_embedding_grad_bytes")
+    st, ctx = _on(stream, dev)
+    with ctx:
+        if out is None:
+            out = torch.empty(rows, dim, dtype=out_dtype or dy.dtype, device=dev)
+        lo = _rows(out, "out", dev, rows, dim)
+        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        _check(lib().zpq_embedding_grad(_ptr(flat), dtype_code(flat.dtype), ld, _ptr(ids), ib, n, first,
+                                        first - 1 if padding is None else padding, rows, dim,
+                                        ctypes.c_float(scale), _ptr(out), dtype_code(out.dtype), lo,
+                                        int(accumulate), _ptr(ws), need.value, st), "zpq_embedding_grad")
+    return out

@@ -21,6 +21,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "zpq.hip")
+SOURCES = [SRC] + [os.path.join(HERE, "csrc", f) for f in ("adamw.hip", "embedding.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libzpq.so")
 ARCH = "gfx950"
@@ -33,20 +34,38 @@ HIPCC_FLAGS = [
 ]
 
 
-def build(verbose: bool = False, save_temps: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = ["hipcc", *HIPCC_FLAGS, f"-I{INCLUDE}", SRC, "-o", tmp]
-    if save_temps:
-        cmd.insert(1, "--save-temps")
+def _run(cmd, verbose, cwd=None):
+    """Run one compiler command; its messages without the host pass's note on
+    the packed-FP32 feature."""
     if verbose:
         print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True,
-                         cwd=os.path.join(HERE, "csrc") if save_temps else None)
+    res = subprocess.run(cmd, capture_output=True, text=True, cwd=cwd)
     noise = "is not a recognized feature for this target"
     err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
-    if err.strip() and verbose:
+    return err
+
+
+def build(verbose: bool = False, save_temps: bool = False) -> str:
+    """Compile every source (side by side) and link libzpq.so."""
+    import concurrent.futures
+    objs = [src[:-len(".hip")] + ".o" for src in SOURCES]
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"] + (["--save-temps"] if save_temps else [])
+
+    def one(src, obj):
+        return _run(["hipcc", *flags, f"-I{INCLUDE}", "-c", src, "-o", obj], verbose,
+                    cwd=os.path.join(HERE, "csrc") if save_temps else None)
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        errs = list(ex.map(one, SOURCES, objs))
+    tmp = LIB + ".tmp"
+    errs.append(_run(["hipcc", f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp],
+                     verbose))
+    for o in objs:
+        os.remove(o)
+    err = "\n".join(e for e in errs if e.strip())
+    if err and verbose:
         print(err, file=sys.stderr)
     os.replace(tmp, LIB)
     return LIB

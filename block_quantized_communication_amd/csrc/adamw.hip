@@ -1,0 +1,693 @@
+// adamw.hip -- the optimizer step over many tensors, the gradient norm it
+// clips by, and the 8-bit states' conversions.
+//
+// One launch covers all tensors: a table in device memory (written by
+// k_fill_* from kernel arguments, so that it is ordered with the stream, can be
+// captured and needs no host memory to outlive the call) lists the tensors
+// and where each one's share of workgroups starts; a workgroup finds its
+// tensor by one or two 64-lane looks (find_start).
+#include <math.h>
+
+#include "step.h"
+
+namespace {
+
+using namespace zpq_step;
+
+constexpr int kTile = kThreads * 8;           // elements of one pass of a workgroup, 8 a lane
+constexpr int kStateBlock = 256;              // elements of an 8-bit state block: 32 lanes
+static_assert(kTile % kStateBlock == 0, "a tile holds whole state blocks");
+
+// ---------------------------------------------------------------------------
+// Tables.
+struct ListEntry { const void* ptr; int64_t n; };
+struct PlanEntry {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    uint8_t* me;
+    uint8_t* ve;
+    void* copy;
+    int64_t n;
+    int64_t base;                             // first random number
+    double decay;
+};
+static_assert(sizeof(ListEntry) + 4 <= 32 && sizeof(PlanEntry) + 4 <= 128, "ZPQ_*_BYTES");
+
+template <class E, int N>
+struct Fill {
+    E entry[N];
+    uint32_t start[N];
+};
+
+// Kernel arguments stay under 4 KB.
+constexpr int kFillList = 128, kFillPlan = 40;
+static_assert(sizeof(Fill<ListEntry, kFillList>) < 3800 && sizeof(Fill<PlanEntry, kFillPlan>) < 3800,
+              "kernel arguments");
+
+template <class E, int N>
+__global__ __launch_bounds__(128) void k_fill(Fill<E, N> f, int32_t first, int32_t count, int32_t all,
+                                              E* __restrict__ entries, uint32_t* __restrict__ starts,
+                                              uint32_t total) {
+    const int i = threadIdx.x;
+    if (i < count) {
+        entries[first + i] = f.entry[i];
+        starts[first + i] = f.start[i];
+    }
+    if (i == 0 && first + count == all) starts[all] = total;
+}
+
+template <class E>
+uint32_t* starts_of(void* table, int32_t count) {
+    return reinterpret_cast<uint32_t*>(static_cast<E*>(table) + count);
+}
+
+// ---------------------------------------------------------------------------
+// Sum of squares.  Every square of a binary32 value is exact in binary64, and
+// v_fma_f64 issues like v_fma_f32 here, so binary64 sums cost one conversion a
+// value and no range checks.  Workgroup b of G takes the chunks
+// [K*b/G, K*(b+1)/G): consecutive, so that the tensor is looked up once and
+// then followed.
+constexpr int kSumChunk = 4 * kTile;
+constexpr int kSumParts = 4096;               // ZPQ_SUMSQ_BYTES / 8
+static_assert(kSumParts * 8 == ZPQ_SUMSQ_BYTES, "workspace");
+
+__device__ __forceinline__ double wg_sum(double x) {
+    __shared__ double part[kThreads / 64];
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+    __syncthreads();
+    double s = part[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 64; ++i) s += part[i];
+    return s;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict__ entries,
+                                                    const uint32_t* __restrict__ starts,
+                                                    int32_t count, uint32_t chunks,
+                                                    double* __restrict__ part) {
+    const uint32_t k0 = (uint32_t)((uint64_t)chunks * blockIdx.x / gridDim.x);
+    const uint32_t k1 = (uint32_t)((uint64_t)chunks * (blockIdx.x + 1) / gridDim.x);
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    uint32_t t = find_start(starts, count, k0);
+    for (uint32_t k = k0; k < k1; ++k) {
+        while (k >= starts[t + 1]) ++t;       // starts[count] = chunks > k: ends
+        const ListEntry e = entries[t];
+        const int64_t at = (int64_t)(k - starts[t]) * kSumChunk;
+        if (at + kSumChunk <= e.n) {
+            Raw8<DT> r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) r[u].load(e.ptr, at + u * kTile + threadIdx.x * 8);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const double x = (double)r[u].get(i);
+                    s[i & 3] = __builtin_fma(x, x, s[i & 3]);
+                }
+        } else {
+            const int64_t end = at + kSumChunk < e.n ? at + kSumChunk : e.n;
+            for (int64_t i = at + threadIdx.x; i < end; i += kThreads) {
+                const double x = (double)load1<DT>(e.ptr, i);
+                s[0] = __builtin_fma(x, x, s[0]);
+            }
+        }
+    }
+    const double sum = wg_sum((s[0] + s[1]) + (s[2] + s[3]));
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+__global__ __launch_bounds__(kThreads) void k_sumsq_join(const double* __restrict__ part,
+                                                         int32_t parts, int32_t accumulate,
+                                                         double* __restrict__ out) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+    s = wg_sum(s);
+    if (threadIdx.x == 0) out[0] = accumulate ? out[0] + s : s;
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit states.  A state value is a binary32 pattern whose exponent field has
+// been moved so that the block's top binade e lands on T (15 for m, 31 for
+// v): then the pattern's bits from 20 up are the code, binary32's own
+// subnormals are the code's subnormals, and rounding is an integer addition
+// below bit 20.  ldexp moves the field, for any e, with one rounding where
+// the result is subnormal.
+
+// Cross-lane maximum of unsigned values over aligned groups of 32 lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t max32(uint32_t v) {
+    v = max(v, dpp<0xB1>(v));                 // quad_perm [1,0,3,2]
+    v = max(v, dpp<0x4E>(v));                 // quad_perm [2,3,0,1]
+    v = max(v, dpp<0x141>(v));                // row_half_mirror
+    v = max(v, dpp<0x140>(v));                // row_mirror
+    return max(v, (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401F));   // lane ^ 16
+}
+
+// Exponent byte of a block from the bits of its largest magnitude: up to
+// 1.875 of a binade stays in it (a carry out of 3 fraction bits would not fit).
+__device__ __forceinline__ uint32_t block_exp(uint32_t amax) {
+    const uint32_t e = (amax + 0xFFFFFu) >> 23;
+    return e < 1 ? 1 : e > 255 ? 255 : e;
+}
+
+template <int MOMENT>
+__device__ __forceinline__ float decode8(uint32_t c, uint32_t e) {
+    if constexpr (MOMENT == 1)
+        return __builtin_amdgcn_ldexpf(__uint_as_float((c & 0x7Fu) << 20 | (c & 0x80u) << 24),
+                                       (int)e - 15);
+    else
+        return __builtin_amdgcn_ldexpf(__uint_as_float(c << 20), (int)e - 31);
+}
+
+// `add` is what goes in below bit 20: a random number for states, half a step
+// (less one, plus the parity) for rounding to nearest even.
+template <int MOMENT>
+__device__ __forceinline__ uint32_t encode8(float x, uint32_t e, uint32_t add, bool nearest) {
+    const uint32_t b = __float_as_uint(__builtin_amdgcn_ldexpf(x, (MOMENT == 1 ? 15 : 31) - (int)e));
+    const uint32_t mag = b & 0x7FFFFFFFu;
+    if (nearest) add = 0x7FFFFu + ((mag >> 20) & 1u);
+    uint32_t c = (mag + add) >> 20;
+    if constexpr (MOMENT == 1) {
+        if (e == 255) return 0x7F;
+        return c | (b >> 31) << 7;
+    } else {
+        if (e == 255) return 0xFF;
+        return c == 0 && !nearest && x > 0.0f ? 1u : c;
+    }
+}
+
+// The random bits of element lo + 2^32 * hi for a key made of seed and step: a
+// multiplicative counter and two rounds of xor-shift and multiply.  Low half
+// for m, high half for v.
+constexpr uint32_t kMulLo = 0x9E3779B1u, kMulHi = 0x85A308D3u;
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x = (x ^ (x >> 16)) * 0xB7E15163u;
+    x = (x ^ (x >> 15)) * 0x243F6A89u;
+    return x ^ (x >> 16);
+}
+inline uint32_t random_key(uint64_t seed, uint64_t step) {
+    uint64_t z = seed + step * 0x9E3779B97F4A7C15ull;
+    z = (z ^ (z >> 31)) * 0xB7E151628AED2A6Bull;
+    z = (z ^ (z >> 29)) * 0x243F6A8885A308D3ull;
+    return (uint32_t)(z >> 32);
+}
+
+// ---------------------------------------------------------------------------
+// The step.
+struct StepArgs {
+    double lr, grad_scale, max_norm;
+    float b1, ob1, b2, ob2, eps, rbc2, rate;  // ob: 1 - b; rbc2: 1/sqrt(1 - b2^t); rate: lr/(1 - b1^t)
+    uint32_t key;
+};
+
+// Workgroup k of the grid (and k + gridDim.x, ...) takes chunk k: chunk_elems
+// consecutive elements of one tensor, in tiles of 8 elements a lane.
+template <int PT, int GT, int CT, int BITS>
+__global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict__ entries,
+                                                    const uint32_t* __restrict__ starts,
+                                                    int32_t count, uint32_t chunks,
+                                                    int32_t chunk_elems, StepArgs a,
+                                                    const double* __restrict__ sumsq) {
+    float c = (float)a.grad_scale;
+    if (sumsq != nullptr) {
+        const double norm = __builtin_sqrt(*sumsq) * a.grad_scale;
+        if (!(norm < __builtin_huge_val())) return;          // also NaN
+        const double cut = a.max_norm / (norm + 1e-6);
+        c = (float)(a.grad_scale * (cut < 1.0 ? cut : 1.0));
+    }
+    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const uint32_t t = find_start(starts, count, k);
+        const PlanEntry e = entries[t];
+        const float keep = (float)(1.0 - a.lr * e.decay);
+        int64_t at = (int64_t)(k - starts[t]) * chunk_elems;
+        const int64_t end = at + chunk_elems < e.n ? at + chunk_elems : e.n;
+        for (; at < end; at += kTile) {
+            const int64_t i0 = at + threadIdx.x * 8;
+            const int have = (int)(e.n - i0 < 0 ? 0 : e.n - i0 < 8 ? e.n - i0 : 8);
+            const bool whole = have == 8;
+            float p[8], g[8], m[8], v[8];
+            // ---- in
+            if (whole) {
+                Raw8<PT> rp;
+                Raw8<GT> rg;
+                rp.load(e.p, i0);
+                rg.load(e.g, i0);
+                if constexpr (BITS == 32) {
+                    Raw8<ZPQ_F32> rm, rv;
+                    rm.load(e.m, i0);
+                    rv.load(e.v, i0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) { m[i] = rm.get(i); v[i] = rv.get(i); }
+                } else {
+                    Raw8<kI8> rm, rv;
+                    rm.load(e.m, i0);
+                    rv.load(e.v, i0);
+                    const uint32_t em = e.me[i0 / kStateBlock], ev = e.ve[i0 / kStateBlock];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        m[i] = decode8<1>((rm.w[i >> 2] >> (8 * (i & 3))) & 0xFFu, em);
+                        v[i] = decode8<2>((rv.w[i >> 2] >> (8 * (i & 3))) & 0xFFu, ev);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) { p[i] = rp.get(i); g[i] = rg.get(i); }
+            } else {
+                uint32_t em = 1, ev = 1;
+                if constexpr (BITS == 8) {
+                    if (have > 0) { em = e.me[i0 / kStateBlock]; ev = e.ve[i0 / kStateBlock]; }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = g[i] = m[i] = v[i] = 0.0f;
+                    if (i < have) {
+                        p[i] = load1<PT>(e.p, i0 + i);
+                        g[i] = load1<GT>(e.g, i0 + i);
+                        if constexpr (BITS == 32) {
+                            m[i] = load1<ZPQ_F32>(e.m, i0 + i);
+                            v[i] = load1<ZPQ_F32>(e.v, i0 + i);
+                        } else {
+                            m[i] = decode8<1>(static_cast<const uint8_t*>(e.m)[i0 + i], em);
+                            v[i] = decode8<2>(static_cast<const uint8_t*>(e.v)[i0 + i], ev);
+                        }
+                    }
+                }
+            }
+            // ---- the step
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = g[i] * c;
+                m[i] = m[i] * a.b1 + x * a.ob1;
+                v[i] = v[i] * a.b2 + (x * a.ob2) * x;
+                const float u = m[i] / (__builtin_sqrtf(v[i]) * a.rbc2 + a.eps);
+                p[i] = p[i] * keep - u * a.rate;
+            }
+            // ---- out
+            uint32_t cm[8], cv[8], em = 1, ev = 1;
+            if constexpr (BITS == 8) {
+                // lanes past the end hold zeros: m and v of zeros stay zeros
+                uint32_t am = 0, av = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    am = max(am, __float_as_uint(m[i]) & 0x7FFFFFFFu);
+                    av = max(av, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+                }
+                em = block_exp(max32(am));
+                ev = block_exp(max32(av));
+                const uint64_t at0 = (uint64_t)(e.base + i0);
+                const uint32_t x0 = (uint32_t)at0 * kMulLo + (uint32_t)(at0 >> 32) * kMulHi + a.key;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {   // base and i0 are multiples of 8: no carry within 8
+                    const uint32_t r = mix(x0 + (uint32_t)i * kMulLo);
+                    cm[i] = encode8<1>(m[i], em, ((r & 0xFFFFu) << 4) + 8, false);
+                    cv[i] = encode8<2>(v[i], ev, ((r >> 16) << 4) + 8, false);
+                }
+            }
+            if (whole) {
+                Raw8<PT> rp;
+                rp.set(p);
+                rp.store(e.p, i0);
+                if constexpr (CT >= 0) {
+                    Raw8<CT> rc;
+                    rc.set(p);
+                    rc.store(e.copy, i0);
+                }
+                if constexpr (BITS == 32) {
+                    Raw8<ZPQ_F32> r;
+                    r.set(m);
+                    r.store(e.m, i0);
+                    r.set(v);
+                    r.store(e.v, i0);
+                } else {
+                    Raw8<kI8> r;
+                    r.w[0] = cm[0] | cm[1] << 8 | cm[2] << 16 | cm[3] << 24;
+                    r.w[1] = cm[4] | cm[5] << 8 | cm[6] << 16 | cm[7] << 24;
+                    r.store(e.m, i0);
+                    r.w[0] = cv[0] | cv[1] << 8 | cv[2] << 16 | cv[3] << 24;
+                    r.w[1] = cv[4] | cv[5] << 8 | cv[6] << 16 | cv[7] << 24;
+                    r.store(e.v, i0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < have) {
+                        store1<PT>(e.p, i0 + i, p[i]);
+                        if constexpr (CT >= 0) store1<CT>(e.copy, i0 + i, p[i]);
+                        if constexpr (BITS == 32) {
+                            store1<ZPQ_F32>(e.m, i0 + i, m[i]);
+                            store1<ZPQ_F32>(e.v, i0 + i, v[i]);
+                        } else {
+                            static_cast<uint8_t*>(e.m)[i0 + i] = (uint8_t)cm[i];
+                            static_cast<uint8_t*>(e.v)[i0 + i] = (uint8_t)cv[i];
+                        }
+                    }
+            }
+            if constexpr (BITS == 8) {
+                if ((threadIdx.x & 31) == 0 && have > 0) {
+                    e.me[i0 / kStateBlock] = (uint8_t)em;
+                    e.ve[i0 / kStateBlock] = (uint8_t)ev;
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit states to floats and back, 8 elements a lane.
+template <int DT, int MOMENT>
+__global__ __launch_bounds__(kThreads) void k_unpack8(const uint8_t* __restrict__ codes,
+                                                      const uint8_t* __restrict__ exps, int64_t n,
+                                                      void* __restrict__ y) {
+    for (int64_t at = (int64_t)blockIdx.x * kTile; at < n; at += (int64_t)gridDim.x * kTile) {
+        const int64_t i0 = at + threadIdx.x * 8;
+        if (i0 >= n) continue;
+        const uint32_t e = exps[i0 / kStateBlock];
+        if (i0 + 8 <= n) {
+            Raw8<kI8> r;
+            r.load(codes, i0);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = decode8<MOMENT>((r.w[i >> 2] >> (8 * (i & 3))) & 0xFFu, e);
+            Raw8<DT> o;
+            o.set(x);
+            o.store(y, i0);
+        } else {
+            for (int i = 0; i < 8 && i0 + i < n; ++i)
+                store1<DT>(y, i0 + i, decode8<MOMENT>(codes[i0 + i], e));
+        }
+    }
+}
+
+template <int DT, int MOMENT>
+__global__ __launch_bounds__(kThreads) void k_pack8(const void* __restrict__ x, int64_t n,
+                                                    uint8_t* __restrict__ codes,
+                                                    uint8_t* __restrict__ exps) {
+    for (int64_t at = (int64_t)blockIdx.x * kTile; at < n; at += (int64_t)gridDim.x * kTile) {
+        const int64_t i0 = at + threadIdx.x * 8;
+        const int have = (int)(n - i0 < 0 ? 0 : n - i0 < 8 ? n - i0 : 8);
+        float v[8];
+        uint32_t a = 0;
+        if (have == 8) {
+            Raw8<DT> r;
+            r.load(x, i0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = r.get(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < have ? load1<DT>(x, i0 + i) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        const uint32_t e = block_exp(max32(a));
+        if (have == 8) {
+            Raw8<kI8> r = {};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.w[i >> 2] |= encode8<MOMENT>(v[i], e, 0, true) << (8 * (i & 3));
+            r.store(codes, i0);
+        } else {
+            for (int i = 0; i < have; ++i) codes[i0 + i] = (uint8_t)encode8<MOMENT>(v[i], e, 0, true);
+        }
+        if ((threadIdx.x & 31) == 0 && have > 0) exps[i0 / kStateBlock] = (uint8_t)e;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+inline unsigned cu_count() {
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+        return 256;
+    return (unsigned)n;
+}
+
+inline unsigned grid_of(int64_t work) { return (unsigned)(work < (1 << 22) ? work : 1 << 22); }
+
+bool list_ok(const zpq_list* l) {
+    return l && l->count >= 0 && l->chunks >= 0 && l->chunks <= 0x7FFFFFFF && l->elems >= 0 &&
+           dtype_bytes(l->dtype) != 0 && (l->chunks == 0 || l->table);
+}
+
+template <int PT, int GT, int CT, int BITS>
+void launch_adamw(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
+    hipLaunchKernelGGL((k_adamw<PT, GT, CT, BITS>), dim3(grid_of(q->chunks)), dim3(kThreads), 0, st,
+                       static_cast<const PlanEntry*>(q->table), starts_of<PlanEntry>(q->table, q->count),
+                       q->count, (uint32_t)q->chunks, q->chunk_elems, a, sumsq);
+}
+template <int PT, int GT, int BITS>
+void launch_adamw_c(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
+    if constexpr (PT == ZPQ_F32) {
+        if (q->copy_dtype == ZPQ_F16) return launch_adamw<PT, GT, ZPQ_F16, BITS>(q, a, sumsq, st);
+        if (q->copy_dtype == ZPQ_BF16) return launch_adamw<PT, GT, ZPQ_BF16, BITS>(q, a, sumsq, st);
+    }
+    launch_adamw<PT, GT, -1, BITS>(q, a, sumsq, st);
+}
+template <int PT, int BITS>
+void launch_adamw_g(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
+    if (q->g_dtype == ZPQ_F32) launch_adamw_c<PT, ZPQ_F32, BITS>(q, a, sumsq, st);
+    else if (q->g_dtype == ZPQ_F16) launch_adamw_c<PT, ZPQ_F16, BITS>(q, a, sumsq, st);
+    else launch_adamw_c<PT, ZPQ_BF16, BITS>(q, a, sumsq, st);
+}
+template <int BITS>
+void launch_adamw_p(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
+    if (q->p_dtype == ZPQ_F32) launch_adamw_g<ZPQ_F32, BITS>(q, a, sumsq, st);
+    else if (q->p_dtype == ZPQ_F16) launch_adamw_g<ZPQ_F16, BITS>(q, a, sumsq, st);
+    else launch_adamw_g<ZPQ_BF16, BITS>(q, a, sumsq, st);
+}
+
+bool finite_at_least(double x, double least) { return x >= least && x <= 1.7976931348623157e308; }
+
+template <int DT>
+void launch_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t moment,
+                   void* y, hipStream_t st) {
+    const dim3 grid(grid_of((n + kTile - 1) / kTile));
+    if (moment == 1)
+        hipLaunchKernelGGL((k_unpack8<DT, 1>), grid, dim3(kThreads), 0, st, codes, exps, n, y);
+    else
+        hipLaunchKernelGGL((k_unpack8<DT, 2>), grid, dim3(kThreads), 0, st, codes, exps, n, y);
+}
+template <int DT>
+void launch_pack(const void* x, int64_t n, int32_t moment, uint8_t* codes, uint8_t* exps,
+                 hipStream_t st) {
+    const dim3 grid(grid_of((n + kTile - 1) / kTile));
+    if (moment == 1)
+        hipLaunchKernelGGL((k_pack8<DT, 1>), grid, dim3(kThreads), 0, st, x, n, codes, exps);
+    else
+        hipLaunchKernelGGL((k_pack8<DT, 2>), grid, dim3(kThreads), 0, st, x, n, codes, exps);
+}
+
+zpq_status state8_check(const void* codes, const void* exps, const void* y, int64_t n, int32_t moment,
+                        int32_t dtype) {
+    if (moment != 1 && moment != 2) return ZPQ_ERR_ARG;
+    if (n < 0 || n > kMaxElems) return ZPQ_ERR_SIZE;
+    const int64_t eb = dtype_bytes(dtype);
+    if (eb == 0) return ZPQ_ERR_DTYPE;
+    if (n == 0) return ZPQ_OK;
+    if (!codes || !exps || !y) return ZPQ_ERR_NULL;
+    if (!aligned(y, eb)) return ZPQ_ERR_ALIGN;
+    const uint64_t blocks = (uint64_t)(n + kStateBlock - 1) / kStateBlock;
+    if (overlaps(codes, n, y, n * eb) || overlaps(exps, blocks, y, n * eb) ||
+        overlaps(codes, n, exps, blocks))
+        return ZPQ_ERR_ALIAS;
+    return ZPQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+zpq_status zpq_list_make(const void* const* ptrs, const int64_t* sizes, int32_t count,
+                         int32_t dtype, void* table, int64_t table_bytes, zpq_list* list,
+                         zpq_stream stream) {
+    if (count < 0) return ZPQ_ERR_ARG;
+    const int64_t eb = dtype_bytes(dtype);
+    if (eb == 0) return ZPQ_ERR_DTYPE;
+    if (!list || (count > 0 && (!ptrs || !sizes || !table))) return ZPQ_ERR_NULL;
+    if (table_bytes < ZPQ_LIST_BYTES(count)) return ZPQ_ERR_SIZE;
+    if (count > 0 && !aligned(table, 16)) return ZPQ_ERR_ALIGN;
+    int64_t elems = 0, chunks = 0;
+    for (int32_t i = 0; i < count; ++i)
+        if (sizes[i] < 0 || sizes[i] > kMaxElems || (elems += sizes[i]) > kMaxElems) return ZPQ_ERR_SIZE;
+    for (int32_t i = 0; i < count; ++i) {
+        if (sizes[i] > 0 && !ptrs[i]) return ZPQ_ERR_NULL;
+        if (sizes[i] > 0 && !aligned(ptrs[i], eb)) return ZPQ_ERR_ALIGN;
+        if (overlaps(ptrs[i], sizes[i] * eb, table, table_bytes)) return ZPQ_ERR_ALIAS;
+        chunks += (sizes[i] + kSumChunk - 1) / kSumChunk;
+    }
+    if (chunks > 0x7FFFFFFF) return ZPQ_ERR_SIZE;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    ListEntry* entries = static_cast<ListEntry*>(table);
+    int64_t start = 0;
+    for (int32_t first = 0; first < count; first += kFillList) {
+        Fill<ListEntry, kFillList> f = {};
+        const int32_t some = count - first < kFillList ? count - first : kFillList;
+        for (int32_t i = 0; i < some; ++i) {
+            f.entry[i] = ListEntry{ptrs[first + i], sizes[first + i]};
+            f.start[i] = (uint32_t)start;
+            start += (sizes[first + i] + kSumChunk - 1) / kSumChunk;
+        }
+        hipLaunchKernelGGL((k_fill<ListEntry, kFillList>), dim3(1), dim3(128), 0, st, f, first, some, count,
+                           entries, starts_of<ListEntry>(table, count), (uint32_t)chunks);
+    }
+    *list = zpq_list{table, elems, chunks, count, dtype};
+    return count > 0 ? after_launch() : ZPQ_OK;
+}
+
+zpq_status zpq_grad_sumsq(const zpq_list* list, double* out, int32_t accumulate, void* workspace,
+                          int64_t workspace_bytes, zpq_stream stream) {
+    if (!list_ok(list)) return list ? ZPQ_ERR_ARG : ZPQ_ERR_NULL;
+    if (!out || !workspace) return ZPQ_ERR_NULL;
+    if (workspace_bytes < ZPQ_SUMSQ_BYTES) return ZPQ_ERR_SIZE;
+    if (!aligned(out, 8) || !aligned(workspace, 16)) return ZPQ_ERR_ALIGN;
+    if (overlaps(out, 8, workspace, ZPQ_SUMSQ_BYTES) ||
+        overlaps(out, 8, list->table, ZPQ_LIST_BYTES(list->count)) ||
+        overlaps(workspace, ZPQ_SUMSQ_BYTES, list->table, ZPQ_LIST_BYTES(list->count)))
+        return ZPQ_ERR_ALIAS;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    double* part = static_cast<double*>(workspace);
+    int64_t parts = (int64_t)cu_count() * 8;
+    if (parts > kSumParts) parts = kSumParts;
+    if (parts > list->chunks) parts = list->chunks;
+    if (parts > 0) {
+        const ListEntry* e = static_cast<const ListEntry*>(list->table);
+        const uint32_t* s = starts_of<ListEntry>(list->table, list->count);
+        const dim3 grid((unsigned)parts);
+        if (list->dtype == ZPQ_F32)
+            hipLaunchKernelGGL(k_sumsq<ZPQ_F32>, grid, dim3(kThreads), 0, st, e, s, list->count,
+                               (uint32_t)list->chunks, part);
+        else if (list->dtype == ZPQ_F16)
+            hipLaunchKernelGGL(k_sumsq<ZPQ_F16>, grid, dim3(kThreads), 0, st, e, s, list->count,
+                               (uint32_t)list->chunks, part);
+        else
+            hipLaunchKernelGGL(k_sumsq<ZPQ_BF16>, grid, dim3(kThreads), 0, st, e, s, list->count,
+                               (uint32_t)list->chunks, part);
+    }
+    hipLaunchKernelGGL(k_sumsq_join, dim3(1), dim3(kThreads), 0, st, part, (int32_t)parts, accumulate, out);
+    return after_launch();
+}
+
+zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, int32_t p_dtype,
+                               int32_t g_dtype, int32_t copy_dtype, int32_t state_bits,
+                               void* table, int64_t table_bytes, zpq_adamw_plan* plan,
+                               zpq_stream stream) {
+    if (count < 0) return ZPQ_ERR_ARG;
+    const int64_t pb = dtype_bytes(p_dtype), gb = dtype_bytes(g_dtype);
+    if (pb == 0 || gb == 0) return ZPQ_ERR_DTYPE;
+    if (copy_dtype != -1 && copy_dtype != ZPQ_F16 && copy_dtype != ZPQ_BF16) return ZPQ_ERR_DTYPE;
+    if (copy_dtype != -1 && p_dtype != ZPQ_F32) return ZPQ_ERR_MODE;
+    if (state_bits != 32 && state_bits != 8) return ZPQ_ERR_ARG;
+    if (!plan || (count > 0 && (!tensors || !table))) return ZPQ_ERR_NULL;
+    if (table_bytes < ZPQ_PLAN_BYTES(count)) return ZPQ_ERR_SIZE;
+    if (count > 0 && !aligned(table, 16)) return ZPQ_ERR_ALIGN;
+    const int64_t sb = state_bits / 8;
+    int64_t elems = 0, tiles = 0;
+    for (int32_t i = 0; i < count; ++i)
+        if (tensors[i].n < 0 || tensors[i].n > kMaxElems || (elems += tensors[i].n) > kMaxElems)
+            return ZPQ_ERR_SIZE;
+    for (int32_t i = 0; i < count; ++i) {
+        const zpq_adamw_tensor& t = tensors[i];
+        if (!finite_at_least(t.weight_decay, 0.0)) return ZPQ_ERR_ARG;
+        if (t.n == 0) continue;
+        if ((copy_dtype == -1) != (t.copy == nullptr)) return ZPQ_ERR_MODE;
+        if (!t.p || !t.g || !t.m || !t.v || (state_bits == 8 && (!t.m_exp || !t.v_exp))) return ZPQ_ERR_NULL;
+        if (!aligned(t.p, pb) || !aligned(t.g, gb) || !aligned(t.m, sb) || !aligned(t.v, sb) ||
+            !aligned(t.copy, 2))
+            return ZPQ_ERR_ALIGN;
+        const uint64_t blocks = state_bits == 8 ? (uint64_t)(t.n + kStateBlock - 1) / kStateBlock : 0;
+        const void* at[8] = {t.p, t.g, t.m, t.v, t.copy, t.m_exp, t.v_exp, table};
+        const uint64_t size[8] = {(uint64_t)(t.n * pb), (uint64_t)(t.n * gb), (uint64_t)(t.n * sb),
+                                  (uint64_t)(t.n * sb), (uint64_t)t.n * 2, blocks, blocks,
+                                  (uint64_t)table_bytes};
+        for (int x = 0; x < 8; ++x)
+            for (int y = x + 1; y < 8; ++y)
+                if (overlaps(at[x], size[x], at[y], size[y])) return ZPQ_ERR_ALIAS;
+        tiles += (t.n + kTile - 1) / kTile;
+    }
+    const int64_t chunk = kTile;
+    int64_t chunks = tiles;
+    if (chunks > 0x7FFFFFFF) return ZPQ_ERR_SIZE;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    PlanEntry* entries = static_cast<PlanEntry*>(table);
+    int64_t start = 0, base = 0;
+    for (int32_t first = 0; first < count; first += kFillPlan) {
+        Fill<PlanEntry, kFillPlan> f = {};
+        const int32_t some = count - first < kFillPlan ? count - first : kFillPlan;
+        for (int32_t i = 0; i < some; ++i) {
+            const zpq_adamw_tensor& t = tensors[first + i];
+            f.entry[i] = PlanEntry{t.p, t.g, t.m, t.v, t.m_exp, t.v_exp, t.copy, t.n, base,
+                                   t.weight_decay};
+            f.start[i] = (uint32_t)start;
+            start += (t.n + chunk - 1) / chunk;
+            base += (t.n + kStateBlock - 1) / kStateBlock * kStateBlock;
+        }
+        hipLaunchKernelGGL((k_fill<PlanEntry, kFillPlan>), dim3(1), dim3(128), 0, st, f, first, some, count,
+                           entries, starts_of<PlanEntry>(table, count), (uint32_t)chunks);
+    }
+    *plan = zpq_adamw_plan{table, elems, chunks, count, p_dtype, g_dtype, copy_dtype, state_bits,
+                           (int32_t)chunk};
+    return count > 0 ? after_launch() : ZPQ_OK;
+}
+
+zpq_status zpq_adamw_step(const zpq_adamw_plan* plan, const zpq_adamw_hyper* h, const double* sumsq,
+                          zpq_stream stream) {
+    if (!plan || !h) return ZPQ_ERR_NULL;
+    if (dtype_bytes(plan->p_dtype) == 0 || dtype_bytes(plan->g_dtype) == 0 ||
+        (plan->state_bits != 32 && plan->state_bits != 8) || plan->count < 0 || plan->chunks < 0 ||
+        plan->chunks > 0x7FFFFFFF || (plan->chunks > 0 && (!plan->table || plan->chunk_elems % kTile != 0 ||
+                                                          plan->chunk_elems <= 0)))
+        return ZPQ_ERR_ARG;
+    if (!finite_at_least(h->lr, 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
+        !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !finite_at_least(h->eps, 1e-30) || h->step < 1 ||
+        !(h->grad_scale > 0.0 && h->grad_scale <= 3.4028234663852886e38) || !(h->max_norm > 0.0))
+        return ZPQ_ERR_ARG;
+    if (!sumsq && h->max_norm <= 1.7976931348623157e308) return ZPQ_ERR_ARG;
+    if (!aligned(sumsq, 8)) return ZPQ_ERR_ALIGN;
+    if (plan->chunks == 0) return ZPQ_OK;
+    StepArgs a;
+    a.lr = h->lr;
+    a.grad_scale = h->grad_scale;
+    a.max_norm = h->max_norm;
+    a.b1 = (float)h->beta1;
+    a.ob1 = (float)(1.0 - h->beta1);
+    a.b2 = (float)h->beta2;
+    a.ob2 = (float)(1.0 - h->beta2);
+    a.eps = (float)h->eps;
+    a.rbc2 = (float)(1.0 / sqrt(1.0 - pow(h->beta2, (double)h->step)));
+    a.rate = (float)(h->lr / (1.0 - pow(h->beta1, (double)h->step)));
+    a.key = random_key(h->seed, (uint64_t)h->step);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (plan->state_bits == 32) launch_adamw_p<32>(plan, a, sumsq, st);
+    else launch_adamw_p<8>(plan, a, sumsq, st);
+    return after_launch();
+}
+
+zpq_status zpq_state8_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t moment,
+                             void* y, int32_t y_dtype, zpq_stream stream) {
+    const zpq_status bad = state8_check(codes, exps, y, n, moment, y_dtype);
+    if (bad != ZPQ_OK || n == 0) return bad;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (y_dtype == ZPQ_F32) launch_unpack<ZPQ_F32>(codes, exps, n, moment, y, st);
+    else if (y_dtype == ZPQ_F16) launch_unpack<ZPQ_F16>(codes, exps, n, moment, y, st);
+    else launch_unpack<ZPQ_BF16>(codes, exps, n, moment, y, st);
+    return after_launch();
+}
+
+zpq_status zpq_state8_pack(const void* x, int32_t x_dtype, int64_t n, int32_t moment,
+                           uint8_t* codes, uint8_t* exps, zpq_stream stream) {
+    const zpq_status bad = state8_check(codes, exps, x, n, moment, x_dtype);
+    if (bad != ZPQ_OK || n == 0) return bad;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (x_dtype == ZPQ_F32) launch_pack<ZPQ_F32>(x, n, moment, codes, exps, st);
+    else if (x_dtype == ZPQ_F16) launch_pack<ZPQ_F16>(x, n, moment, codes, exps, st);
+    else launch_pack<ZPQ_BF16>(x, n, moment, codes, exps, st);
+    return after_launch();
+}
+
+}  // extern "C"

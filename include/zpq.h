@@ -157,6 +157,178 @@ zpq_status zpq_qgz_dequant_reduce_requant_i4(const uint8_t* in_codes, const floa
                                              void* out_vals, int32_t out_dtype, float divisor,
                                              zpq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * The ends of the step around qwZ and qgZ: the averaged gradient slice of hop
+ * 2 goes into zpq_adamw_step, whose 16-bit copy of the weights is what qwZ
+ * quantizes for the next all-gather; the gathered INT8 table is read by
+ * zpq_embedding_i8 as it is; zpq_embedding_grad makes the table's gradient,
+ * which qgZ sends.  (The pages name the optimizer step only as what follows
+ * the gradient average; these operators are defined here.)
+ *
+ * They follow the conventions above, except that sizes need not be whole
+ * blocks and that pointers need the alignment of their element only: 16-byte
+ * alignment is faster, not required.
+ */
+
+/* Bytes of device memory that a table of `count` tensors takes, for
+ * zpq_list_make and for zpq_adamw_plan_make (16-byte aligned). */
+#define ZPQ_LIST_BYTES(count) ((int64_t)(count) * 32 + 64)
+#define ZPQ_PLAN_BYTES(count) ((int64_t)(count) * 128 + 64)
+
+/* A list of tensors of one type: a table in the caller's device memory, and
+ * what the host has to know of it.  Filled by zpq_list_make; the table's
+ * contents (addresses among them) stand until it is made again. */
+typedef struct {
+    void* table;
+    int64_t elems;     /* of all tensors */
+    int64_t chunks;    /* workgroup shares */
+    int32_t count;
+    int32_t dtype;
+} zpq_list;
+
+/*
+ * Describe `count` tensors: ptrs[i] holds sizes[i] elements of type `dtype`
+ * (NULL only where sizes[i] is 0).  The table is written by small kernels on
+ * `stream`, so later work on that stream sees it; ptrs and sizes are host
+ * arrays and may go when the call returns.
+ */
+zpq_status zpq_list_make(const void* const* ptrs, const int64_t* sizes, int32_t count,
+                         int32_t dtype, void* table, int64_t table_bytes, zpq_list* list,
+                         zpq_stream stream);
+
+/*
+ * Sum of squares over a list (the squared norm that clipping needs; ranks add
+ * theirs): out[0] = sum of g^2, or out[0] += with accumulate, in binary64
+ * throughout, in an order that depends on the sizes and the number of compute
+ * units only.  workspace: ZPQ_SUMSQ_BYTES bytes of device memory, 16-byte
+ * aligned, contents irrelevant.
+ */
+#define ZPQ_SUMSQ_BYTES 32768
+zpq_status zpq_grad_sumsq(const zpq_list* list, double* out, int32_t accumulate, void* workspace,
+                          int64_t workspace_bytes, zpq_stream stream);
+
+/* One tensor of an optimizer step; all device pointers.  The tensors of one
+ * plan must not overlap one another, nor a tensor's own parts. */
+typedef struct {
+    void* p;             /* [n] weights                                    (updated) */
+    const void* g;       /* [n] gradient */
+    void* m;             /* [n] first moment: fp32, or 8-bit codes         (updated) */
+    void* v;             /* [n] second moment: fp32 >= 0, or 8-bit codes   (updated) */
+    uint8_t* m_exp;      /* [ceil(n/256)] exponent bytes of 8-bit states, else NULL */
+    uint8_t* v_exp;      /* [ceil(n/256)] likewise                         (updated) */
+    void* copy;          /* [n] the new weights in copy_dtype, or NULL     (written) */
+    int64_t n;
+    double weight_decay;
+} zpq_adamw_tensor;
+
+typedef struct {
+    void* table;
+    int64_t elems, chunks;
+    int32_t count, p_dtype, g_dtype, copy_dtype, state_bits, chunk_elems;
+} zpq_adamw_plan;
+
+/*
+ * Lay out `count` tensors for zpq_adamw_step.  p_dtype and g_dtype: any element
+ * type.  copy_dtype: ZPQ_F16 or ZPQ_BF16 with p_dtype ZPQ_F32 and every copy
+ * set, or -1 and every copy NULL (ZPQ_ERR_MODE otherwise).  state_bits: 32
+ * or 8.  table, table_bytes, stream: as in zpq_list_make.
+ */
+zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, int32_t p_dtype,
+                               int32_t g_dtype, int32_t copy_dtype, int32_t state_bits,
+                               void* table, int64_t table_bytes, zpq_adamw_plan* plan,
+                               zpq_stream stream);
+
+typedef struct {
+    double lr, beta1, beta2, eps;  /* lr >= 0, 0 <= beta < 1, eps >= 1e-30 */
+    double grad_scale;             /* > 0: gradients are multiplied by it (loss scale, averaging) */
+    double max_norm;               /* > 0: largest norm of the scaled gradients; infinity: none */
+    int64_t step;                  /* >= 1: which step this is, for the bias corrections */
+    uint64_t seed;                 /* of the random numbers that round 8-bit states */
+} zpq_adamw_hyper;
+
+/*
+ * One AdamW step over all tensors of a plan, element by element:
+ *   c  = fl32(grad_scale * min(1, max_norm / (grad_scale * sqrt(sumsq) + 1e-6)))
+ *   g' = g * c
+ *   m' = beta1 * m + (1 - beta1) * g'
+ *   v' = beta2 * v + ((1 - beta2) * g') * g'
+ *   p' = p * (1 - lr * weight_decay)
+ *        - lr / (1 - beta1^step) * (m' / (sqrt(v') / sqrt(1 - beta2^step) + eps))
+ * in binary32, one rounding an operation, the constants rounded once from
+ * binary64; p' is rounded to nearest even into p_dtype and copy_dtype.
+ *
+ * sumsq: device pointer to the squared norm of the unscaled gradients (all
+ * ranks'), or NULL: c = fl32(grad_scale), and max_norm must be infinite
+ * (ZPQ_ERR_ARG).  A sumsq that is not finite leaves every output as it was.
+ *
+ * 8-bit states: blocks of 256 consecutive elements of a tensor (the last one
+ * may be short) have one exponent byte e >= 1, the binary32 exponent field of
+ * the block's largest magnitude after rounding it up to 3 fraction bits.  m
+ * is a sign, a 4-bit exponent field f and 3 fraction bits q, v a 5-bit field
+ * and 3 fraction bits: with T = 15 or 31 the value is
+ * (1 + q/8) * 2^(f - T + e - 127), or q/8 * 2^(1 - T + e - 127) for f = 0.
+ * New states are rounded up or down at random, up with the probability of the
+ * distance, 16 random bits a value: an average that a step moves by 1 part in
+ * a thousand would stand still under rounding to nearest.  A v' above 0 never
+ * becomes 0.  A block with a value that is not finite, or over 1.875 * 2^127,
+ * becomes infinite as a whole.  The random bits are a hash of (seed, step,
+ * element): element i of tensor t counts as b_t + i, b_t the sum of the sizes
+ * before t, each rounded up to 256.
+ */
+zpq_status zpq_adamw_step(const zpq_adamw_plan* plan, const zpq_adamw_hyper* hyper,
+                          const double* sumsq, zpq_stream stream);
+
+/* 8-bit states to and from float tensors (checkpoints); moment: 1 (m) or 2
+ * (v).  Packing rounds to nearest even, magnitudes of v (its sign is lost);
+ * blocks as above, of one tensor of n elements. */
+zpq_status zpq_state8_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t moment,
+                             void* y, int32_t y_dtype, zpq_stream stream);
+zpq_status zpq_state8_pack(const void* x, int32_t x_dtype, int64_t n, int32_t moment,
+                           uint8_t* codes, uint8_t* exps, zpq_stream stream);
+
+/*
+ * Embedding lookup: out row t = RNE(scale * table row (ids[t] - first)), the
+ * product in binary32; a row of zeros where ids[t] - first is not in [0, rows)
+ * (padding, or a row of another shard of the vocabulary).
+ *   table [rows] rows of dim elements of type t_dtype, ld_table elements apart
+ *   ids   [tokens] of 4 or 8 bytes (id_bytes)
+ *   out   [tokens] rows of dim elements of type out_dtype, ld_out apart
+ * zpq_embedding_i8 reads the table as qwZ gathers it: INT8 codes [rows * dim]
+ * and one fp32 scale for each `block` of them (rows need not be whole blocks;
+ * scales [ceil(rows * dim / block)]); its row element is fl32(code * scale).
+ * dim >= 1, ld >= dim; tokens, rows < 2^31.
+ */
+zpq_status zpq_embedding(const void* table, int32_t t_dtype, int64_t rows, int64_t dim,
+                         int64_t ld_table, const void* ids, int32_t id_bytes, int64_t tokens,
+                         int64_t first, float scale, void* out, int32_t out_dtype, int64_t ld_out,
+                         zpq_stream stream);
+zpq_status zpq_embedding_i8(const int8_t* codes, const float* scales, int64_t rows, int64_t dim,
+                            int32_t block, const void* ids, int32_t id_bytes, int64_t tokens,
+                            int64_t first, float scale, void* out, int32_t out_dtype,
+                            int64_t ld_out, zpq_stream stream);
+
+/*
+ * Gradient of the lookup, dense: for each row r
+ *   grad[r] = RNE([grad[r] +] fl32(scale * sum of dy[t] over t with ids[t] - first = r))
+ * (with accumulate the fp32 sum of both is rounded once, and rows without a
+ * token are not touched; without, they become zeros).  The sum is in binary32,
+ * in an order that depends on the ids only: the tokens are sorted by row, equal
+ * rows in token order, and long rows are summed in parts; no atomics.  Ids outside [first, first + rows) and ids
+ * equal to `padding` count for nothing (give padding = -1, or any id outside,
+ * for none).
+ *   dy    [tokens] rows of dim elements of type dy_dtype, ld_dy apart
+ *   grad  [rows] rows of dim elements of type grad_dtype, ld_grad apart
+ *   workspace: zpq_embedding_grad_bytes bytes of device memory, 16-byte
+ *   aligned, contents irrelevant
+ * tokens <= 2^28, rows <= 2^27, dim <= 2^28.
+ */
+zpq_status zpq_embedding_grad_bytes(int64_t tokens, int64_t dim, int64_t* bytes);
+zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* ids,
+                              int32_t id_bytes, int64_t tokens, int64_t first, int64_t padding,
+                              int64_t rows, int64_t dim, float scale, void* grad,
+                              int32_t grad_dtype, int64_t ld_grad, int32_t accumulate,
+                              void* workspace, int64_t workspace_bytes, zpq_stream stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* zpq_status_str(zpq_status s);
 
