@@ -107,7 +107,7 @@ def lib():
         L.zpq_embedding.argtypes = [vp, i32, i64, i64, i64, vp, i32, i64, i64, f32, vp, i32, i64, vp]
         L.zpq_embedding_i8.argtypes = [vp, vp, i64, i64, i32, vp, i32, i64, i64, f32, vp, i32, i64,
                                        vp]
-        L.zpq_embedding_grad_bytes.argtypes = [i64, i64, ctypes.POINTER(i64)]
+        L.zpq_embedding_grad_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
         L.zpq_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, i64, i64, f32, vp,
                                          i32, i64, i32, vp, i64, vp]
         for f in (L.zpq_quant_i8, L.zpq_dequant_i8, L.zpq_quant_i8_tensor,
@@ -606,7 +606,7 @@ def embedding_grad(ids, dy, rows, scale=1.0, first=0, padding=None, out_dtype=No
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     need = ctypes.c_int64()
-    _check(lib().zpq_embedding_grad_bytes(n, dim, ctypes.byref(need)), "zpq_embedding_grad_bytes")
+    _check(lib().zpq_embedding_grad_bytes(n, rows, dim, ctypes.byref(need)), "zpq_embedding_grad_bytes")
     st, ctx = _on(stream, dev)
     with ctx:
         if out is None:

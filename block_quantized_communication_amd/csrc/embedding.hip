@@ -117,80 +117,197 @@ __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a) {
 
 // ---------------------------------------------------------------------------
 // Sorting the tokens by row.  A token is the 64-bit number row * 2^32 + position
-// (row = `rows` for what does not count): all different, so any correct sort
-// is the stable one.  Tiles of N are sorted in LDS by a bitonic network; then
-// runs are merged kFan at a time by ranks: an element's place in the merged run is
-// its place in its own plus, for each other run, how many elements there are
-// smaller (a binary search).  No counters, no atomics, two launches up to
-// kFan * N tokens.
-constexpr int kFan = 32;
-
-template <int N, int THREADS>
-__global__ __launch_bounds__(THREADS) void k_sort_tile(const void* __restrict__ ids,
-                                                       int32_t id_bytes, uint32_t tokens,
-                                                       int64_t first, int64_t padding, int64_t rows,
-                                                       uint64_t* __restrict__ out) {
-    __shared__ uint64_t s[N];
-    const uint32_t base = blockIdx.x * N;
-    for (int i = threadIdx.x; i < N; i += THREADS) {
-        const uint32_t t = base + i;
-        uint64_t x = ~0ull;
-        if (t < tokens) {
-            const int64_t id = load_id(ids, id_bytes, t);
-            const uint64_t r = (uint64_t)id - (uint64_t)first;
-            x = (r < (uint64_t)rows && id != padding ? r : (uint64_t)rows) << 32 | t;
-        }
-        s[i] = x;
-    }
-    __syncthreads();
-    for (int k = 2; k <= N; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int i = threadIdx.x; i < N / 2; i += THREADS) {
-                const int lo = (i & (j - 1)) | (i & ~(j - 1)) << 1, hi = lo | j;
-                const uint64_t a = s[lo], b = s[hi];
-                if ((a > b) == ((lo & k) == 0)) { s[lo] = b; s[hi] = a; }
-            }
-            __syncthreads();
-        }
-    for (int i = threadIdx.x; i < N; i += THREADS)
-        if (base + i < tokens) out[base + i] = s[i];
+// (row = `rows` for what does not count).  All are different, so any correct sort
+// is the stable one.
+struct Ids {
+    const void* ids;
+    int64_t first, padding, rows;
+    int32_t id_bytes;
+    uint32_t tokens;
+};
+__device__ __forceinline__ uint32_t key_of(const Ids& a, uint32_t t) {
+    const int64_t id = load_id(a.ids, a.id_bytes, t);
+    const uint64_t r = (uint64_t)id - (uint64_t)a.first;
+    return r < (uint64_t)a.rows && id != a.padding ? (uint32_t)r : (uint32_t)a.rows;
 }
 
-// kLanes lanes search for one element, each in kFan / kLanes of the group's runs.
-constexpr int kLanes = 8;
-__global__ __launch_bounds__(kThreads) void k_merge(const uint64_t* __restrict__ in, uint32_t tokens,
-                                                    uint32_t run, uint64_t* __restrict__ out) {
-    const uint64_t g = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-    const uint32_t e = (uint32_t)(g / kLanes), part = (uint32_t)(g % kLanes);
-    if (e >= tokens) return;                  // whole groups of lanes: tokens are counted in them
-    const uint64_t x = in[e];
-    const uint32_t own = e / run, group = own / kFan * kFan;
-    const uint64_t start = (uint64_t)group * run;
-    uint32_t lo[kFan / kLanes], n[kFan / kLanes];
-    uint64_t at[kFan / kLanes];
+// Up to kRankTokens: a token's place is the number of tokens that come before
+// it, counted by comparing it with all of them.  A workgroup places 64 tokens, one a
+// lane; its waves share the others, 64 at a time through LDS (a broadcast read
+// gives 4, and each is one compare and one add with carry for 64 tokens).
+constexpr uint32_t kRankTokens = 16384;
+constexpr int kRankWaves = 16;
+__global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __restrict__ out) {
+    __shared__ uint32_t keys[kRankWaves][64];
+    __shared__ uint32_t counts[kRankWaves][64];
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    const uint32_t own = blockIdx.x, t = own * 64 + lane;
+    const uint32_t key = t < a.tokens ? key_of(a, t) : 0xFFFFFFFEu;
+    const uint32_t blocks = (a.tokens + 63) / 64;
+    uint32_t before = 0;
+    for (uint32_t b = wave; b < blocks; b += kRankWaves) {
+        const uint32_t j = b * 64 + lane;
+        __builtin_amdgcn_wave_barrier();
+        keys[wave][lane] = j < a.tokens ? key_of(a, j) : 0xFFFFFFFFu;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const u32x4* other = reinterpret_cast<const u32x4*>(keys[wave]);
+        if (b != own) {
+            // equal rows of earlier tokens come before, those of later ones do not
+            const uint32_t below = b < own ? key + 1 : key;
 #pragma unroll
-    for (int r = 0; r < kFan / kLanes; ++r) {
-        const uint32_t which = group + r * kLanes + part;
-        at[r] = (uint64_t)which * run;
-        n[r] = at[r] >= tokens ? 0 : tokens - at[r] < run ? (uint32_t)(tokens - at[r]) : run;
-        lo[r] = 0;
-        if (which == own) { lo[r] = e - own * run; n[r] = 0; }
-    }
-    for (uint32_t left = run; left > 0; left >>= 1) {   // n halves at least as fast as `left`
-#pragma unroll
-        for (int r = 0; r < kFan / kLanes; ++r)
-            if (n[r] > 0) {
-                const uint32_t half = n[r] >> 1;
-                if (in[at[r] + lo[r] + half] < x) { lo[r] += half + 1; n[r] -= half + 1; }
-                else n[r] = half;
+            for (int i = 0; i < 16; ++i) {
+                const u32x4 k = other[i];
+                before += (k.x < below) + (k.y < below) + (k.z < below) + (k.w < below);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) before += keys[wave][i] < (i < (int)lane ? key + 1 : key);
+        }
     }
-    uint32_t rank = 0;
+    counts[wave][lane] = before;
+    __syncthreads();
+    if (wave == 0 && t < a.tokens) {
 #pragma unroll
-    for (int r = 0; r < kFan / kLanes; ++r) rank += lo[r];
+        for (int w = 1; w < kRankWaves; ++w) before += counts[w][lane];
+        out[before] = (uint64_t)key << 32 | t;
+    }
+}
+
+// More tokens: a radix sort from the lowest digit, `bits` (at most 9) a pass, stable by
+// construction.  k_digit_counts counts each tile's digits; k_digit_place gives every
+// token its place: tokens with smaller digits, the same digit in earlier tiles, in
+// earlier waves of the tile, and earlier in its wave (found by ballots).
+constexpr int kMaxDigits = 512, kSortThreads = 1024, kSortTile = 4 * kSortThreads;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr uint32_t kDirectTiles = 64;         // up to this many tiles their counts are summed in place
+
+struct Pass {
+    int32_t shift, bits;
+    uint32_t tiles;
+};
+
+template <bool FIRST>
+__device__ __forceinline__ uint64_t sort_item(const Ids& a, const uint64_t* __restrict__ in, uint32_t t) {
+    if constexpr (FIRST) return (uint64_t)key_of(a, t) << 32 | t;
+    else return in[t];
+}
+
+// counts[digit][tile]
+template <bool FIRST>
+__global__ __launch_bounds__(kSortThreads) void k_digit_counts(Ids a, const uint64_t* __restrict__ in,
+                                                               Pass p, uint32_t* __restrict__ counts) {
+    __shared__ uint32_t n[kMaxDigits];
+    if (threadIdx.x < kMaxDigits) n[threadIdx.x] = 0;
+    __syncthreads();
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) rank += __shfl_xor(rank, d);
-    if (part == 0) out[start + rank] = x;
+    for (int k = 0; k < kSortTile / kSortThreads; ++k) {
+        const uint32_t t = blockIdx.x * kSortTile + k * kSortThreads + threadIdx.x;
+        if (t < a.tokens)
+            atomicAdd(&n[(uint32_t)(sort_item<FIRST>(a, in, t) >> (32 + p.shift)) & ((1u << p.bits) - 1)], 1u);
+    }
+    __syncthreads();
+    if (threadIdx.x < (1u << p.bits)) counts[threadIdx.x * p.tiles + blockIdx.x] = n[threadIdx.x];
+}
+
+// Many tiles: each digit's counts to the number in earlier tiles, in place, and
+// its total; one wave a digit.
+__global__ __launch_bounds__(64) void k_digit_scan(Pass p, uint32_t* __restrict__ counts,
+                                                   uint32_t* __restrict__ totals) {
+    uint32_t* row = counts + blockIdx.x * p.tiles;
+    uint32_t sum = 0;
+    for (uint32_t b = 0; b < p.tiles; b += 64) {
+        const uint32_t i = b + threadIdx.x;
+        const uint32_t x = i < p.tiles ? row[i] : 0;
+        uint32_t s = x;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t y = __shfl_up(s, d);
+            if ((int)threadIdx.x >= d) s += y;
+        }
+        if (i < p.tiles) row[i] = sum + s - x;
+        sum += __shfl(s, 63);
+    }
+    if (threadIdx.x == 0) totals[blockIdx.x] = sum;
+}
+
+template <bool FIRST>
+__global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint64_t* __restrict__ in,
+                                                              Pass p, const uint32_t* __restrict__ counts,
+                                                              const uint32_t* __restrict__ totals,
+                                                              uint64_t* __restrict__ out) {
+    __shared__ uint32_t seen[kSortWaves][kMaxDigits];      // of each wave, then before each wave
+    __shared__ uint32_t scan[2][kMaxDigits];
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    constexpr int kEach = kSortTile / kSortThreads;
+    uint64_t x[kEach];
+    uint32_t digit[kEach], rank[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {         // wave w holds the tile's tokens [256 w, 256 w + 256)
+        const uint32_t t = blockIdx.x * kSortTile + (wave * kEach + k) * 64 + lane;
+        x[k] = t < a.tokens ? sort_item<FIRST>(a, in, t) : ~0ull;
+    }
+    for (uint32_t i = lane; i < kMaxDigits; i += 64) seen[wave][i] = 0;
+    // the digit's share of earlier tiles, and its total
+    uint32_t total = 0, earlier = 0;
+    if (threadIdx.x < (1u << p.bits)) {
+        const uint32_t* row = counts + threadIdx.x * p.tiles;
+        if (p.tiles <= kDirectTiles) {
+            for (uint32_t b = 0; b < p.tiles; ++b) {
+                const uint32_t n = row[b];
+                total += n;
+                if (b < blockIdx.x) earlier += n;
+            }
+        } else {
+            total = totals[threadIdx.x];
+            earlier = row[blockIdx.x];
+        }
+    }
+    if (threadIdx.x < kMaxDigits) scan[0][threadIdx.x] = total;
+    __syncthreads();
+    const uint64_t lower = (1ull << lane) - 1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const uint32_t t = blockIdx.x * kSortTile + (wave * kEach + k) * 64 + lane;
+        const bool there = t < a.tokens;
+        digit[k] = (uint32_t)(x[k] >> (32 + p.shift)) & ((1u << p.bits) - 1);
+        uint64_t same = __ballot(there);
+        for (int b = 0; b < p.bits; ++b) {
+            const uint64_t on = __ballot((digit[k] >> b) & 1u);
+            same &= (digit[k] >> b) & 1u ? on : ~on;
+        }
+        rank[k] = seen[wave][digit[k]] + (uint32_t)__popcll(same & lower);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (there && (same & lower) == 0) seen[wave][digit[k]] += (uint32_t)__popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    // exclusive sums: over the digits of the totals, over the waves of a digit
+    int from = 0;
+    for (int d = 1; d < (1 << p.bits); d <<= 1) {
+        if (threadIdx.x < kMaxDigits)
+            scan[from ^ 1][threadIdx.x] =
+                scan[from][threadIdx.x] + ((int)threadIdx.x >= d ? scan[from][threadIdx.x - d] : 0);
+        from ^= 1;
+        __syncthreads();
+    }
+    __syncthreads();                          // the waves' counts
+    if (threadIdx.x < kMaxDigits) {
+        uint32_t at = scan[from][threadIdx.x] - total + earlier;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            const uint32_t n = seen[w][threadIdx.x];
+            seen[w][threadIdx.x] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const uint32_t t = blockIdx.x * kSortTile + (wave * kEach + k) * 64 + lane;
+        if (t < a.tokens) out[seen[wave][digit[k]] + rank[k]] = x[k];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -206,6 +323,7 @@ struct GradArgs {
     const uint64_t* sorted;
     const void* dy;
     void* grad;
+    uint32_t* starts;                         // [rows + 1]: each row's first place in `sorted`
     float* part[kMaxLevels];                  // [tokens >> 6l][dim] sums of level l = 1, 2, ...
     int64_t ld_dy, ld_grad, dim, rows;
     uint32_t tokens;
@@ -213,21 +331,22 @@ struct GradArgs {
     float scale;
 };
 
-// acc += `count` rows of 8 floats, `stride` elements apart; or dy rows by position.
+// acc += `count` rows of 8 elements; row(j, base) gives the place of the j-th.
 template <int DT, class Row>
 __device__ __forceinline__ void add_rows(float (&acc)[8], uint32_t count, bool narrow, int dim, Row row) {
+    constexpr int kFlight = 8;                // loads in flight
     uint32_t j = 0;
     if (!narrow) {
-        for (; j + 4 <= count; j += 4) {
-            Raw8<DT> r[4];
+        for (; j + kFlight <= count; j += kFlight) {
+            Raw8<DT> r[kFlight];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kFlight; ++u) {
                 const void* base;
                 const int64_t at = row(j + u, base);
-                r[u].load(base, at);
+                r[u].template load<false>(base, at);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < kFlight; ++u)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] += r[u].get(i);
         }
@@ -235,7 +354,7 @@ __device__ __forceinline__ void add_rows(float (&acc)[8], uint32_t count, bool n
             Raw8<DT> r;
             const void* base;
             const int64_t at = row(j, base);
-            r.load(base, at);
+            r.template load<false>(base, at);
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] += r.get(i);
         }
@@ -250,11 +369,32 @@ __device__ __forceinline__ void add_rows(float (&acc)[8], uint32_t count, bool n
     }
 }
 
-// Level `level` sums: lane L takes piece L % pieces of group L / pieces.
+// First place of the sorted list whose row is not below r.
+__device__ __forceinline__ uint32_t lower_bound(const uint64_t* __restrict__ s, uint32_t n, uint64_t r) {
+    uint32_t lo = 0;
+    while (n > 0) {
+        const uint32_t half = n >> 1;
+        if (s[lo + half] >> 32 < r) { lo += half + 1; n -= half + 1; } else n = half;
+    }
+    return lo;
+}
+
+// Level `level` sums: lane L takes piece L % pieces of group L / pieces.  On level 1
+// the workgroups from `start_blocks` on; those before find the rows' first places, a
+// row a lane.
 template <int DT, bool FIRST>
 __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t level, uint32_t lanes,
-                                                         Divisor pieces) {
-    const uint32_t lane = blockIdx.x * kThreads + threadIdx.x;
+                                                         uint32_t start_blocks, Divisor pieces) {
+    uint32_t block = blockIdx.x;
+    if constexpr (FIRST) {
+        if (block < start_blocks) {
+            const uint32_t r = block * kThreads + threadIdx.x;
+            if (r <= a.rows) a.starts[r] = lower_bound(a.sorted, a.tokens, r);
+            return;
+        }
+        block -= start_blocks;
+    }
+    const uint32_t lane = block * kThreads + threadIdx.x;
     if (lane >= lanes) return;
     const uint32_t group = quotient(lane, pieces);
     const uint32_t lo = group << (kGroupLog * level);            // whole groups only: in range
@@ -287,99 +427,109 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
     }
 }
 
-// First place of the sorted list whose row is not below r.
-__device__ __forceinline__ uint32_t lower_bound(const uint64_t* __restrict__ s, uint32_t n, uint64_t r) {
-    uint32_t lo = 0;
-    while (n > 0) {
-        const uint32_t half = n >> 1;
-        if (s[lo + half] >> 32 < r) { lo += half + 1; n -= half + 1; } else n = half;
-    }
-    return lo;
+// Reads of wave-uniform addresses through the scalar cache, of what earlier
+// launches wrote.
+template <class T>
+__device__ __forceinline__ T load_uniform(const T* p, int64_t i) {
+    typedef const T __attribute__((address_space(4))) scalar_t;
+    return reinterpret_cast<scalar_t*>(reinterpret_cast<uintptr_t>(p))[i];
 }
 
-// Workgroup b takes rows b, b + G, b + 2G, ... (kRows of them): frequent tokens
-// tend to have neighbouring ids, and this spreads them.
-constexpr int kRows = 16;
-template <int DT, int OT, bool ADD>
-__global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, Divisor pieces) {
-    __shared__ uint32_t begin[kRows], end[kRows];
-    if (threadIdx.x < 2 * kRows) {
-        const uint32_t r = threadIdx.x >> 1;
-        const uint64_t row = (uint64_t)r * gridDim.x + blockIdx.x;
-        const uint32_t at = lower_bound(a.sorted, a.tokens, row + (threadIdx.x & 1));
-        if (threadIdx.x & 1) end[r] = at; else begin[r] = at;
-    }
-    __syncthreads();
-    const bool narrow = a.dim < 8;
-    for (uint32_t k = threadIdx.x; k < kRows * pieces.d; k += kThreads) {
-        const uint32_t r = quotient(k, pieces);
-        const int64_t row = (int64_t)r * gridDim.x + blockIdx.x;
-        if (row >= a.rows) break;             // later k: later rows
-        const uint32_t e = end[r];
-        uint32_t at = begin[r];
-        if (ADD && at == e) continue;
-        int64_t col = (int64_t)(k - r * pieces.d) * 8;
-        const int count = (int)(a.dim - col < 8 ? a.dim - col : 8);    // elements this lane writes
-        if (!narrow && count < 8) col = a.dim - 8;
-        float acc[8] = {};
-        while (at < e) {
-            int level = a.levels;
-            while (level > 0 && ((at & ((1u << (kGroupLog * level)) - 1)) != 0 ||
-                                 e - at < (1u << (kGroupLog * level))))
-                --level;
-            if (level == 0) {
-                // up to the next group that could be whole
-                uint32_t stop = a.levels > 0 ? (at | (kGroup - 1)) + 1 : e;
-                if (stop > e || stop == 0) stop = e;
-                add_rows<DT>(acc, stop - at, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
-                    base = a.dy;
-                    return (int64_t)(uint32_t)a.sorted[at + j] * a.ld_dy + col;
-                });
-                at = stop;
-            } else {
-                // groups of this level up to the end, or to where a larger one starts
-                const uint32_t shift = kGroupLog * level;
-                uint32_t groups = (e - at) >> shift;
-                if (level < a.levels) {
-                    const uint32_t next = kGroup - ((at >> shift) & (kGroup - 1));
-                    if (next < groups) groups = next;
-                }
-                const int64_t g0 = at >> shift;
-                const float* part = a.part[level - 1];
-                add_rows<ZPQ_F32>(acc, groups, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
-                    base = part;
-                    return (g0 + j) * a.dim + col;
-                });
-                at += groups << shift;
+// Piece `piece` of row `row`, whose tokens are the places [at, e) of the list;
+// UNIFORM: the same row in the whole wave.
+template <int DT, int OT, bool ADD, bool UNIFORM>
+__device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t piece, uint32_t at, uint32_t e) {
+    const bool narrow = !UNIFORM && a.dim < 8;         // a wave's 64 pieces are more than one
+    int64_t col = (int64_t)piece * 8;
+    const int count = (int)(a.dim - col < 8 ? a.dim - col : 8);    // elements this lane writes
+    if (!narrow && count < 8) col = a.dim - 8;
+    float acc[8] = {};
+#pragma unroll 1
+    while (at < e) {
+        int level = a.levels;
+#pragma unroll 1
+        while (level > 0 && ((at & ((1u << (kGroupLog * level)) - 1)) != 0 ||
+                             e - at < (1u << (kGroupLog * level))))
+            --level;
+        if (level == 0) {
+            // up to the next group that could be whole
+            uint32_t stop = a.levels > 0 ? (at | (kGroup - 1)) + 1 : e;
+            if (stop > e) stop = e;
+            add_rows<DT>(acc, stop - at, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+                base = a.dy;
+                const uint64_t token = UNIFORM ? load_uniform(a.sorted, at + j) : a.sorted[at + j];
+                return (int64_t)(uint32_t)token * a.ld_dy + col;
+            });
+            at = stop;
+        } else {
+            // groups of this level up to the end, or to where a larger one starts
+            const uint32_t shift = kGroupLog * level;
+            uint32_t groups = (e - at) >> shift;
+            if (level < a.levels) {
+                const uint32_t next = kGroup - ((at >> shift) & (kGroup - 1));
+                if (next < groups) groups = next;
             }
+            const int64_t g0 = at >> shift;
+            const float* part = a.part[level - 1];
+            add_rows<ZPQ_F32>(acc, groups, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+                base = part;
+                return (g0 + j) * a.dim + col;
+            });
+            at += groups << shift;
         }
-        const int64_t o = row * a.ld_grad + col;
-        if (!narrow) {
-            Raw8<OT> old;
-            if constexpr (ADD) old.load(a.grad, o);
+    }
+    const int64_t o = row * a.ld_grad + col;
+    if (!narrow) {
+        Raw8<OT> old;
+        if constexpr (ADD) old.load(a.grad, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                acc[i] *= a.scale;
-                if constexpr (ADD) acc[i] = old.get(i) + acc[i];
-            }
-            if (count == 8) {
-                Raw8<OT> out;
-                out.set(acc);
-                out.store(a.grad, o);
-            } else {
-#pragma unroll
-                for (int i = 1; i < 8; ++i)
-                    if (i >= 8 - count) store1<OT>(a.grad, o + i, acc[i]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            acc[i] *= a.scale;
+            if constexpr (ADD) acc[i] = old.get(i) + acc[i];
+        }
+        if (count == 8) {
+            Raw8<OT> out;
+            out.set(acc);
+            out.store(a.grad, o);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < count) {
-                    float x = acc[i] * a.scale;
-                    if constexpr (ADD) x = load1<OT>(a.grad, o + i) + x;
-                    store1<OT>(a.grad, o + i, x);
-                }
+            for (int i = 1; i < 8; ++i)
+                if (i >= 8 - count) store1<OT>(a.grad, o + i, acc[i]);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < count) {
+                float x = acc[i] * a.scale;
+                if constexpr (ADD) x = load1<OT>(a.grad, o + i) + x;
+                store1<OT>(a.grad, o + i, x);
+            }
+    }
+}
+
+// WIDE: a wave takes 64 pieces of one row, so that the row's places and positions
+// are scalar; `pieces` counts waves a row.  Otherwise lanes are dealt out row by
+// row, several rows a wave.
+template <int DT, int OT, bool ADD, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first_row, uint32_t lanes,
+                                                       Divisor pieces) {
+    const uint32_t lane = blockIdx.x * kThreads + threadIdx.x;
+    if constexpr (WIDE) {
+        const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lane >> 6));
+        if (wave >= lanes) return;
+        const uint32_t r = quotient(wave, pieces);
+        const int64_t row = first_row + r;
+        const uint32_t at = load_uniform(a.starts, row), e = load_uniform(a.starts, row + 1);
+        const uint32_t piece = (wave - r * pieces.d) * 64 + (threadIdx.x & 63u);
+        if ((ADD && at == e) || (int64_t)piece * 8 >= a.dim) return;
+        row_sum<DT, OT, ADD, true>(a, row, piece, at, e);
+    } else {
+        if (lane >= lanes) return;
+        const uint32_t r = quotient(lane, pieces);
+        const int64_t row = first_row + r;
+        const uint32_t at = a.starts[row], e = a.starts[row + 1];
+        if (ADD && at == e) return;
+        row_sum<DT, OT, ADD, false>(a, row, lane - r * pieces.d, at, e);
     }
 }
 
@@ -438,62 +588,108 @@ zpq_status lookup(const void* table, int32_t t_dtype, const float* scales, int32
 }
 
 struct GradWorkspace {
-    int64_t sorted[2], part[kMaxLevels], bytes;
+    int64_t sorted[2], counts, totals, starts, part[kMaxLevels], bytes;
     int32_t levels;
 };
 
-// Levels are used from where a row could hold a whole group and more: 2 groups
-// of tokens.
-inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim) {
+// Level 1 pays from a few hundred tokens on, a further level (a launch that
+// mostly finds nothing to sum) only where a row could hold very many groups.
+inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim, int64_t rows) {
     GradWorkspace w = {};
-    const int64_t list = (tokens * 8 + 255) / 256 * 256;
-    w.sorted[0] = 0;
-    w.sorted[1] = list;
-    w.bytes = 2 * list;
-    for (int l = 1; l <= kMaxLevels && (tokens >> (kGroupLog * l)) >= 2; ++l) {
-        w.part[l - 1] = w.bytes;
-        w.bytes += ((tokens >> (kGroupLog * l)) * dim * 4 + 255) / 256 * 256;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = w.bytes;
+        w.bytes += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    w.starts = take((rows + 1) * 4);
+    w.sorted[0] = take(tokens * 8);
+    if (tokens > kRankTokens) {
+        w.sorted[1] = take(tokens * 8);
+        w.counts = take((tokens + kSortTile - 1) / kSortTile * kMaxDigits * 4);
+        w.totals = take(kMaxDigits * 4);
+    }
+    for (int l = 1; l <= kMaxLevels && (tokens >> (kGroupLog * l)) >= (l == 1 ? 4 : 32); ++l) {
+        w.part[l - 1] = take((tokens >> (kGroupLog * l)) * dim * 4);
         w.levels = l;
     }
     return w;
 }
 
+// The sorted list; `list` and `other` are exchanged as the passes need.
+void sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* counts, uint32_t* totals,
+                 hipStream_t st) {
+    if (a.tokens == 0) return;
+    if (a.tokens <= kRankTokens) {
+        hipLaunchKernelGGL(k_rank, dim3((a.tokens + 63) / 64), dim3(64 * kRankWaves), 0, st, a, list);
+        return;
+    }
+    int bits = 1;
+    while (a.rows >> bits) ++bits;            // of the largest key, `rows`
+    const int passes = (bits + 8) / 9;
+    Pass p = {0, (bits + passes - 1) / passes, (a.tokens + kSortTile - 1) / kSortTile};
+    for (int i = 0; i < passes; ++i, p.shift += p.bits) {
+        const dim3 grid(p.tiles), block(kSortThreads);
+        if (i == 0) hipLaunchKernelGGL(k_digit_counts<true>, grid, block, 0, st, a, list, p, counts);
+        else hipLaunchKernelGGL(k_digit_counts<false>, grid, block, 0, st, a, list, p, counts);
+        if (p.tiles > kDirectTiles)
+            hipLaunchKernelGGL(k_digit_scan, dim3(1u << p.bits), dim3(64), 0, st, p, counts, totals);
+        if (i == 0) hipLaunchKernelGGL(k_digit_place<true>, grid, block, 0, st, a, list, p, counts, totals, other);
+        else hipLaunchKernelGGL(k_digit_place<false>, grid, block, 0, st, a, list, p, counts, totals, other);
+        uint64_t* t = list;
+        list = other;
+        other = t;
+    }
+}
+
 template <int DT>
 void launch_groups(const GradArgs& a, hipStream_t st) {
     const uint32_t pieces = (uint32_t)((a.dim + 7) / 8);
-    for (int l = 1; l <= a.levels; ++l) {
-        const uint32_t lanes = (a.tokens >> (kGroupLog * l)) * pieces;
-        const dim3 grid((lanes + kThreads - 1) / kThreads);
+    const uint32_t start_blocks = (uint32_t)(a.rows / kThreads + 1);
+    for (int l = 1; l <= (a.levels > 0 ? a.levels : 1); ++l) {
+        const uint32_t lanes = l <= a.levels ? (a.tokens >> (kGroupLog * l)) * pieces : 0;
+        const unsigned blocks = lanes / kThreads + (lanes % kThreads != 0);
         if (l == 1)
-            hipLaunchKernelGGL((k_group_sums<DT, true>), grid, dim3(kThreads), 0, st, a, l, lanes,
-                               divisor(pieces));
+            hipLaunchKernelGGL((k_group_sums<DT, true>), dim3(blocks + start_blocks), dim3(kThreads), 0, st, a, l,
+                               lanes, start_blocks, divisor(pieces));
         else
-            hipLaunchKernelGGL((k_group_sums<DT, false>), grid, dim3(kThreads), 0, st, a, l, lanes,
+            hipLaunchKernelGGL((k_group_sums<DT, false>), dim3(blocks), dim3(kThreads), 0, st, a, l, lanes, 0,
                                divisor(pieces));
     }
 }
+template <int DT, int OT, bool ADD>
+void launch_rows(const GradArgs& a, hipStream_t st) {
+    const uint32_t pieces = (uint32_t)((a.dim + 7) / 8);
+    const bool wide = pieces >= 33;
+    const uint32_t per_row = wide ? (pieces + 63) / 64 : pieces;
+    const int64_t some = (1 << (wide ? 24 : 30)) / per_row;       // rows a launch: at most 2^30 lanes
+    for (int64_t first = 0; first < a.rows; first += some) {
+        const uint32_t n = (uint32_t)((a.rows - first < some ? a.rows - first : some) * per_row);
+        if (wide)
+            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, true>), dim3(n / 4 + (n % 4 != 0)), dim3(kThreads), 0, st,
+                               a, first, n, divisor(per_row));
+        else
+            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, false>), dim3(n / kThreads + (n % kThreads != 0)),
+                               dim3(kThreads), 0, st, a, first, n, divisor(per_row));
+    }
+}
 template <int DT, int OT>
-void launch_rows(const GradArgs& a, bool add, hipStream_t st) {
-    const dim3 grid((unsigned)((a.rows + kRows - 1) / kRows));
-    const Divisor pieces = divisor((uint32_t)((a.dim + 7) / 8));
-    if (add)
-        hipLaunchKernelGGL((k_row_sums<DT, OT, true>), grid, dim3(kThreads), 0, st, a, pieces);
-    else
-        hipLaunchKernelGGL((k_row_sums<DT, OT, false>), grid, dim3(kThreads), 0, st, a, pieces);
+void launch_rows_add(const GradArgs& a, bool add, hipStream_t st) {
+    if (add) launch_rows<DT, OT, true>(a, st);
+    else launch_rows<DT, OT, false>(a, st);
 }
 template <int DT>
 void launch_grad(const GradArgs& a, int32_t grad_dtype, bool add, hipStream_t st) {
     launch_groups<DT>(a, st);
-    if (grad_dtype == ZPQ_F32) launch_rows<DT, ZPQ_F32>(a, add, st);
-    else if (grad_dtype == ZPQ_F16) launch_rows<DT, ZPQ_F16>(a, add, st);
-    else launch_rows<DT, ZPQ_BF16>(a, add, st);
+    if (grad_dtype == ZPQ_F32) launch_rows_add<DT, ZPQ_F32>(a, add, st);
+    else if (grad_dtype == ZPQ_F16) launch_rows_add<DT, ZPQ_F16>(a, add, st);
+    else launch_rows_add<DT, ZPQ_BF16>(a, add, st);
 }
 
-// A launch holds less than 2^32 work-items, kLanes a token and kThreads for
-// kRows rows; rows of pieces and groups of pieces are counted in 31 bits.
+// A launch holds less than 2^32 work-items; groups of pieces are counted in 31
+// bits, a launch's rows of pieces in 30.
 bool grad_sizes_ok(int64_t tokens, int64_t dim, int64_t rows) {
-    return tokens >= 0 && tokens <= (1LL << 28) && dim >= 1 && dim <= (1 << 28) && rows <= (1LL << 27) &&
-           (tokens >> kGroupLog) * ((dim + 7) / 8) < (1LL << 31) && kRows * ((dim + 7) / 8) < (1LL << 31);
+    return tokens >= 0 && tokens <= (1LL << 28) && dim >= 1 && dim <= (1 << 28) && rows >= 0 &&
+           rows <= (1LL << 27) && (tokens >> kGroupLog) * ((dim + 7) / 8) < (1LL << 31);
 }
 
 }  // namespace
@@ -540,10 +736,10 @@ zpq_status zpq_embedding_i8(const int8_t* codes, const float* scales, int64_t ro
                   out_dtype, ld_out, static_cast<hipStream_t>(stream));
 }
 
-zpq_status zpq_embedding_grad_bytes(int64_t tokens, int64_t dim, int64_t* bytes) {
+zpq_status zpq_embedding_grad_bytes(int64_t tokens, int64_t rows, int64_t dim, int64_t* bytes) {
     if (!bytes) return ZPQ_ERR_NULL;
-    if (!grad_sizes_ok(tokens, dim, 0)) return ZPQ_ERR_SIZE;
-    *bytes = grad_workspace(tokens, dim).bytes;
+    if (!grad_sizes_ok(tokens, dim, rows)) return ZPQ_ERR_SIZE;
+    *bytes = grad_workspace(tokens, dim, rows).bytes;
     return ZPQ_OK;
 }
 
@@ -558,8 +754,8 @@ zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, c
     if (yb == 0 || gb == 0) return ZPQ_ERR_DTYPE;
     if (id_bytes != 4 && id_bytes != 8) return ZPQ_ERR_ARG;
     if (rows == 0) return ZPQ_OK;
-    const GradWorkspace w = grad_workspace(tokens, dim);
-    if (!grad || (tokens > 0 && (!dy || !ids || !workspace))) return ZPQ_ERR_NULL;
+    const GradWorkspace w = grad_workspace(tokens, dim, rows);
+    if (!grad || !workspace || (tokens > 0 && (!dy || !ids))) return ZPQ_ERR_NULL;
     if (workspace_bytes < w.bytes) return ZPQ_ERR_SIZE;
     if (!aligned(grad, gb) || !aligned(dy, yb) || !aligned(ids, id_bytes) || !aligned(workspace, 16))
         return ZPQ_ERR_ALIGN;
@@ -573,30 +769,12 @@ zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, c
 
     hipStream_t st = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
+    auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
     uint64_t* list = reinterpret_cast<uint64_t*>(ws + w.sorted[0]);
     uint64_t* other = reinterpret_cast<uint64_t*>(ws + w.sorted[1]);
-    const uint32_t n = (uint32_t)tokens;
-    uint32_t run = 1024;
-    if (n > 0 && n <= 256) {
-        hipLaunchKernelGGL((k_sort_tile<256, 128>), dim3(1), dim3(128), 0, st, ids, id_bytes, n, first, padding,
-                           rows, list);
-    } else if (n > 0 && n <= 1024 * kFan) {
-        hipLaunchKernelGGL((k_sort_tile<1024, 512>), dim3((n + 1023) / 1024), dim3(512), 0, st, ids, id_bytes, n,
-                           first, padding, rows, list);
-    } else if (n > 0) {
-        run = 4096;
-        hipLaunchKernelGGL((k_sort_tile<4096, 1024>), dim3((n + 4095) / 4096), dim3(1024), 0, st, ids, id_bytes, n,
-                           first, padding, rows, list);
-    }
-    for (uint64_t r = run; r < n; r *= kFan) {
-        const uint64_t lanes = (uint64_t)n * kLanes;
-        hipLaunchKernelGGL(k_merge, dim3((unsigned)((lanes + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                           list, n, (uint32_t)r, other);
-        uint64_t* t = list;
-        list = other;
-        other = t;
-    }
-    GradArgs a = {list, dy, grad, {}, ld_dy, ld_grad, dim, rows, n, w.levels, scale};
+    sort_tokens(Ids{ids, first, padding, rows, id_bytes, (uint32_t)tokens}, list, other, words(w.counts),
+                words(w.totals), st);
+    GradArgs a = {list, dy, grad, words(w.starts), {}, ld_dy, ld_grad, dim, rows, (uint32_t)tokens, w.levels, scale};
     for (int l = 0; l < w.levels; ++l) a.part[l] = reinterpret_cast<float*>(ws + w.part[l]);
     if (dy_dtype == ZPQ_F32) launch_grad<ZPQ_F32>(a, grad_dtype, accumulate != 0, st);
     else if (dy_dtype == ZPQ_F16) launch_grad<ZPQ_F16>(a, grad_dtype, accumulate != 0, st);

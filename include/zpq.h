@@ -322,7 +322,7 @@ zpq_status zpq_embedding_i8(const int8_t* codes, const float* scales, int64_t ro
  *   aligned, contents irrelevant
  * tokens <= 2^28, rows <= 2^27, dim <= 2^28.
  */
-zpq_status zpq_embedding_grad_bytes(int64_t tokens, int64_t dim, int64_t* bytes);
+zpq_status zpq_embedding_grad_bytes(int64_t tokens, int64_t rows, int64_t dim, int64_t* bytes);
 zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* ids,
                               int32_t id_bytes, int64_t tokens, int64_t first, int64_t padding,
                               int64_t rows, int64_t dim, float scale, void* grad,

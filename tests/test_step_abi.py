@@ -203,10 +203,11 @@ def test_grad_refusals():
     assert grad(rows=0, out=0) == OK
     assert grad(tokens=0, acc=1) == OK
     n = ctypes.c_int64()
-    assert zpq.lib().zpq_embedding_grad_bytes(10, 16, None) == NULL
-    assert zpq.lib().zpq_embedding_grad_bytes(-1, 16, ctypes.byref(n)) == SIZE
-    assert zpq.lib().zpq_embedding_grad_bytes(0, 16, ctypes.byref(n)) == OK and n.value == 0
-    assert zpq.lib().zpq_embedding_grad_bytes(1 << 28, 64, ctypes.byref(n)) == OK and n.value >= 2 << 31
+    assert zpq.lib().zpq_embedding_grad_bytes(10, 5, 16, None) == NULL
+    assert zpq.lib().zpq_embedding_grad_bytes(-1, 5, 16, ctypes.byref(n)) == SIZE
+    assert zpq.lib().zpq_embedding_grad_bytes(1, -1, 16, ctypes.byref(n)) == SIZE
+    assert zpq.lib().zpq_embedding_grad_bytes(0, 5, 16, ctypes.byref(n)) == OK and 24 <= n.value <= 4096
+    assert zpq.lib().zpq_embedding_grad_bytes(1 << 28, 5, 64, ctypes.byref(n)) == OK and n.value >= 2 << 31
 
 
 def test_structures_match_the_header():
