@@ -14,9 +14,10 @@ namespace {
 
 using namespace zpq_step;
 
-constexpr int kTile = kThreads * 8;           // elements of one pass of a workgroup, 8 a lane
-constexpr int kStateBlock = 256;              // elements of an 8-bit state block: 32 lanes
-static_assert(kTile % kStateBlock == 0, "a tile holds whole state blocks");
+constexpr int kStateBlock = 256;              // elements of an 8-bit state block: one wave, 4 a lane
+constexpr int kPart = kThreads * 4;           // elements that a workgroup takes at once, 4 a lane
+constexpr int kParts = 2;                     // parts of a step tile, all loaded before any is computed
+constexpr int kTile = kPart * kParts;
 
 // ---------------------------------------------------------------------------
 // Tables.
@@ -69,7 +70,8 @@ uint32_t* starts_of(void* table, int32_t count) {
 // value and no range checks.  Workgroup b of G takes the chunks
 // [K*b/G, K*(b+1)/G): consecutive, so that the tensor is looked up once and
 // then followed.
-constexpr int kSumChunk = 4 * kTile;
+template <int DT> constexpr int kSumEach = DT == ZPQ_F32 ? 4 : 8;       // elements a lane
+constexpr int kSumChunk = 8192;               // elements of a workgroup's share
 constexpr int kSumParts = 4096;               // ZPQ_SUMSQ_BYTES / 8
 static_assert(kSumParts * 8 == ZPQ_SUMSQ_BYTES, "workspace");
 
@@ -99,13 +101,14 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
         const ListEntry e = entries[t];
         const int64_t at = (int64_t)(k - starts[t]) * kSumChunk;
         if (at + kSumChunk <= e.n) {
-            Raw8<DT> r[4];
+            constexpr int E = kSumEach<DT>, N = kSumChunk / (kThreads * E);
+            Raw<DT, E> r[N];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) r[u].load(e.ptr, at + u * kTile + threadIdx.x * 8);
+            for (int u = 0; u < N; ++u) r[u].load(e.ptr, at + (u * kThreads + threadIdx.x) * E);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < N; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < E; ++i) {
                     const double x = (double)r[u].get(i);
                     s[i & 3] = __builtin_fma(x, x, s[i & 3]);
                 }
@@ -125,7 +128,16 @@ __global__ __launch_bounds__(kThreads) void k_sumsq_join(const double* __restric
                                                          int32_t parts, int32_t accumulate,
                                                          double* __restrict__ out) {
     double s = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+    for (int b = 0; b < parts; b += 8 * kThreads) {
+        double x[8];                          // loaded together
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = b + u * kThreads + threadIdx.x;
+            x[u] = i < parts ? part[i] : 0.0;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += x[u];
+    }
     s = wg_sum(s);
     if (threadIdx.x == 0) out[0] = accumulate ? out[0] + s : s;
 }
@@ -138,17 +150,21 @@ __global__ __launch_bounds__(kThreads) void k_sumsq_join(const double* __restric
 // below bit 20.  ldexp moves the field, for any e, with one rounding where
 // the result is subnormal.
 
-// Cross-lane maximum of unsigned values over aligned groups of 32 lanes.
+// Maximum over the wave of unsigned values, as a scalar.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ uint32_t max32(uint32_t v) {
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = max(v, dpp<0xB1>(v));                 // quad_perm [1,0,3,2]
     v = max(v, dpp<0x4E>(v));                 // quad_perm [2,3,0,1]
     v = max(v, dpp<0x141>(v));                // row_half_mirror
-    v = max(v, dpp<0x140>(v));                // row_mirror
-    return max(v, (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401F));   // lane ^ 16
+    v = max(v, dpp<0x140>(v));                // row_mirror: rows of 16 done
+    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
+    const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32);
+    const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+    return max(max(a, b), max(c, d));
 }
 
 // Exponent byte of a block from the bits of its largest magnitude: up to
@@ -208,8 +224,107 @@ struct StepArgs {
     uint32_t key;
 };
 
+// 4 elements a lane of one part: loaded together, stepped, stored.  A wave holds
+// 256 consecutive elements, which is a state block: the exponents of 8-bit
+// states are scalars.
+template <int PT, int GT, int CT, int BITS>
+struct Part {
+    static constexpr int ST = BITS == 32 ? ZPQ_F32 : kI8;
+    Raw<PT, 4> p;
+    Raw<GT, 4> g;
+    Raw<ST, 4> m, v;
+    uint32_t em, ev;
+    int64_t i0;
+    int have;                                 // elements of this lane, 0 to 4
+
+    __device__ __forceinline__ void load(const PlanEntry& e, int64_t at) {
+        i0 = at + threadIdx.x * 4;
+        have = (int)(e.n - i0 < 0 ? 0 : e.n - i0 < 4 ? e.n - i0 : 4);
+        em = ev = 1;
+        if constexpr (BITS == 8) {
+            const int64_t b = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) + at / kStateBlock;
+            if (b * kStateBlock < e.n) { em = e.me[b]; ev = e.ve[b]; }
+        }
+        if (have == 4) {
+            p.load(e.p, i0);
+            g.load(e.g, i0);
+            m.load(e.m, i0);
+            v.load(e.v, i0);
+        } else {
+            p.load_some(e.p, i0, have);
+            g.load_some(e.g, i0, have);
+            m.load_some(e.m, i0, have);
+            v.load_some(e.v, i0, have);
+        }
+    }
+
+    __device__ __forceinline__ void step(const PlanEntry& e, const StepArgs& a, float c, float keep) {
+        float pp[4], mm[4], vv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float m0, v0;
+            if constexpr (BITS == 32) {
+                m0 = m.get(i);
+                v0 = v.get(i);
+            } else {
+                m0 = decode8<1>(m.byte(i), em);
+                v0 = decode8<2>(v.byte(i), ev);
+            }
+            const float x = g.get(i) * c;
+            mm[i] = m0 * a.b1 + x * a.ob1;
+            vv[i] = v0 * a.b2 + (x * a.ob2) * x;
+            const float u = mm[i] / (__builtin_sqrtf(vv[i]) * a.rbc2 + a.eps);
+            pp[i] = p.get(i) * keep - u * a.rate;
+        }
+        p.set(pp);
+        if constexpr (BITS == 32) {
+            m.set(mm);
+            v.set(vv);
+        } else {
+            // lanes past the end hold zeros: m and v of zeros stay zeros
+            uint32_t am = 0, av = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                am = max(am, __float_as_uint(mm[i]) & 0x7FFFFFFFu);
+                av = max(av, __float_as_uint(vv[i]) & 0x7FFFFFFFu);
+            }
+            em = block_exp(wave_max(am));
+            ev = block_exp(wave_max(av));
+            const uint64_t n0 = (uint64_t)(e.base + i0);
+            const uint32_t x0 = (uint32_t)n0 * kMulLo + (uint32_t)(n0 >> 32) * kMulHi + a.key;
+            m.w[0] = v.w[0] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {     // base and i0 are multiples of 4: no carry within 4
+                const uint32_t r = mix(x0 + (uint32_t)i * kMulLo);
+                m.w[0] |= encode8<1>(mm[i], em, ((r & 0xFFFFu) << 4) + 8, false) << (8 * i);
+                v.w[0] |= encode8<2>(vv[i], ev, ((r >> 16) << 4) + 8, false) << (8 * i);
+            }
+        }
+        // out
+        Raw<CT < 0 ? ZPQ_F16 : CT, 4> copy;
+        if constexpr (CT >= 0) copy.set(pp);
+        if (have == 4) {
+            p.store(e.p, i0);
+            if constexpr (CT >= 0) copy.store(e.copy, i0);
+            m.store(e.m, i0);
+            v.store(e.v, i0);
+        } else {
+            p.store_some(e.p, i0, have);
+            if constexpr (CT >= 0) copy.store_some(e.copy, i0, have);
+            m.store_some(e.m, i0, have);
+            v.store_some(e.v, i0, have);
+        }
+        if constexpr (BITS == 8) {
+            if ((threadIdx.x & 63) == 0 && have > 0) {
+                e.me[i0 / kStateBlock] = (uint8_t)em;
+                e.ve[i0 / kStateBlock] = (uint8_t)ev;
+            }
+        }
+    }
+};
+
 // Workgroup k of the grid (and k + gridDim.x, ...) takes chunk k: chunk_elems
-// consecutive elements of one tensor, in tiles of 8 elements a lane.
+// consecutive elements of one tensor, in tiles of kParts parts.
 template <int PT, int GT, int CT, int BITS>
 __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict__ entries,
                                                     const uint32_t* __restrict__ starts,
@@ -230,157 +345,45 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict_
         int64_t at = (int64_t)(k - starts[t]) * chunk_elems;
         const int64_t end = at + chunk_elems < e.n ? at + chunk_elems : e.n;
         for (; at < end; at += kTile) {
-            const int64_t i0 = at + threadIdx.x * 8;
-            const int have = (int)(e.n - i0 < 0 ? 0 : e.n - i0 < 8 ? e.n - i0 : 8);
-            const bool whole = have == 8;
-            float p[8], g[8], m[8], v[8];
-            // ---- in
-            if (whole) {
-                Raw8<PT> rp;
-                Raw8<GT> rg;
-                rp.load(e.p, i0);
-                rg.load(e.g, i0);
-                if constexpr (BITS == 32) {
-                    Raw8<ZPQ_F32> rm, rv;
-                    rm.load(e.m, i0);
-                    rv.load(e.v, i0);
+            Part<PT, GT, CT, BITS> part[kParts];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) { m[i] = rm.get(i); v[i] = rv.get(i); }
-                } else {
-                    Raw8<kI8> rm, rv;
-                    rm.load(e.m, i0);
-                    rv.load(e.v, i0);
-                    const uint32_t em = e.me[i0 / kStateBlock], ev = e.ve[i0 / kStateBlock];
+            for (int u = 0; u < kParts; ++u) part[u].load(e, at + u * kPart);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        m[i] = decode8<1>((rm.w[i >> 2] >> (8 * (i & 3))) & 0xFFu, em);
-                        v[i] = decode8<2>((rv.w[i >> 2] >> (8 * (i & 3))) & 0xFFu, ev);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) { p[i] = rp.get(i); g[i] = rg.get(i); }
-            } else {
-                uint32_t em = 1, ev = 1;
-                if constexpr (BITS == 8) {
-                    if (have > 0) { em = e.me[i0 / kStateBlock]; ev = e.ve[i0 / kStateBlock]; }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    p[i] = g[i] = m[i] = v[i] = 0.0f;
-                    if (i < have) {
-                        p[i] = load1<PT>(e.p, i0 + i);
-                        g[i] = load1<GT>(e.g, i0 + i);
-                        if constexpr (BITS == 32) {
-                            m[i] = load1<ZPQ_F32>(e.m, i0 + i);
-                            v[i] = load1<ZPQ_F32>(e.v, i0 + i);
-                        } else {
-                            m[i] = decode8<1>(static_cast<const uint8_t*>(e.m)[i0 + i], em);
-                            v[i] = decode8<2>(static_cast<const uint8_t*>(e.v)[i0 + i], ev);
-                        }
-                    }
-                }
-            }
-            // ---- the step
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = g[i] * c;
-                m[i] = m[i] * a.b1 + x * a.ob1;
-                v[i] = v[i] * a.b2 + (x * a.ob2) * x;
-                const float u = m[i] / (__builtin_sqrtf(v[i]) * a.rbc2 + a.eps);
-                p[i] = p[i] * keep - u * a.rate;
-            }
-            // ---- out
-            uint32_t cm[8], cv[8], em = 1, ev = 1;
-            if constexpr (BITS == 8) {
-                // lanes past the end hold zeros: m and v of zeros stay zeros
-                uint32_t am = 0, av = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    am = max(am, __float_as_uint(m[i]) & 0x7FFFFFFFu);
-                    av = max(av, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-                }
-                em = block_exp(max32(am));
-                ev = block_exp(max32(av));
-                const uint64_t at0 = (uint64_t)(e.base + i0);
-                const uint32_t x0 = (uint32_t)at0 * kMulLo + (uint32_t)(at0 >> 32) * kMulHi + a.key;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {   // base and i0 are multiples of 8: no carry within 8
-                    const uint32_t r = mix(x0 + (uint32_t)i * kMulLo);
-                    cm[i] = encode8<1>(m[i], em, ((r & 0xFFFFu) << 4) + 8, false);
-                    cv[i] = encode8<2>(v[i], ev, ((r >> 16) << 4) + 8, false);
-                }
-            }
-            if (whole) {
-                Raw8<PT> rp;
-                rp.set(p);
-                rp.store(e.p, i0);
-                if constexpr (CT >= 0) {
-                    Raw8<CT> rc;
-                    rc.set(p);
-                    rc.store(e.copy, i0);
-                }
-                if constexpr (BITS == 32) {
-                    Raw8<ZPQ_F32> r;
-                    r.set(m);
-                    r.store(e.m, i0);
-                    r.set(v);
-                    r.store(e.v, i0);
-                } else {
-                    Raw8<kI8> r;
-                    r.w[0] = cm[0] | cm[1] << 8 | cm[2] << 16 | cm[3] << 24;
-                    r.w[1] = cm[4] | cm[5] << 8 | cm[6] << 16 | cm[7] << 24;
-                    r.store(e.m, i0);
-                    r.w[0] = cv[0] | cv[1] << 8 | cv[2] << 16 | cv[3] << 24;
-                    r.w[1] = cv[4] | cv[5] << 8 | cv[6] << 16 | cv[7] << 24;
-                    r.store(e.v, i0);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < have) {
-                        store1<PT>(e.p, i0 + i, p[i]);
-                        if constexpr (CT >= 0) store1<CT>(e.copy, i0 + i, p[i]);
-                        if constexpr (BITS == 32) {
-                            store1<ZPQ_F32>(e.m, i0 + i, m[i]);
-                            store1<ZPQ_F32>(e.v, i0 + i, v[i]);
-                        } else {
-                            static_cast<uint8_t*>(e.m)[i0 + i] = (uint8_t)cm[i];
-                            static_cast<uint8_t*>(e.v)[i0 + i] = (uint8_t)cv[i];
-                        }
-                    }
-            }
-            if constexpr (BITS == 8) {
-                if ((threadIdx.x & 31) == 0 && have > 0) {
-                    e.me[i0 / kStateBlock] = (uint8_t)em;
-                    e.ve[i0 / kStateBlock] = (uint8_t)ev;
-                }
-            }
+            for (int u = 0; u < kParts; ++u) part[u].step(e, a, c, keep);
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// 8-bit states to floats and back, 8 elements a lane.
+// 8-bit states to floats and back, 4 elements a lane: a wave holds a block.
+constexpr int kConvParts = 4;
 template <int DT, int MOMENT>
 __global__ __launch_bounds__(kThreads) void k_unpack8(const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ exps, int64_t n,
                                                       void* __restrict__ y) {
-    for (int64_t at = (int64_t)blockIdx.x * kTile; at < n; at += (int64_t)gridDim.x * kTile) {
-        const int64_t i0 = at + threadIdx.x * 8;
-        if (i0 >= n) continue;
-        const uint32_t e = exps[i0 / kStateBlock];
-        if (i0 + 8 <= n) {
-            Raw8<kI8> r;
-            r.load(codes, i0);
-            float x[8];
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    constexpr int64_t kAll = (int64_t)kPart * kConvParts;
+    for (int64_t at = blockIdx.x * kAll; at < n; at += gridDim.x * kAll) {
+        Raw<kI8, 4> r[kConvParts];
+        uint32_t e[kConvParts];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = decode8<MOMENT>((r.w[i >> 2] >> (8 * (i & 3))) & 0xFFu, e);
-            Raw8<DT> o;
+        for (int u = 0; u < kConvParts; ++u) {
+            const int64_t first = at + u * kPart, i0 = first + threadIdx.x * 4;
+            const int64_t b = first / kStateBlock + wave;
+            e[u] = b * kStateBlock < n ? exps[b] : 1;
+            if (i0 + 4 <= n) r[u].load(codes, i0);
+            else r[u].load_some(codes, i0, (int)(n - i0 < 0 ? 0 : n - i0));
+        }
+#pragma unroll
+        for (int u = 0; u < kConvParts; ++u) {
+            const int64_t i0 = at + u * kPart + threadIdx.x * 4;
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = decode8<MOMENT>(r[u].byte(i), e[u]);
+            Raw<DT, 4> o;
             o.set(x);
-            o.store(y, i0);
-        } else {
-            for (int i = 0; i < 8 && i0 + i < n; ++i)
-                store1<DT>(y, i0 + i, decode8<MOMENT>(codes[i0 + i], e));
+            if (i0 + 4 <= n) o.store(y, i0);
+            else o.store_some(y, i0, (int)(n - i0 < 0 ? 0 : n - i0));
         }
     }
 }
@@ -389,32 +392,23 @@ template <int DT, int MOMENT>
 __global__ __launch_bounds__(kThreads) void k_pack8(const void* __restrict__ x, int64_t n,
                                                     uint8_t* __restrict__ codes,
                                                     uint8_t* __restrict__ exps) {
-    for (int64_t at = (int64_t)blockIdx.x * kTile; at < n; at += (int64_t)gridDim.x * kTile) {
-        const int64_t i0 = at + threadIdx.x * 8;
-        const int have = (int)(n - i0 < 0 ? 0 : n - i0 < 8 ? n - i0 : 8);
-        float v[8];
+    for (int64_t at = (int64_t)blockIdx.x * kPart; at < n; at += (int64_t)gridDim.x * kPart) {
+        const int64_t i0 = at + threadIdx.x * 4;
+        const int have = (int)(n - i0 < 0 ? 0 : n - i0 < 4 ? n - i0 : 4);
+        Raw<DT, 4> r;
+        if (have == 4) r.load(x, i0);
+        else r.load_some(x, i0, have);
         uint32_t a = 0;
-        if (have == 8) {
-            Raw8<DT> r;
-            r.load(x, i0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = r.get(i);
-        } else {
+        for (int i = 0; i < 4; ++i) a = max(a, __float_as_uint(r.get(i)) & 0x7FFFFFFFu);
+        const uint32_t e = block_exp(wave_max(a));
+        Raw<kI8, 4> c;
+        c.w[0] = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < have ? load1<DT>(x, i0 + i) : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        const uint32_t e = block_exp(max32(a));
-        if (have == 8) {
-            Raw8<kI8> r = {};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r.w[i >> 2] |= encode8<MOMENT>(v[i], e, 0, true) << (8 * (i & 3));
-            r.store(codes, i0);
-        } else {
-            for (int i = 0; i < have; ++i) codes[i0 + i] = (uint8_t)encode8<MOMENT>(v[i], e, 0, true);
-        }
-        if ((threadIdx.x & 31) == 0 && have > 0) exps[i0 / kStateBlock] = (uint8_t)e;
+        for (int i = 0; i < 4; ++i) c.w[0] |= encode8<MOMENT>(r.get(i), e, 0, true) << (8 * i);
+        if (have == 4) c.store(codes, i0);
+        else c.store_some(codes, i0, have);
+        if ((threadIdx.x & 63) == 0 && have > 0) exps[i0 / kStateBlock] = (uint8_t)e;
     }
 }
 
@@ -467,7 +461,7 @@ bool finite_at_least(double x, double least) { return x >= least && x <= 1.79769
 template <int DT>
 void launch_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t moment,
                    void* y, hipStream_t st) {
-    const dim3 grid(grid_of((n + kTile - 1) / kTile));
+    const dim3 grid(grid_of((n + kPart * kConvParts - 1) / (kPart * kConvParts)));
     if (moment == 1)
         hipLaunchKernelGGL((k_unpack8<DT, 1>), grid, dim3(kThreads), 0, st, codes, exps, n, y);
     else
@@ -476,7 +470,7 @@ void launch_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t
 template <int DT>
 void launch_pack(const void* x, int64_t n, int32_t moment, uint8_t* codes, uint8_t* exps,
                  hipStream_t st) {
-    const dim3 grid(grid_of((n + kTile - 1) / kTile));
+    const dim3 grid(grid_of((n + kPart - 1) / kPart));
     if (moment == 1)
         hipLaunchKernelGGL((k_pack8<DT, 1>), grid, dim3(kThreads), 0, st, x, n, codes, exps);
     else

@@ -1,15 +1,19 @@
 // embedding.hip -- embedding lookup with scaling, from a float table or from
 // qwZ's gathered INT8 blocks, and the embedding's gradient by sorted tokens.
 //
-// A row is cut into pieces of 8 elements, one a lane; the last piece of a row
-// whose length is no multiple of 8 is moved back so that it ends with the row
-// (it reads, and in the lookup writes, some elements twice).  Rows shorter
-// than 8 are one piece, handled element by element.
+// A row is cut into pieces of E elements, one a lane: 8, or 4 where a side is
+// fp32, so that no access is wider than 16 bytes.  The last piece of a row whose
+// length is no multiple of E is moved back so that it ends with the row (it
+// reads, and in the lookup writes, some elements twice).  Rows shorter than E are
+// one piece, handled element by element.
 #include "step.h"
 
 namespace {
 
 using namespace zpq_step;
+
+template <int A, int B>
+constexpr int piece_elems() { return A == ZPQ_F32 || B == ZPQ_F32 ? 4 : 8; }
 
 // n / d for n < 2^31 by a multiplication: with m = ceil(2^(31+s) / d) and 2^s >= d,
 // n * m / 2^(31+s) exceeds n / d by less than (n / 2^31) / d < 1 / d, too little to
@@ -38,15 +42,16 @@ struct LookupArgs {
     const float* scales;
     const void* ids;
     void* out;
-    int64_t rows, dim, ld_table, first, ld_out;
+    int64_t tokens, rows, dim, ld_table, first, ld_out;
     float scale;
     int32_t id_bytes, log_block;
-    uint32_t lanes;                           // tokens * pieces, < 2^31
+    uint32_t lanes;                           // tokens of this launch * pieces, < 2^31
     Divisor pieces;
 };
 
 template <int TT, int OT, int U>
 __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a) {
+    constexpr int E = piece_elems<TT, OT>();
     uint32_t lane[U], token[U];
     int64_t row[U];
     int32_t col[U];
@@ -54,11 +59,11 @@ __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a) {
     for (int u = 0; u < U; ++u) {
         lane[u] = (blockIdx.x * U + u) * kThreads + threadIdx.x;
         token[u] = quotient(lane[u], a.pieces);
-        col[u] = (int32_t)(lane[u] - token[u] * a.pieces.d) * 8;
+        col[u] = (int32_t)(lane[u] - token[u] * a.pieces.d) * E;
         row[u] = lane[u] < a.lanes ? load_id(a.ids, a.id_bytes, token[u])
                                   : (int64_t)((uint64_t)a.first - 1);
     }
-    if (a.dim < 8) {
+    if (a.dim < E) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (lane[u] >= a.lanes) continue;
@@ -76,25 +81,25 @@ __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a) {
         }
         return;
     }
-    Raw8<TT> in[U];
+    Raw<TT, E> in[U];
     float s0[U], s1[U];
     int32_t left[U];                          // elements of the piece that s0 scales
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (col[u] > a.dim - 8) col[u] = (int32_t)a.dim - 8;
+        if (col[u] > a.dim - E) col[u] = (int32_t)a.dim - E;
         const uint64_t r = (uint64_t)row[u] - (uint64_t)a.first;
         const bool there = r < (uint64_t)a.rows;
 #pragma unroll
-        for (int i = 0; i < Raw8<TT>::WORDS; ++i) in[u].w[i] = 0;
+        for (int i = 0; i < Raw<TT, E>::WORDS; ++i) in[u].w[i] = 0;
         s0[u] = s1[u] = 1.0f;
-        left[u] = 8;
+        left[u] = E;
         if (there) {
             const int64_t e = (int64_t)r * a.ld_table + col[u];
             in[u].template load<false>(a.table, e);
             if constexpr (TT == kI8) {
                 s0[u] = a.scales[e >> a.log_block];
                 left[u] = (1 << a.log_block) - (int32_t)(e & ((1 << a.log_block) - 1));
-                s1[u] = left[u] < 8 ? a.scales[(e >> a.log_block) + 1] : s0[u];
+                s1[u] = left[u] < E ? a.scales[(e >> a.log_block) + 1] : s0[u];
             }
         }
     }
@@ -102,14 +107,14 @@ __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a) {
     for (int u = 0; u < U; ++u) {
         if (lane[u] >= a.lanes) continue;
         const bool there = (uint64_t)row[u] - (uint64_t)a.first < (uint64_t)a.rows;
-        float x[8];
+        float x[E];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < E; ++i) {
             x[i] = in[u].get(i);
             if constexpr (TT == kI8) x[i] *= i < left[u] ? s0[u] : s1[u];
             x[i] = there ? x[i] * a.scale : 0.0f;
         }
-        Raw8<OT> o;
+        Raw<OT, E> o;
         o.set(x);
         o.store(a.out, token[u] * a.ld_out + col[u]);
     }
@@ -145,10 +150,15 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __res
     const uint32_t key = t < a.tokens ? key_of(a, t) : 0xFFFFFFFEu;
     const uint32_t blocks = (a.tokens + 63) / 64;
     uint32_t before = 0;
-    for (uint32_t b = wave; b < blocks; b += kRankWaves) {
+    auto key_at = [&](uint32_t b) {
         const uint32_t j = b * 64 + lane;
+        return b < blocks && j < a.tokens ? key_of(a, j) : 0xFFFFFFFFu;
+    };
+    uint32_t next = key_at(wave);
+    for (uint32_t b = wave; b < blocks; b += kRankWaves) {
         __builtin_amdgcn_wave_barrier();
-        keys[wave][lane] = j < a.tokens ? key_of(a, j) : 0xFFFFFFFFu;
+        keys[wave][lane] = next;
+        next = key_at(b + kRankWaves);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         const u32x4* other = reinterpret_cast<const u32x4*>(keys[wave]);
@@ -193,7 +203,7 @@ __device__ __forceinline__ uint64_t sort_item(const Ids& a, const uint64_t* __re
     else return in[t];
 }
 
-// counts[digit][tile]
+// counts[tile][digit]
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void k_digit_counts(Ids a, const uint64_t* __restrict__ in,
                                                                Pass p, uint32_t* __restrict__ counts) {
@@ -207,25 +217,25 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_counts(Ids a, const uint
             atomicAdd(&n[(uint32_t)(sort_item<FIRST>(a, in, t) >> (32 + p.shift)) & ((1u << p.bits) - 1)], 1u);
     }
     __syncthreads();
-    if (threadIdx.x < (1u << p.bits)) counts[threadIdx.x * p.tiles + blockIdx.x] = n[threadIdx.x];
+    if (threadIdx.x < (1u << p.bits)) counts[(uint64_t)blockIdx.x << p.bits | threadIdx.x] = n[threadIdx.x];
 }
 
 // Many tiles: each digit's counts to the number in earlier tiles, in place, and
 // its total; one wave a digit.
 __global__ __launch_bounds__(64) void k_digit_scan(Pass p, uint32_t* __restrict__ counts,
                                                    uint32_t* __restrict__ totals) {
-    uint32_t* row = counts + blockIdx.x * p.tiles;
+    uint32_t* row = counts + blockIdx.x;
     uint32_t sum = 0;
     for (uint32_t b = 0; b < p.tiles; b += 64) {
         const uint32_t i = b + threadIdx.x;
-        const uint32_t x = i < p.tiles ? row[i] : 0;
+        const uint32_t x = i < p.tiles ? row[(uint64_t)i << p.bits] : 0;
         uint32_t s = x;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const uint32_t y = __shfl_up(s, d);
             if ((int)threadIdx.x >= d) s += y;
         }
-        if (i < p.tiles) row[i] = sum + s - x;
+        if (i < p.tiles) row[(uint64_t)i << p.bits] = sum + s - x;
         sum += __shfl(s, 63);
     }
     if (threadIdx.x == 0) totals[blockIdx.x] = sum;
@@ -251,16 +261,21 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint6
     // the digit's share of earlier tiles, and its total
     uint32_t total = 0, earlier = 0;
     if (threadIdx.x < (1u << p.bits)) {
-        const uint32_t* row = counts + threadIdx.x * p.tiles;
+        const uint32_t* row = counts + threadIdx.x;
         if (p.tiles <= kDirectTiles) {
-            for (uint32_t b = 0; b < p.tiles; ++b) {
-                const uint32_t n = row[b];
-                total += n;
-                if (b < blockIdx.x) earlier += n;
+            for (uint32_t b = 0; b < p.tiles; b += 16) {
+                uint32_t n[16];               // loaded together
+#pragma unroll
+                for (uint32_t u = 0; u < 16; ++u) n[u] = b + u < p.tiles ? row[(b + u) << p.bits] : 0;
+#pragma unroll
+                for (uint32_t u = 0; u < 16; ++u) {
+                    total += n[u];
+                    earlier += b + u < blockIdx.x ? n[u] : 0;
+                }
             }
         } else {
             total = totals[threadIdx.x];
-            earlier = row[blockIdx.x];
+            earlier = row[(uint64_t)blockIdx.x << p.bits];
         }
     }
     if (threadIdx.x < kMaxDigits) scan[0][threadIdx.x] = total;
@@ -331,14 +346,14 @@ struct GradArgs {
     float scale;
 };
 
-// acc += `count` rows of 8 elements; row(j, base) gives the place of the j-th.
-template <int DT, class Row>
-__device__ __forceinline__ void add_rows(float (&acc)[8], uint32_t count, bool narrow, int dim, Row row) {
+// acc += `count` rows of E elements; row(j, base) gives the place of the j-th.
+template <int DT, int E, class Row>
+__device__ __forceinline__ void add_rows(float (&acc)[E], uint32_t count, bool narrow, int dim, Row row) {
     constexpr int kFlight = 8;                // loads in flight
     uint32_t j = 0;
     if (!narrow) {
         for (; j + kFlight <= count; j += kFlight) {
-            Raw8<DT> r[kFlight];
+            Raw<DT, E> r[kFlight];
 #pragma unroll
             for (int u = 0; u < kFlight; ++u) {
                 const void* base;
@@ -348,22 +363,22 @@ __device__ __forceinline__ void add_rows(float (&acc)[8], uint32_t count, bool n
 #pragma unroll
             for (int u = 0; u < kFlight; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += r[u].get(i);
+                for (int i = 0; i < E; ++i) acc[i] += r[u].get(i);
         }
         for (; j < count; ++j) {
-            Raw8<DT> r;
+            Raw<DT, E> r;
             const void* base;
             const int64_t at = row(j, base);
             r.template load<false>(base, at);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += r.get(i);
+            for (int i = 0; i < E; ++i) acc[i] += r.get(i);
         }
     } else {
         for (; j < count; ++j) {
             const void* base;
             const int64_t at = row(j, base);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < E; ++i)
                 if (i < dim) acc[i] += load1<DT>(base, at + i);
         }
     }
@@ -385,6 +400,7 @@ __device__ __forceinline__ uint32_t lower_bound(const uint64_t* __restrict__ s, 
 template <int DT, bool FIRST>
 __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t level, uint32_t lanes,
                                                          uint32_t start_blocks, Divisor pieces) {
+    constexpr int E = FIRST ? piece_elems<DT, DT>() : 4;
     uint32_t block = blockIdx.x;
     if constexpr (FIRST) {
         if (block < start_blocks) {
@@ -401,18 +417,18 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
     const uint32_t hi = lo + (1u << (kGroupLog * level)) - 1;
     const uint64_t key = a.sorted[lo] >> 32;
     if (key != a.sorted[hi] >> 32 || key >= (uint64_t)a.rows) return;
-    const bool narrow = a.dim < 8;
-    int64_t col = (int64_t)(lane - group * pieces.d) * 8;
-    if (!narrow && col > a.dim - 8) col = a.dim - 8;
-    float acc[8] = {};
+    const bool narrow = a.dim < E;
+    int64_t col = (int64_t)(lane - group * pieces.d) * E;
+    if (!narrow && col > a.dim - E) col = a.dim - E;
+    float acc[E] = {};
     if constexpr (FIRST) {
-        add_rows<DT>(acc, kGroup, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+        add_rows<DT, E>(acc, kGroup, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
             base = a.dy;
             return (int64_t)(uint32_t)a.sorted[lo + j] * a.ld_dy + col;
         });
     } else {
         const int64_t below = (int64_t)group << kGroupLog;
-        add_rows<ZPQ_F32>(acc, kGroup, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+        add_rows<ZPQ_F32, E>(acc, kGroup, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
             base = a.part[level - 2];
             return (below + j) * a.dim + col;
         });
@@ -421,9 +437,9 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
     if (narrow) {
         for (int i = 0; i < (int)a.dim; ++i) to[(int64_t)group * a.dim + i] = acc[i];
     } else {
-        Raw8<ZPQ_F32> o;
+        Raw<ZPQ_F32, E> o;
         o.set(acc);
-        o.store<false>(to, (int64_t)group * a.dim + col);
+        o.template store<false>(to, (int64_t)group * a.dim + col);
     }
 }
 
@@ -439,11 +455,12 @@ __device__ __forceinline__ T load_uniform(const T* p, int64_t i) {
 // UNIFORM: the same row in the whole wave.
 template <int DT, int OT, bool ADD, bool UNIFORM>
 __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t piece, uint32_t at, uint32_t e) {
-    const bool narrow = !UNIFORM && a.dim < 8;         // a wave's 64 pieces are more than one
-    int64_t col = (int64_t)piece * 8;
-    const int count = (int)(a.dim - col < 8 ? a.dim - col : 8);    // elements this lane writes
-    if (!narrow && count < 8) col = a.dim - 8;
-    float acc[8] = {};
+    constexpr int E = piece_elems<DT, OT>();
+    const bool narrow = !UNIFORM && a.dim < E;         // a wave's 64 pieces are more than one
+    int64_t col = (int64_t)piece * E;
+    const int count = (int)(a.dim - col < E ? a.dim - col : E);    // elements this lane writes
+    if (!narrow && count < E) col = a.dim - E;
+    float acc[E] = {};
 #pragma unroll 1
     while (at < e) {
         int level = a.levels;
@@ -455,7 +472,7 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
             // up to the next group that could be whole
             uint32_t stop = a.levels > 0 ? (at | (kGroup - 1)) + 1 : e;
             if (stop > e) stop = e;
-            add_rows<DT>(acc, stop - at, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+            add_rows<DT, E>(acc, stop - at, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
                 base = a.dy;
                 const uint64_t token = UNIFORM ? load_uniform(a.sorted, at + j) : a.sorted[at + j];
                 return (int64_t)(uint32_t)token * a.ld_dy + col;
@@ -471,7 +488,7 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
             }
             const int64_t g0 = at >> shift;
             const float* part = a.part[level - 1];
-            add_rows<ZPQ_F32>(acc, groups, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+            add_rows<ZPQ_F32, E>(acc, groups, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
                 base = part;
                 return (g0 + j) * a.dim + col;
             });
@@ -480,25 +497,25 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
     }
     const int64_t o = row * a.ld_grad + col;
     if (!narrow) {
-        Raw8<OT> old;
+        Raw<OT, E> old;
         if constexpr (ADD) old.load(a.grad, o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < E; ++i) {
             acc[i] *= a.scale;
             if constexpr (ADD) acc[i] = old.get(i) + acc[i];
         }
-        if (count == 8) {
-            Raw8<OT> out;
+        if (count == E) {
+            Raw<OT, E> out;
             out.set(acc);
             out.store(a.grad, o);
         } else {
 #pragma unroll
-            for (int i = 1; i < 8; ++i)
-                if (i >= 8 - count) store1<OT>(a.grad, o + i, acc[i]);
+            for (int i = 1; i < E; ++i)
+                if (i >= E - count) store1<OT>(a.grad, o + i, acc[i]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < E; ++i)
             if (i < count) {
                 float x = acc[i] * a.scale;
                 if constexpr (ADD) x = load1<OT>(a.grad, o + i) + x;
@@ -521,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first
         const int64_t row = first_row + r;
         const uint32_t at = load_uniform(a.starts, row), e = load_uniform(a.starts, row + 1);
         const uint32_t piece = (wave - r * pieces.d) * 64 + (threadIdx.x & 63u);
-        if ((ADD && at == e) || (int64_t)piece * 8 >= a.dim) return;
+        if ((ADD && at == e) || (int64_t)piece * piece_elems<DT, OT>() >= a.dim) return;
         row_sum<DT, OT, ADD, true>(a, row, piece, at, e);
     } else {
         if (lane >= lanes) return;
@@ -535,10 +552,23 @@ __global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first
 
 // ---------------------------------------------------------------------------
 // Host side.
+// Launches of at most 2^30 lanes: the division's range.
 template <int TT, int OT>
-void launch_lookup(const LookupArgs& a, hipStream_t st) {
-    const unsigned grid = (a.lanes + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL((k_lookup<TT, OT, 1>), dim3(grid), dim3(kThreads), 0, st, a);
+void launch_lookup(LookupArgs a, hipStream_t st) {
+    constexpr int E = piece_elems<TT, OT>();
+    const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
+    a.pieces = divisor(pieces);
+    const char* ids = static_cast<const char*>(a.ids);
+    char* out = static_cast<char*>(a.out);
+    const int64_t some = (1 << 30) / pieces;
+    for (int64_t t = 0; t < a.tokens; t += some) {
+        const int64_t n = a.tokens - t < some ? a.tokens - t : some;
+        a.ids = ids + t * a.id_bytes;
+        a.out = out + t * a.ld_out * elem_bytes<OT>();
+        a.lanes = (uint32_t)(n * pieces);
+        const unsigned grid = (a.lanes + kThreads - 1) / kThreads;
+        hipLaunchKernelGGL((k_lookup<TT, OT, 1>), dim3(grid), dim3(kThreads), 0, st, a);
+    }
 }
 template <int TT>
 void launch_lookup_o(const LookupArgs& a, int32_t out_dtype, hipStream_t st) {
@@ -564,26 +594,11 @@ zpq_status rows_ok(int64_t rows, int64_t tokens, int64_t dim, int64_t ld_a, int6
     return ZPQ_OK;
 }
 
-zpq_status lookup(const void* table, int32_t t_dtype, const float* scales, int32_t log_block, int64_t rows,
-                  int64_t dim, int64_t ld_table, const void* ids, int32_t id_bytes, int64_t tokens,
-                  int64_t first, float scale, void* out, int32_t out_dtype, int64_t ld_out,
-                  hipStream_t st) {
-    const uint32_t pieces = (uint32_t)((dim + 7) / 8);
-    LookupArgs a = {table, scales, ids, out, rows, dim, ld_table, first, ld_out, scale, id_bytes,
-                    log_block, 0, divisor(pieces)};
-    // launches of at most 2^30 lanes: the division's range
-    const int64_t some = (1 << 30) / pieces;
-    const int64_t ob = dtype_bytes(out_dtype);
-    for (int64_t t = 0; t < tokens; t += some) {
-        const int64_t n = tokens - t < some ? tokens - t : some;
-        a.ids = static_cast<const char*>(ids) + t * id_bytes;
-        a.out = static_cast<char*>(out) + t * ld_out * ob;
-        a.lanes = (uint32_t)(n * pieces);
-        if (t_dtype == ZPQ_F32) launch_lookup_o<ZPQ_F32>(a, out_dtype, st);
-        else if (t_dtype == ZPQ_F16) launch_lookup_o<ZPQ_F16>(a, out_dtype, st);
-        else if (t_dtype == ZPQ_BF16) launch_lookup_o<ZPQ_BF16>(a, out_dtype, st);
-        else launch_lookup_o<kI8>(a, out_dtype, st);
-    }
+zpq_status lookup(const LookupArgs& a, int32_t t_dtype, int32_t out_dtype, hipStream_t st) {
+    if (t_dtype == ZPQ_F32) launch_lookup_o<ZPQ_F32>(a, out_dtype, st);
+    else if (t_dtype == ZPQ_F16) launch_lookup_o<ZPQ_F16>(a, out_dtype, st);
+    else if (t_dtype == ZPQ_BF16) launch_lookup_o<ZPQ_BF16>(a, out_dtype, st);
+    else launch_lookup_o<kI8>(a, out_dtype, st);
     return after_launch();
 }
 
@@ -643,9 +658,10 @@ void sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* coun
 
 template <int DT>
 void launch_groups(const GradArgs& a, hipStream_t st) {
-    const uint32_t pieces = (uint32_t)((a.dim + 7) / 8);
     const uint32_t start_blocks = (uint32_t)(a.rows / kThreads + 1);
     for (int l = 1; l <= (a.levels > 0 ? a.levels : 1); ++l) {
+        const int E = l == 1 ? piece_elems<DT, DT>() : 4;
+        const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
         const uint32_t lanes = l <= a.levels ? (a.tokens >> (kGroupLog * l)) * pieces : 0;
         const unsigned blocks = lanes / kThreads + (lanes % kThreads != 0);
         if (l == 1)
@@ -658,7 +674,8 @@ void launch_groups(const GradArgs& a, hipStream_t st) {
 }
 template <int DT, int OT, bool ADD>
 void launch_rows(const GradArgs& a, hipStream_t st) {
-    const uint32_t pieces = (uint32_t)((a.dim + 7) / 8);
+    constexpr int E = piece_elems<DT, OT>();
+    const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
     const bool wide = pieces >= 33;
     const uint32_t per_row = wide ? (pieces + 63) / 64 : pieces;
     const int64_t some = (1 << (wide ? 24 : 30)) / per_row;       // rows a launch: at most 2^30 lanes
@@ -689,7 +706,7 @@ void launch_grad(const GradArgs& a, int32_t grad_dtype, bool add, hipStream_t st
 // bits, a launch's rows of pieces in 30.
 bool grad_sizes_ok(int64_t tokens, int64_t dim, int64_t rows) {
     return tokens >= 0 && tokens <= (1LL << 28) && dim >= 1 && dim <= (1 << 28) && rows >= 0 &&
-           rows <= (1LL << 27) && (tokens >> kGroupLog) * ((dim + 7) / 8) < (1LL << 31);
+           rows <= (1LL << 27) && (tokens >> kGroupLog) * ((dim + 3) / 4) < (1LL << 31);
 }
 
 }  // namespace
@@ -710,8 +727,9 @@ zpq_status zpq_embedding(const void* table, int32_t t_dtype, int64_t rows, int64
     const uint64_t on = span(tokens, dim, ld_out, ob);
     if (overlaps(out, on, table, span(rows, dim, ld_table, tb)) || overlaps(out, on, ids, tokens * id_bytes))
         return ZPQ_ERR_ALIAS;
-    return lookup(table, t_dtype, nullptr, 0, rows, dim, ld_table, ids, id_bytes, tokens, first, scale, out,
-                  out_dtype, ld_out, static_cast<hipStream_t>(stream));
+    return lookup(LookupArgs{table, nullptr, ids, out, tokens, rows, dim, ld_table, first, ld_out, scale, id_bytes, 0,
+                             0, {}},
+                  t_dtype, out_dtype, static_cast<hipStream_t>(stream));
 }
 
 zpq_status zpq_embedding_i8(const int8_t* codes, const float* scales, int64_t rows, int64_t dim,
@@ -732,8 +750,9 @@ zpq_status zpq_embedding_i8(const int8_t* codes, const float* scales, int64_t ro
     if (overlaps(out, on, codes, tn) || overlaps(out, on, scales, (tn + block - 1) / block * 4) ||
         overlaps(out, on, ids, tokens * id_bytes))
         return ZPQ_ERR_ALIAS;
-    return lookup(codes, kI8, scales, log_block, rows, dim, dim, ids, id_bytes, tokens, first, scale, out,
-                  out_dtype, ld_out, static_cast<hipStream_t>(stream));
+    return lookup(LookupArgs{codes, scales, ids, out, tokens, rows, dim, dim, first, ld_out, scale, id_bytes,
+                             log_block, 0, {}},
+                  kI8, out_dtype, static_cast<hipStream_t>(stream));
 }
 
 zpq_status zpq_embedding_grad_bytes(int64_t tokens, int64_t rows, int64_t dim, int64_t* bytes) {

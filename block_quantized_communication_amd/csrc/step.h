@@ -43,23 +43,33 @@ __device__ __forceinline__ void store1(void* base, int64_t i, float x) {
     else static_cast<__bf16*>(base)[i] = (__bf16)x;
 }
 
-// 8 consecutive elements as raw words: 16-byte accesses (8-byte ones for
-// INT8) at any byte address, which global memory allows in the unaligned access
-// mode that every HSA process runs in.  NT: non-temporal, for what is read or
-// written once.
+// E consecutive elements as raw words, accessed 4, 8 or 16 bytes at a time at any
+// byte address, which global memory allows in the unaligned access mode that
+// every HSA process runs in.  NT: non-temporal, for what is read or written once.
+// E * elem_bytes is at most 16 where speed matters: then one access of a wave
+// covers consecutive bytes.  (8 fp32 elements a lane, two 16-byte accesses that
+// each cover every other 16 bytes, ran the 32-bit optimizer step at 4.9 TB/s and an
+// fp32 read at 4.9 TB/s.)
+typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 
-template <int DT>
-struct Raw8 {
-    static constexpr int WORDS = 8 * elem_bytes<DT>() / 4;
+template <int DT, int E>
+struct Raw {
+    static_assert(E == 4 || E == 8, "4 or 8 elements");
+    static constexpr int WORDS = E * elem_bytes<DT>() / 4;
     uint32_t w[WORDS];
 
     template <bool NT = true>
     __device__ __forceinline__ void load(const void* base, int64_t i) {
         const char* p = static_cast<const char*>(base) + i * elem_bytes<DT>();
-        if constexpr (WORDS == 2) {
-            const u32x2 t = *reinterpret_cast<const u32x2_any*>(p);
+        if constexpr (WORDS == 1) {
+            const u32_any* q = reinterpret_cast<const u32_any*>(p);
+            if constexpr (NT) w[0] = __builtin_nontemporal_load(q); else w[0] = *q;
+        } else if constexpr (WORDS == 2) {
+            const u32x2_any* q = reinterpret_cast<const u32x2_any*>(p);
+            u32x2 t;
+            if constexpr (NT) t = __builtin_nontemporal_load(q); else t = *q;
             w[0] = t.x; w[1] = t.y;
         } else {
 #pragma unroll
@@ -71,34 +81,16 @@ struct Raw8 {
             }
         }
     }
-    __device__ __forceinline__ float get(int k) const {
-        if constexpr (DT == ZPQ_F32) return __uint_as_float(w[k]);
-        else if constexpr (DT == ZPQ_F16)
-            return (float)(__builtin_bit_cast(f16x2, w[k >> 1])[k & 1]);
-        else if constexpr (DT == ZPQ_BF16)
-            return __uint_as_float((k & 1) ? (w[k >> 1] & 0xFFFF0000u) : (w[k >> 1] << 16));
-        else return (float)(int8_t)(w[k >> 2] >> (8 * (k & 3)));
-    }
-    __device__ __forceinline__ void set(const float (&x)[8]) {
-        if constexpr (DT == ZPQ_F32) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(x[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const f32x2 f = {x[2 * k], x[2 * k + 1]};
-                if constexpr (DT == ZPQ_F16)
-                    w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
-                else
-                    w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
-            }
-        }
-    }
     template <bool NT = true>
     __device__ __forceinline__ void store(void* base, int64_t i) const {
         char* p = static_cast<char*>(base) + i * elem_bytes<DT>();
-        if constexpr (WORDS == 2) {
-            *reinterpret_cast<u32x2_any*>(p) = u32x2{w[0], w[1]};
+        if constexpr (WORDS == 1) {
+            u32_any* q = reinterpret_cast<u32_any*>(p);
+            if constexpr (NT) __builtin_nontemporal_store(w[0], q); else *q = w[0];
+        } else if constexpr (WORDS == 2) {
+            const u32x2 t = {w[0], w[1]};
+            u32x2_any* q = reinterpret_cast<u32x2_any*>(p);
+            if constexpr (NT) __builtin_nontemporal_store(t, q); else *q = t;
         } else {
 #pragma unroll
             for (int k = 0; k < WORDS / 4; ++k) {
@@ -107,6 +99,55 @@ struct Raw8 {
                 if constexpr (NT) __builtin_nontemporal_store(t, q); else *q = t;
             }
         }
+    }
+    __device__ __forceinline__ uint32_t byte(int k) const { return (w[k >> 2] >> (8 * (k & 3))) & 0xFFu; }
+    __device__ __forceinline__ float get(int k) const {
+        if constexpr (DT == ZPQ_F32) return __uint_as_float(w[k]);
+        else if constexpr (DT == ZPQ_F16)
+            return (float)(__builtin_bit_cast(f16x2, w[k >> 1])[k & 1]);
+        else if constexpr (DT == ZPQ_BF16)
+            return __uint_as_float((k & 1) ? (w[k >> 1] & 0xFFFF0000u) : (w[k >> 1] << 16));
+        else return (float)(int8_t)byte(k);
+    }
+    __device__ __forceinline__ void set(const float (&x)[E]) {
+        if constexpr (DT == ZPQ_F32) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) w[k] = __float_as_uint(x[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) {
+                const f32x2 f = {x[2 * k], x[2 * k + 1]};
+                if constexpr (DT == ZPQ_F16)
+                    w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+                else
+                    w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+            }
+        }
+    }
+    // the first `have` elements one by one (the rest as zeros; not written)
+    __device__ __forceinline__ void load_some(const void* base, int64_t i, int have) {
+        if constexpr (DT == kI8) {
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) w[k] = 0;
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (k < have)
+                    w[k >> 2] |= (uint32_t)static_cast<const uint8_t*>(base)[i + k] << (8 * (k & 3));
+        } else {
+            float x[E];
+#pragma unroll
+            for (int k = 0; k < E; ++k) x[k] = k < have ? load1<DT>(base, i + k) : 0.0f;
+            set(x);
+        }
+    }
+    __device__ __forceinline__ void store_some(void* base, int64_t i, int have) const {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (k < have) {
+                if constexpr (DT == kI8) static_cast<uint8_t*>(base)[i + k] = (uint8_t)byte(k);
+                else if constexpr (DT == ZPQ_F32) static_cast<uint32_t*>(base)[i + k] = w[k];
+                else static_cast<uint16_t*>(base)[i + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+            }
     }
 };
 
