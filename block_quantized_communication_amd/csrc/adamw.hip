@@ -150,21 +150,21 @@ __global__ __launch_bounds__(kThreads) void k_sumsq_join(const double* __restric
 // below bit 20.  ldexp moves the field, for any e, with one rounding where
 // the result is subnormal.
 
-// Maximum over the wave of unsigned values, as a scalar.
+// Maximum over the wave of unsigned values, as a scalar: within rows of 16 lanes
+// by lane permutes, then lane 15 to the next row and lane 31 to the upper half,
+// which leaves it in lane 63.
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = max(v, dpp<0xB1>(v));                 // quad_perm [1,0,3,2]
-    v = max(v, dpp<0x4E>(v));                 // quad_perm [2,3,0,1]
-    v = max(v, dpp<0x141>(v));                // row_half_mirror
-    v = max(v, dpp<0x140>(v));                // row_mirror: rows of 16 done
-    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
-    const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
-    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32);
-    const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
-    return max(max(a, b), max(c, d));
+    v = max_dpp<0xB1>(v);                     // quad_perm [1,0,3,2]
+    v = max_dpp<0x4E>(v);                     // quad_perm [2,3,0,1]
+    v = max_dpp<0x141>(v);                    // row_half_mirror
+    v = max_dpp<0x140>(v);                    // row_mirror
+    v = max_dpp<0x142>(v);                    // row_bcast:15
+    v = max_dpp<0x143>(v);                    // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // Exponent byte of a block from the bits of its largest magnitude: up to
@@ -174,30 +174,46 @@ __device__ __forceinline__ uint32_t block_exp(uint32_t amax) {
     return e < 1 ? 1 : e > 255 ? 255 : e;
 }
 
+// Value of byte i of w.
 template <int MOMENT>
-__device__ __forceinline__ float decode8(uint32_t c, uint32_t e) {
-    if constexpr (MOMENT == 1)
-        return __builtin_amdgcn_ldexpf(__uint_as_float((c & 0x7Fu) << 20 | (c & 0x80u) << 24),
-                                       (int)e - 15);
+__device__ __forceinline__ float decode8(uint32_t w, int i, uint32_t e) {
+    if constexpr (MOMENT == 1)                // the sign down to bit 31 and, masked off again, 27..30
+        return __builtin_amdgcn_ldexpf(
+            __uint_as_float((uint32_t)((int32_t)(w << (24 - 8 * i)) >> 4) & 0x87F00000u), (int)e - 15);
     else
-        return __builtin_amdgcn_ldexpf(__uint_as_float(c << 20), (int)e - 31);
+        return __builtin_amdgcn_ldexpf(
+            __uint_as_float((i < 3 ? w << (20 - 8 * i) : w >> 4) & 0x0FF00000u), (int)e - 31);
 }
 
-// `add` is what goes in below bit 20: a random number for states, half a step
-// (less one, plus the parity) for rounding to nearest even.
-template <int MOMENT>
-__device__ __forceinline__ uint32_t encode8(float x, uint32_t e, uint32_t add, bool nearest) {
-    const uint32_t b = __float_as_uint(__builtin_amdgcn_ldexpf(x, (MOMENT == 1 ? 15 : 31) - (int)e));
-    const uint32_t mag = b & 0x7FFFFFFFu;
-    if (nearest) add = 0x7FFFFu + ((mag >> 20) & 1u);
-    uint32_t c = (mag + add) >> 20;
-    if constexpr (MOMENT == 1) {
-        if (e == 255) return 0x7F;
-        return c | (b >> 31) << 7;
-    } else {
-        if (e == 255) return 0xFF;
-        return c == 0 && !nearest && x > 0.0f ? 1u : c;
+// Byte 3 of each of 4 words.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __builtin_amdgcn_perm(b, a, 0x0C0C0703u) | __builtin_amdgcn_perm(d, c, 0x07030C0Cu);
+}
+
+// Codes of 4 values of a block with exponent byte e.  add[i] is what goes in below
+// bit 20: a random number for states; NEAREST: half a step (less one, plus the
+// parity), for rounding to nearest even.
+template <int MOMENT, bool NEAREST>
+__device__ __forceinline__ uint32_t encode8(const float (&x)[4], uint32_t e, const uint32_t (&add)[4]) {
+    if (e == 255) return MOMENT == 1 ? 0x7F7F7F7Fu : 0xFFFFFFFFu;
+    uint32_t t[4];                            // the code in the top byte
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mag = __float_as_uint(
+            __builtin_amdgcn_ldexpf(__builtin_fabsf(x[i]), (MOMENT == 1 ? 15 : 31) - (int)e));
+        t[i] = (mag + (NEAREST ? 0x7FFFFu + ((mag >> 20) & 1u) : add[i])) << 4;
     }
+    if constexpr (MOMENT == 2 && !NEAREST) {  // a value above 0 does not become 0
+        if (__any(min(min(t[0], t[1]), min(t[2], t[3])) < 1u << 24)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = max(t[i], x[i] > 0.0f ? 1u << 24 : 0u);
+        }
+    }
+    uint32_t c = top_bytes(t[0], t[1], t[2], t[3]);
+    if constexpr (MOMENT == 1)
+        c |= top_bytes(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                       __float_as_uint(x[3])) & 0x80808080u;
+    return c;
 }
 
 // The random bits of element lo + 2^32 * hi for a key made of seed and step: a
@@ -217,7 +233,10 @@ inline uint32_t random_key(uint64_t seed, uint64_t step) {
 }
 
 // ---------------------------------------------------------------------------
-// The step.
+// The step.  The root and the quotient are the hardware's (1 ulp each; the IEEE
+// sequences took 25 of about 110 instructions an element in the 8-bit step,
+// which they bound): with eps >= 1e-30 the quotient's denominator is a normal
+// number, and a v below 2^-126 has a root of 0.
 struct StepArgs {
     double lr, grad_scale, max_norm;
     float b1, ob1, b2, ob2, eps, rbc2, rate;  // ob: 1 - b; rbc2: 1/sqrt(1 - b2^t); rate: lr/(1 - b1^t)
@@ -234,27 +253,31 @@ struct Part {
     Raw<GT, 4> g;
     Raw<ST, 4> m, v;
     uint32_t em, ev;
-    int64_t i0;
+    int64_t at;                               // of the part: a scalar
+    uint32_t lane;                            // this lane's first element in it
     int have;                                 // elements of this lane, 0 to 4
 
-    __device__ __forceinline__ void load(const PlanEntry& e, int64_t at) {
-        i0 = at + threadIdx.x * 4;
-        have = (int)(e.n - i0 < 0 ? 0 : e.n - i0 < 4 ? e.n - i0 : 4);
+    __device__ __forceinline__ void load(const PlanEntry& e, int64_t at_) {
+        at = at_;
+        lane = threadIdx.x * 4;
+        const int64_t left = e.n - at - kPart;                // past the part, or missing
+        have = left >= 0 ? 4 : (int)(left + kPart - lane);
+        have = have < 0 ? 0 : have > 4 ? 4 : have;
         em = ev = 1;
         if constexpr (BITS == 8) {
-            const int64_t b = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) + at / kStateBlock;
+            const int64_t b = at / kStateBlock + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
             if (b * kStateBlock < e.n) { em = e.me[b]; ev = e.ve[b]; }
         }
         if (have == 4) {
-            p.load(e.p, i0);
-            g.load(e.g, i0);
-            m.load(e.m, i0);
-            v.load(e.v, i0);
+            p.load(from<PT>(e.p, at), lane);
+            g.load(from<GT>(e.g, at), lane);
+            m.load(from<ST>(e.m, at), lane);
+            v.load(from<ST>(e.v, at), lane);
         } else {
-            p.load_some(e.p, i0, have);
-            g.load_some(e.g, i0, have);
-            m.load_some(e.m, i0, have);
-            v.load_some(e.v, i0, have);
+            p.load_some(e.p, at + lane, have);
+            g.load_some(e.g, at + lane, have);
+            m.load_some(e.m, at + lane, have);
+            v.load_some(e.v, at + lane, have);
         }
     }
 
@@ -267,14 +290,14 @@ struct Part {
                 m0 = m.get(i);
                 v0 = v.get(i);
             } else {
-                m0 = decode8<1>(m.byte(i), em);
-                v0 = decode8<2>(v.byte(i), ev);
+                m0 = decode8<1>(m.w[0], i, em);
+                v0 = decode8<2>(v.w[0], i, ev);
             }
             const float x = g.get(i) * c;
             mm[i] = m0 * a.b1 + x * a.ob1;
             vv[i] = v0 * a.b2 + (x * a.ob2) * x;
-            const float u = mm[i] / (__builtin_sqrtf(vv[i]) * a.rbc2 + a.eps);
-            pp[i] = p.get(i) * keep - u * a.rate;
+            const float den = __builtin_amdgcn_sqrtf(vv[i]) * a.rbc2 + a.eps;
+            pp[i] = p.get(i) * keep - mm[i] * __builtin_amdgcn_rcpf(den) * a.rate;
         }
         p.set(pp);
         if constexpr (BITS == 32) {
@@ -290,34 +313,41 @@ struct Part {
             }
             em = block_exp(wave_max(am));
             ev = block_exp(wave_max(av));
-            const uint64_t n0 = (uint64_t)(e.base + i0);
-            const uint32_t x0 = (uint32_t)n0 * kMulLo + (uint32_t)(n0 >> 32) * kMulHi + a.key;
-            m.w[0] = v.w[0] = 0;
+            // the wave's first element counts as a multiple of 256, so that none of its
+            // 256 carries into the upper 32 bits
+            const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+            const uint64_t n0 = (uint64_t)(e.base + at) + wave * kStateBlock;
+            const uint32_t x0 = (uint32_t)n0 * kMulLo + (uint32_t)(n0 >> 32) * kMulHi + a.key +
+                                (threadIdx.x & 63u) * 4 * kMulLo;
+            uint32_t rm[4], rv[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {     // base and i0 are multiples of 4: no carry within 4
+            for (int i = 0; i < 4; ++i) {
                 const uint32_t r = mix(x0 + (uint32_t)i * kMulLo);
-                m.w[0] |= encode8<1>(mm[i], em, ((r & 0xFFFFu) << 4) + 8, false) << (8 * i);
-                v.w[0] |= encode8<2>(vv[i], ev, ((r >> 16) << 4) + 8, false) << (8 * i);
+                rm[i] = (r << 4 & 0xFFFF0u) | 8u;
+                rv[i] = (r >> 12 & 0xFFFF0u) | 8u;
             }
+            m.w[0] = encode8<1, false>(mm, em, rm);
+            v.w[0] = encode8<2, false>(vv, ev, rv);
         }
         // out
         Raw<CT < 0 ? ZPQ_F16 : CT, 4> copy;
         if constexpr (CT >= 0) copy.set(pp);
         if (have == 4) {
-            p.store(e.p, i0);
-            if constexpr (CT >= 0) copy.store(e.copy, i0);
-            m.store(e.m, i0);
-            v.store(e.v, i0);
+            p.store(from<PT>(e.p, at), lane);
+            if constexpr (CT >= 0) copy.store(from<CT>(e.copy, at), lane);
+            m.store(from<ST>(e.m, at), lane);
+            v.store(from<ST>(e.v, at), lane);
         } else {
-            p.store_some(e.p, i0, have);
-            if constexpr (CT >= 0) copy.store_some(e.copy, i0, have);
-            m.store_some(e.m, i0, have);
-            v.store_some(e.v, i0, have);
+            p.store_some(e.p, at + lane, have);
+            if constexpr (CT >= 0) copy.store_some(e.copy, at + lane, have);
+            m.store_some(e.m, at + lane, have);
+            v.store_some(e.v, at + lane, have);
         }
         if constexpr (BITS == 8) {
             if ((threadIdx.x & 63) == 0 && have > 0) {
-                e.me[i0 / kStateBlock] = (uint8_t)em;
-                e.ve[i0 / kStateBlock] = (uint8_t)ev;
+                const int64_t b = (at + lane) / kStateBlock;
+                e.me[b] = (uint8_t)em;
+                e.ve[b] = (uint8_t)ev;
             }
         }
     }
@@ -379,7 +409,7 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(const uint8_t* __restrict_
             const int64_t i0 = at + u * kPart + threadIdx.x * 4;
             float x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = decode8<MOMENT>(r[u].byte(i), e[u]);
+            for (int i = 0; i < 4; ++i) x[i] = decode8<MOMENT>(r[u].w[0], i, e[u]);
             Raw<DT, 4> o;
             o.set(x);
             if (i0 + 4 <= n) o.store(y, i0);
@@ -398,14 +428,16 @@ __global__ __launch_bounds__(kThreads) void k_pack8(const void* __restrict__ x, 
         Raw<DT, 4> r;
         if (have == 4) r.load(x, i0);
         else r.load_some(x, i0, have);
+        float v[4];
         uint32_t a = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a = max(a, __float_as_uint(r.get(i)) & 0x7FFFFFFFu);
+        for (int i = 0; i < 4; ++i) {
+            v[i] = r.get(i);
+            a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        }
         const uint32_t e = block_exp(wave_max(a));
         Raw<kI8, 4> c;
-        c.w[0] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c.w[0] |= encode8<MOMENT>(r.get(i), e, 0, true) << (8 * i);
+        c.w[0] = encode8<MOMENT, true>(v, e, {});
         if (have == 4) c.store(codes, i0);
         else c.store_some(codes, i0, have);
         if ((threadIdx.x & 63) == 0 && have > 0) exps[i0 / kStateBlock] = (uint8_t)e;

@@ -43,6 +43,16 @@ __device__ __forceinline__ void store1(void* base, int64_t i, float x) {
     else static_cast<__bf16*>(base)[i] = (__bf16)x;
 }
 
+// Address of element i, for a scalar i: lanes then add 32-bit offsets.
+template <int DT>
+__device__ __forceinline__ const void* from(const void* base, int64_t i) {
+    return static_cast<const char*>(base) + i * elem_bytes<DT>();
+}
+template <int DT>
+__device__ __forceinline__ void* from(void* base, int64_t i) {
+    return static_cast<char*>(base) + i * elem_bytes<DT>();
+}
+
 // E consecutive elements as raw words, accessed 4, 8 or 16 bytes at a time at any
 // byte address, which global memory allows in the unaligned access mode that
 // every HSA process runs in.  NT: non-temporal, for what is read or written once.
