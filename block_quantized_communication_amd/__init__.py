@@ -27,6 +27,7 @@ Around the communication path (tensors need their element's alignment only):
 """
 import contextlib
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,7 +45,7 @@ EXPORTS = ("zpq_quant_i8", "zpq_dequant_i8", "zpq_quant_i8_tensor", "zpq_qgz_reo
            "zpq_embedding_grad_bytes", "zpq_embedding_grad")
 
 STATE_BLOCK = 256          # elements that share an exponent byte in 8-bit optimizer states
-SUMSQ_BYTES = 32768        # ZPQ_SUMSQ_BYTES
+LIST_FIXED_BYTES = 20736   # ZPQ_LIST_BYTES(0)
 
 
 class _List(ctypes.Structure):
@@ -98,7 +99,7 @@ def lib():
         L.zpq_qgz_dequant_reduce_requant_i4.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp, i32,
                                                         f32, vp]
         L.zpq_list_make.argtypes = [vp, vp, i32, i32, vp, i64, ctypes.POINTER(_List), vp]
-        L.zpq_grad_sumsq.argtypes = [ctypes.POINTER(_List), vp, i32, vp, i64, vp]
+        L.zpq_grad_sumsq.argtypes = [ctypes.POINTER(_List), vp, i32, vp]
         L.zpq_adamw_plan_make.argtypes = [ctypes.POINTER(_AdamwTensor), i32, i32, i32, i32, i32, vp,
                                           i64, ctypes.POINTER(_AdamwPlan), vp]
         L.zpq_adamw_step.argtypes = [ctypes.POINTER(_AdamwPlan), ctypes.POINTER(_AdamwHyper), vp, vp]
@@ -290,7 +291,18 @@ def abi_version():
 
 # ---------------------------------------------------------------------------
 # Around the communication path: optimizer step, gradient norm, embedding.
+#
+# The smallest of these calls take less time on the GPU than here, so the checks
+# are plain comparisons and pointers go to ctypes as integers.
 _here = contextlib.nullcontext()
+_codes = {}
+
+
+def _code(dt):
+    c = _codes.get(dt)
+    if c is None:
+        c = _codes[dt] = dtype_code(dt)
+    return c
 
 
 def _on(stream, device):
@@ -298,14 +310,14 @@ def _on(stream, device):
     the stream that it runs on, so that freeing it is ordered with its use."""
     torch = _torch()
     if stream is None:
-        s = torch.cuda.current_stream(device)
-        if device.index == torch.cuda.current_device():
-            return ctypes.c_void_p(s.cuda_stream), _here
-    else:
-        s = stream
-        if s.device != device:
-            raise ValueError(f"stream is on {s.device}, the tensors are on {device}")
-    return ctypes.c_void_p(s.cuda_stream), torch.cuda.stream(s)
+        index = device.index
+        raw = torch._C._cuda_getCurrentRawStream(index)
+        if index == torch.cuda.current_device():
+            return raw, _here
+        return raw, torch.cuda.stream(torch.cuda.current_stream(device))
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _one_device(tensors, name):
@@ -320,12 +332,14 @@ def _one_dtype(tensors, name):
     kinds = {t.dtype for t in tensors}
     if len(kinds) != 1:
         raise ValueError(f"{name}: need tensors of one type, got {sorted(map(str, kinds))}")
-    return dtype_code(next(iter(kinds)))
+    return _code(next(iter(kinds)))
 
 
 class TensorList:
     """Tensors of one type on one GPU, laid out once for grad_sumsq.  Keeps the
-    tensors; their storage must not be replaced (set_, resize_) meanwhile."""
+    tensors; their storage must not be replaced (set_, resize_) meanwhile.  The
+    list's table also holds the partial sums of the call that runs: one call at
+    a time, in stream order."""
 
     def __init__(self, tensors, stream=None):
         torch = _torch()
@@ -338,11 +352,12 @@ class TensorList:
         ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
         sizes = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
         st, ctx = _on(stream, self.device)
+        self._c = _List()
+        self._ref = ctypes.byref(self._c)
         with ctx:
-            self._table = torch.empty(n * 32 + 64, dtype=torch.uint8, device=self.device)
-            self._c = _List()
-            _check(lib().zpq_list_make(ptrs, sizes, n, dt, _ptr(self._table), self._table.numel(),
-                                       ctypes.byref(self._c), st), "zpq_list_make")
+            self._table = torch.empty(n * 32 + LIST_FIXED_BYTES, dtype=torch.uint8, device=self.device)
+            _check(lib().zpq_list_make(ptrs, sizes, n, dt, self._table.data_ptr(), self._table.numel(),
+                                       self._ref, st), "zpq_list_make")
 
 
 def grad_sumsq(tensors, out=None, accumulate=False, stream=None):
@@ -350,16 +365,15 @@ def grad_sumsq(tensors, out=None, accumulate=False, stream=None):
     accumulate: several lists, one norm).  tensors: a TensorList, or tensors."""
     torch = _torch()
     tl = tensors if isinstance(tensors, TensorList) else TensorList(tensors, stream=stream)
-    if accumulate and out is None:
-        raise ValueError("accumulate needs out")
     st, ctx = _on(stream, tl.device)
     with ctx:
-        if out is None:
+        if out is not None:
+            _need(out, torch.float64, 1, "out", tl.device)
+        elif accumulate:
+            raise ValueError("accumulate needs out")
+        else:
             out = torch.empty(1, dtype=torch.float64, device=tl.device)
-        _need(out, torch.float64, 1, "out", tl.device)
-        ws = torch.empty(SUMSQ_BYTES, dtype=torch.uint8, device=tl.device)
-        _check(lib().zpq_grad_sumsq(ctypes.byref(tl._c), _ptr(out), int(accumulate), _ptr(ws),
-                                    SUMSQ_BYTES, st), "zpq_grad_sumsq")
+        _check(lib().zpq_grad_sumsq(tl._ref, out.data_ptr(), accumulate, st), "zpq_grad_sumsq")
     return out
 
 
@@ -457,9 +471,9 @@ class AdamW:
         plan = _AdamwPlan()
         with ctx:
             _check(lib().zpq_adamw_plan_make(rows, count, self._pd, gd, self._cd, self.state_bits,
-                                             _ptr(self._table), self._table.numel(), ctypes.byref(plan), st),
+                                             self._table.data_ptr(), self._table.numel(), ctypes.byref(plan), st),
                    "zpq_adamw_plan_make")
-            self._plan, self.grads = plan, grads
+            self._plan, self._ref, self.grads = plan, ctypes.byref(plan), grads
             self._list = TensorList(grads, stream=stream)
 
     def grad_sumsq(self, out=None, accumulate=False, stream=None):
@@ -471,16 +485,20 @@ class AdamW:
         squared norm of the unscaled gradients over all ranks; where it is not
         finite nothing changes.  max_norm: clip the scaled gradients to it
         (needs sumsq)."""
+        norm = None
         if sumsq is not None:
             _need(sumsq, _torch().float64, 1, "sumsq", self.device)
+            norm = sumsq.data_ptr()
         elif max_norm is not None:
             raise ValueError("max_norm needs sumsq")
         h = _AdamwHyper(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, grad_scale,
-                        float("inf") if max_norm is None else max_norm, step, self.seed)
+                        _INF if max_norm is None else max_norm, step, self.seed)
         st, ctx = _on(stream, self.device)
         with ctx:
-            _check(lib().zpq_adamw_step(ctypes.byref(self._plan), ctypes.byref(h), _ptr(sumsq), st),
-                   "zpq_adamw_step")
+            _check(lib().zpq_adamw_step(self._ref, ctypes.byref(h), norm, st), "zpq_adamw_step")
+
+
+_INF = float("inf")
 
 
 def state8_unpack(codes, exps, moment, dtype=None, out=None, stream=None):
@@ -494,9 +512,10 @@ def state8_unpack(codes, exps, moment, dtype=None, out=None, stream=None):
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=dtype or torch.float32, device=dev)
-        _need(out, out.dtype, n, "out", dev)
-        _check(lib().zpq_state8_unpack(_ptr(codes), _ptr(exps), n, moment, _ptr(out),
-                                       dtype_code(out.dtype), st), "zpq_state8_unpack")
+        else:
+            _need(out, out.dtype, n, "out", dev)
+        _check(lib().zpq_state8_unpack(codes.data_ptr(), exps.data_ptr(), n, moment, out.data_ptr(),
+                                       _code(out.dtype), st), "zpq_state8_unpack")
     return out
 
 
@@ -513,40 +532,41 @@ def state8_pack(x, moment, out=None, stream=None):
         codes, exps = out
         _need(codes, torch.uint8, n, "codes", dev)
         _need(exps, torch.uint8, -(-n // STATE_BLOCK), "exps", dev)
-        _check(lib().zpq_state8_pack(_ptr(x), dtype_code(x.dtype), n, moment, _ptr(codes), _ptr(exps),
-                                     st), "zpq_state8_pack")
+        _check(lib().zpq_state8_pack(x.data_ptr(), _code(x.dtype), n, moment, codes.data_ptr(),
+                                     exps.data_ptr(), st), "zpq_state8_pack")
     return codes, exps
 
 
 def _ids(ids):
     torch = _torch()
     dev = _gpu(ids, "ids")
-    if ids.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"ids: need int32 or int64, got {ids.dtype}")
-    return dev, ids.element_size()
+    if ids.dtype == torch.int64:
+        return dev, 8
+    if ids.dtype == torch.int32:
+        return dev, 4
+    raise ValueError(f"ids: need int32 or int64, got {ids.dtype}")
 
 
 def _rows(t, name, device, rows=None, dim=None):
     """t as rows: a 2-D tensor on `device` whose rows are contiguous (they may
     lie further apart); returns the distance."""
-    if not t.is_cuda or t.device != device or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name}: need a 2-D tensor on {device} with contiguous rows, got "
                          f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
-    if (rows is not None and t.shape[0] != rows) or (dim is not None and t.shape[1] != dim):
+    n, d = t.shape
+    if (rows is not None and n != rows) or (dim is not None and d != dim):
         raise ValueError(f"{name}: need {rows} x {dim}, got {tuple(t.shape)}")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if ld < t.shape[1]:
+    ld = t.stride(0) if n > 1 else d
+    if ld < d:
         raise ValueError(f"{name}: rows overlap (strides {tuple(t.stride())})")
     return ld
 
 
 def _lookup_out(ids, dim, out, dtype, dev):
-    """(out as given to the caller, out as rows)."""
-    torch = _torch()
+    """(output, distance of its rows)."""
     if out is None:
-        out = torch.empty(*ids.shape, dim, dtype=dtype, device=dev)
-        return out, out.view(-1, dim) if out.numel() else out.reshape(ids.numel(), dim)
-    return out, out if out.dim() == 2 else out.view(-1, out.shape[-1])
+        return _torch().empty(ids.shape + (dim,), dtype=dtype, device=dev), dim
+    return out, _rows(out if out.dim() == 2 else out.view(-1, out.shape[-1]), "out", dev, ids.numel(), dim)
 
 
 def embedding(ids, table, scale=1.0, first=0, out_dtype=None, out=None, stream=None):
@@ -558,11 +578,10 @@ def embedding(ids, table, scale=1.0, first=0, out_dtype=None, out=None, stream=N
     rows, dim = table.shape
     st, ctx = _on(stream, dev)
     with ctx:
-        out, flat = _lookup_out(ids, dim, out, out_dtype or table.dtype, dev)
-        lo = _rows(flat, "out", dev, ids.numel(), dim)
-        _check(lib().zpq_embedding(_ptr(table), dtype_code(table.dtype), rows, dim, ld, _ptr(ids), ib,
-                                   ids.numel(), first, ctypes.c_float(scale), _ptr(flat),
-                                   dtype_code(flat.dtype), lo, st), "zpq_embedding")
+        out, lo = _lookup_out(ids, dim, out, out_dtype or table.dtype, dev)
+        _check(lib().zpq_embedding(table.data_ptr(), _code(table.dtype), rows, dim, ld, ids.data_ptr(), ib,
+                                   ids.numel(), first, scale, out.data_ptr(), _code(out.dtype), lo, st),
+               "zpq_embedding")
     return out
 
 
@@ -581,12 +600,18 @@ def embedding_i8(ids, codes, scales, rows, dim, block=256, scale=1.0, first=0, o
                          f"{scales.numel()} of {scales.dtype}")
     st, ctx = _on(stream, dev)
     with ctx:
-        out, flat = _lookup_out(ids, dim, out, out_dtype or torch.float16, dev)
-        lo = _rows(flat, "out", dev, ids.numel(), dim)
-        _check(lib().zpq_embedding_i8(_ptr(codes), _ptr(scales), rows, dim, block, _ptr(ids), ib,
-                                      ids.numel(), first, ctypes.c_float(scale), _ptr(flat),
-                                      dtype_code(flat.dtype), lo, st), "zpq_embedding_i8")
+        out, lo = _lookup_out(ids, dim, out, out_dtype or torch.float16, dev)
+        _check(lib().zpq_embedding_i8(codes.data_ptr(), scales.data_ptr(), rows, dim, block, ids.data_ptr(), ib,
+                                      ids.numel(), first, scale, out.data_ptr(), _code(out.dtype), lo, st),
+               "zpq_embedding_i8")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _grad_bytes(tokens, rows, dim):
+    need = ctypes.c_int64()
+    _check(lib().zpq_embedding_grad_bytes(tokens, rows, dim, ctypes.byref(need)), "zpq_embedding_grad_bytes")
+    return need.value
 
 
 def embedding_grad(ids, dy, rows, scale=1.0, first=0, padding=None, out_dtype=None, out=None,
@@ -600,21 +625,20 @@ def embedding_grad(ids, dy, rows, scale=1.0, first=0, padding=None, out_dtype=No
     if dy.dim() != 2:
         _gpu(dy, "dy", dev)
         dy = dy.view(-1, dy.shape[-1])
-    flat = dy
-    n, dim = ids.numel(), flat.shape[1]
-    ld = _rows(flat, "dy", dev, n, dim)
-    if accumulate and out is None:
-        raise ValueError("accumulate needs out")
-    need = ctypes.c_int64()
-    _check(lib().zpq_embedding_grad_bytes(n, rows, dim, ctypes.byref(need)), "zpq_embedding_grad_bytes")
+    n, dim = ids.numel(), dy.shape[1]
+    ld = _rows(dy, "dy", dev, n, dim)
+    need = _grad_bytes(n, rows, dim)
     st, ctx = _on(stream, dev)
     with ctx:
-        if out is None:
-            out = torch.empty(rows, dim, dtype=out_dtype or dy.dtype, device=dev)
-        lo = _rows(out, "out", dev, rows, dim)
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        _check(lib().zpq_embedding_grad(_ptr(flat), dtype_code(flat.dtype), ld, _ptr(ids), ib, n, first,
-                                        first - 1 if padding is None else padding, rows, dim,
-                                        ctypes.c_float(scale), _ptr(out), dtype_code(out.dtype), lo,
-                                        int(accumulate), _ptr(ws), need.value, st), "zpq_embedding_grad")
+        if out is not None:
+            lo = _rows(out, "out", dev, rows, dim)
+        elif accumulate:
+            raise ValueError("accumulate needs out")
+        else:
+            out, lo = torch.empty((rows, dim), dtype=out_dtype or dy.dtype, device=dev), dim
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib().zpq_embedding_grad(dy.data_ptr(), _code(dy.dtype), ld, ids.data_ptr(), ib, n, first,
+                                        first - 1 if padding is None else padding, rows, dim, scale,
+                                        out.data_ptr(), _code(out.dtype), lo, accumulate, ws.data_ptr(), need,
+                                        st), "zpq_embedding_grad")
     return out

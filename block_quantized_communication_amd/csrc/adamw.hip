@@ -8,6 +8,8 @@
 // tensor by one or two 64-lane looks (find_start).
 #include <math.h>
 
+#include <atomic>
+
 #include "step.h"
 
 namespace {
@@ -34,7 +36,17 @@ struct PlanEntry {
     int64_t base;                             // first random number
     double decay;
 };
-static_assert(sizeof(ListEntry) + 4 <= 32 && sizeof(PlanEntry) + 4 <= 128, "ZPQ_*_BYTES");
+// A list's table: partial sums, counts of workgroups that are done (0 between
+// calls; each on a cache line of its own), entries, starts.  A plan's: entries,
+// starts.
+constexpr int kSumParts = 2048, kSumGroup = 32, kSumGroups = kSumParts / kSumGroup;
+struct Count { uint32_t n, unused[15]; };
+struct ListHead {
+    unsigned long long part[kSumParts];       // bits of binary64
+    Count group[kSumGroups], all;
+};
+static_assert(sizeof(ListHead) + 64 <= ZPQ_LIST_BYTES(0) && sizeof(ListEntry) + 4 <= 32 &&
+              sizeof(PlanEntry) + 4 <= 128, "ZPQ_*_BYTES");
 
 template <class E, int N>
 struct Fill {
@@ -50,8 +62,9 @@ static_assert(sizeof(Fill<ListEntry, kFillList>) < 3800 && sizeof(Fill<PlanEntry
 template <class E, int N>
 __global__ __launch_bounds__(128) void k_fill(Fill<E, N> f, int32_t first, int32_t count, int32_t all,
                                               E* __restrict__ entries, uint32_t* __restrict__ starts,
-                                              uint32_t total) {
+                                              uint32_t total, ListHead* __restrict__ head) {
     const int i = threadIdx.x;
+    if (head != nullptr && i <= kSumGroups) (i < kSumGroups ? head->group[i] : head->all).n = 0;
     if (i < count) {
         entries[first + i] = f.entry[i];
         starts[first + i] = f.start[i];
@@ -60,8 +73,12 @@ __global__ __launch_bounds__(128) void k_fill(Fill<E, N> f, int32_t first, int32
 }
 
 template <class E>
-uint32_t* starts_of(void* table, int32_t count) {
-    return reinterpret_cast<uint32_t*>(static_cast<E*>(table) + count);
+uint32_t* starts_of(E* entries, int32_t count) {
+    return reinterpret_cast<uint32_t*>(entries + count);
+}
+inline PlanEntry* plan_entries(void* table) { return static_cast<PlanEntry*>(table); }
+inline ListEntry* list_entries(void* table) {
+    return reinterpret_cast<ListEntry*>(static_cast<ListHead*>(table) + 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -72,11 +89,10 @@ uint32_t* starts_of(void* table, int32_t count) {
 // then followed.
 template <int DT> constexpr int kSumEach = DT == ZPQ_F32 ? 4 : 8;       // elements a lane
 constexpr int kSumChunk = 8192;               // elements of a workgroup's share
-constexpr int kSumParts = 4096;               // ZPQ_SUMSQ_BYTES / 8
-static_assert(kSumParts * 8 == ZPQ_SUMSQ_BYTES, "workspace");
 
 __device__ __forceinline__ double wg_sum(double x) {
     __shared__ double part[kThreads / 64];
+    __syncthreads();                          // an earlier sum's reads
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
@@ -87,11 +103,18 @@ __device__ __forceinline__ double wg_sum(double x) {
     return s;
 }
 
+// Counts the caller; true for the last of n, which leaves the count at 0.
+__device__ __forceinline__ bool count_to(uint32_t* count, uint32_t n) {
+    if (__hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != n - 1) return false;
+    (void)__hip_atomic_exchange(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict__ entries,
                                                     const uint32_t* __restrict__ starts,
-                                                    int32_t count, uint32_t chunks,
-                                                    double* __restrict__ part) {
+                                                    int32_t count, uint32_t chunks, ListHead* head,
+                                                    int32_t accumulate, double* out) {
     const uint32_t k0 = (uint32_t)((uint64_t)chunks * blockIdx.x / gridDim.x);
     const uint32_t k1 = (uint32_t)((uint64_t)chunks * (blockIdx.x + 1) / gridDim.x);
     double s[4] = {0.0, 0.0, 0.0, 0.0};
@@ -121,26 +144,45 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
         }
     }
     const double sum = wg_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (threadIdx.x == 0) part[blockIdx.x] = sum;
-}
-
-__global__ __launch_bounds__(kThreads) void k_sumsq_join(const double* __restrict__ part,
-                                                         int32_t parts, int32_t accumulate,
-                                                         double* __restrict__ out) {
-    double s = 0.0;
-    for (int b = 0; b < parts; b += 8 * kThreads) {
-        double x[8];                          // loaded together
+    // The workgroup that finishes last adds the partial sums, always in the same
+    // order.  Sums and counts are touched by read-modify-writes at agent scope only: these
+    // are carried out where all XCDs' accesses meet, and one whose old value has come
+    // back is done.  So a workgroup counts itself (waiting for its exchange) after
+    // its sum can be read by all, and the one that counts to the end reads every sum.
+    // Counting is in groups of 32, then the groups: 2048 additions to one word took 12 us.
+    // (A release and an acquire would write back and invalidate the L2 for each
+    // workgroup: 107 us for 50 M elements, against 18 without the joining.)
+    __shared__ bool last;
+    if (threadIdx.x == 0) {
+        unsigned long long old = __hip_atomic_exchange(&head->part[blockIdx.x], __double_as_longlong(sum),
+                                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" : "+v"(old) : : "memory");
+        const uint32_t g = blockIdx.x / kSumGroup, groups = (gridDim.x + kSumGroup - 1) / kSumGroup;
+        const uint32_t members = g + 1 < groups ? kSumGroup : gridDim.x - g * kSumGroup;
+        last = count_to(&head->group[g].n, members) && count_to(&head->all.n, groups);
+    }
+    __syncthreads();
+    if (!last) return;
+    double all = 0.0;
+    for (uint32_t b = 0; b < gridDim.x; b += 8 * kThreads) {
+        unsigned long long x[8] = {};         // fetched together
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int i = b + u * kThreads + threadIdx.x;
-            x[u] = i < parts ? part[i] : 0.0;
+            const uint32_t i = b + u * kThreads + threadIdx.x;
+            if (i < gridDim.x)
+                x[u] = __hip_atomic_exchange(&head->part[i], 0ull, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) s += x[u];
+        for (int u = 0; u < 8; ++u) all += __longlong_as_double((long long)x[u]);
     }
-    s = wg_sum(s);
-    if (threadIdx.x == 0) out[0] = accumulate ? out[0] + s : s;
+    all = wg_sum(all);
+    if (threadIdx.x == 0) {
+        out[0] = accumulate ? out[0] + all : all;
+    }
 }
+
+__global__ void k_zero(double* out) { out[0] = 0.0; }
 
 // ---------------------------------------------------------------------------
 // 8-bit states.  A state value is a binary32 pattern whose exponent field has
@@ -385,35 +427,38 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict_
 }
 
 // ---------------------------------------------------------------------------
-// 8-bit states to floats and back, 4 elements a lane: a wave holds a block.
-constexpr int kConvParts = 4;
+// 8-bit states to floats and back.  Floats are written 16 bytes a lane.
+constexpr int kConvParts = 2;
+template <int DT> constexpr int kConvEach = DT == ZPQ_F32 ? 4 : 8;
 template <int DT, int MOMENT>
 __global__ __launch_bounds__(kThreads) void k_unpack8(const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ exps, int64_t n,
                                                       void* __restrict__ y) {
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    constexpr int64_t kAll = (int64_t)kPart * kConvParts;
+    constexpr int E = kConvEach<DT>;
+    constexpr int64_t kAll = (int64_t)kThreads * E * kConvParts;
     for (int64_t at = blockIdx.x * kAll; at < n; at += gridDim.x * kAll) {
-        Raw<kI8, 4> r[kConvParts];
+        Raw<kI8, E> r[kConvParts];
         uint32_t e[kConvParts];
+        int have[kConvParts];
 #pragma unroll
         for (int u = 0; u < kConvParts; ++u) {
-            const int64_t first = at + u * kPart, i0 = first + threadIdx.x * 4;
-            const int64_t b = first / kStateBlock + wave;
-            e[u] = b * kStateBlock < n ? exps[b] : 1;
-            if (i0 + 4 <= n) r[u].load(codes, i0);
-            else r[u].load_some(codes, i0, (int)(n - i0 < 0 ? 0 : n - i0));
+            const uint32_t lane = (u * kThreads + threadIdx.x) * E;
+            const int64_t left = n - at - lane;
+            have[u] = left >= E ? E : left > 0 ? (int)left : 0;
+            e[u] = have[u] > 0 ? (exps + at / kStateBlock)[lane / kStateBlock] : 1;
+            if (have[u] == E) r[u].load(codes + at, lane);
+            else r[u].load_some(codes + at, lane, have[u]);
         }
 #pragma unroll
         for (int u = 0; u < kConvParts; ++u) {
-            const int64_t i0 = at + u * kPart + threadIdx.x * 4;
-            float x[4];
+            const uint32_t lane = (u * kThreads + threadIdx.x) * E;
+            float x[E];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = decode8<MOMENT>(r[u].w[0], i, e[u]);
-            Raw<DT, 4> o;
+            for (int i = 0; i < E; ++i) x[i] = decode8<MOMENT>(r[u].w[i >> 2], i & 3, e[u]);
+            Raw<DT, E> o;
             o.set(x);
-            if (i0 + 4 <= n) o.store(y, i0);
-            else o.store_some(y, i0, (int)(n - i0 < 0 ? 0 : n - i0));
+            if (have[u] == E) o.store(from<DT>(y, at), lane);
+            else o.store_some(from<DT>(y, at), lane, have[u]);
         }
     }
 }
@@ -446,11 +491,18 @@ __global__ __launch_bounds__(kThreads) void k_pack8(const void* __restrict__ x, 
 
 // ---------------------------------------------------------------------------
 // Host side.
+// Compute units of the current device, cached per device (threads may race to
+// fill an entry, with the same value).
 inline unsigned cu_count() {
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-        return 256;
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+            n = 256;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
     return (unsigned)n;
 }
 
@@ -464,7 +516,7 @@ bool list_ok(const zpq_list* l) {
 template <int PT, int GT, int CT, int BITS>
 void launch_adamw(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
     hipLaunchKernelGGL((k_adamw<PT, GT, CT, BITS>), dim3(grid_of(q->chunks)), dim3(kThreads), 0, st,
-                       static_cast<const PlanEntry*>(q->table), starts_of<PlanEntry>(q->table, q->count),
+                       plan_entries(q->table), starts_of(plan_entries(q->table), q->count),
                        q->count, (uint32_t)q->chunks, q->chunk_elems, a, sumsq);
 }
 template <int PT, int GT, int BITS>
@@ -493,7 +545,8 @@ bool finite_at_least(double x, double least) { return x >= least && x <= 1.79769
 template <int DT>
 void launch_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t moment,
                    void* y, hipStream_t st) {
-    const dim3 grid(grid_of((n + kPart * kConvParts - 1) / (kPart * kConvParts)));
+    constexpr int64_t kAll = (int64_t)kThreads * kConvEach<DT> * kConvParts;
+    const dim3 grid(grid_of((n + kAll - 1) / kAll));
     if (moment == 1)
         hipLaunchKernelGGL((k_unpack8<DT, 1>), grid, dim3(kThreads), 0, st, codes, exps, n, y);
     else
@@ -549,7 +602,7 @@ zpq_status zpq_list_make(const void* const* ptrs, const int64_t* sizes, int32_t 
     }
     if (chunks > 0x7FFFFFFF) return ZPQ_ERR_SIZE;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    ListEntry* entries = static_cast<ListEntry*>(table);
+    ListEntry* entries = list_entries(table);
     int64_t start = 0;
     for (int32_t first = 0; first < count; first += kFillList) {
         Fill<ListEntry, kFillList> f = {};
@@ -560,42 +613,38 @@ zpq_status zpq_list_make(const void* const* ptrs, const int64_t* sizes, int32_t 
             start += (sizes[first + i] + kSumChunk - 1) / kSumChunk;
         }
         hipLaunchKernelGGL((k_fill<ListEntry, kFillList>), dim3(1), dim3(128), 0, st, f, first, some, count,
-                           entries, starts_of<ListEntry>(table, count), (uint32_t)chunks);
+                           entries, starts_of(entries, count), (uint32_t)chunks, static_cast<ListHead*>(table));
     }
     *list = zpq_list{table, elems, chunks, count, dtype};
     return count > 0 ? after_launch() : ZPQ_OK;
 }
 
-zpq_status zpq_grad_sumsq(const zpq_list* list, double* out, int32_t accumulate, void* workspace,
-                          int64_t workspace_bytes, zpq_stream stream) {
+zpq_status zpq_grad_sumsq(const zpq_list* list, double* out, int32_t accumulate, zpq_stream stream) {
     if (!list_ok(list)) return list ? ZPQ_ERR_ARG : ZPQ_ERR_NULL;
-    if (!out || !workspace) return ZPQ_ERR_NULL;
-    if (workspace_bytes < ZPQ_SUMSQ_BYTES) return ZPQ_ERR_SIZE;
-    if (!aligned(out, 8) || !aligned(workspace, 16)) return ZPQ_ERR_ALIGN;
-    if (overlaps(out, 8, workspace, ZPQ_SUMSQ_BYTES) ||
-        overlaps(out, 8, list->table, ZPQ_LIST_BYTES(list->count)) ||
-        overlaps(workspace, ZPQ_SUMSQ_BYTES, list->table, ZPQ_LIST_BYTES(list->count)))
-        return ZPQ_ERR_ALIAS;
+    if (!out) return ZPQ_ERR_NULL;
+    if (!aligned(out, 8)) return ZPQ_ERR_ALIGN;
+    if (overlaps(out, 8, list->table, ZPQ_LIST_BYTES(list->count))) return ZPQ_ERR_ALIAS;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    double* part = static_cast<double*>(workspace);
+    if (list->chunks == 0) {
+        if (!accumulate) hipLaunchKernelGGL(k_zero, dim3(1), dim3(1), 0, st, out);
+        return after_launch();
+    }
     int64_t parts = (int64_t)cu_count() * 8;
     if (parts > kSumParts) parts = kSumParts;
     if (parts > list->chunks) parts = list->chunks;
-    if (parts > 0) {
-        const ListEntry* e = static_cast<const ListEntry*>(list->table);
-        const uint32_t* s = starts_of<ListEntry>(list->table, list->count);
-        const dim3 grid((unsigned)parts);
-        if (list->dtype == ZPQ_F32)
-            hipLaunchKernelGGL(k_sumsq<ZPQ_F32>, grid, dim3(kThreads), 0, st, e, s, list->count,
-                               (uint32_t)list->chunks, part);
-        else if (list->dtype == ZPQ_F16)
-            hipLaunchKernelGGL(k_sumsq<ZPQ_F16>, grid, dim3(kThreads), 0, st, e, s, list->count,
-                               (uint32_t)list->chunks, part);
-        else
-            hipLaunchKernelGGL(k_sumsq<ZPQ_BF16>, grid, dim3(kThreads), 0, st, e, s, list->count,
-                               (uint32_t)list->chunks, part);
-    }
-    hipLaunchKernelGGL(k_sumsq_join, dim3(1), dim3(kThreads), 0, st, part, (int32_t)parts, accumulate, out);
+    ListEntry* e = list_entries(list->table);
+    const uint32_t* s = starts_of(e, list->count);
+    ListHead* head = static_cast<ListHead*>(list->table);
+    const dim3 grid((unsigned)parts);
+    if (list->dtype == ZPQ_F32)
+        hipLaunchKernelGGL(k_sumsq<ZPQ_F32>, grid, dim3(kThreads), 0, st, e, s, list->count,
+                           (uint32_t)list->chunks, head, accumulate, out);
+    else if (list->dtype == ZPQ_F16)
+        hipLaunchKernelGGL(k_sumsq<ZPQ_F16>, grid, dim3(kThreads), 0, st, e, s, list->count,
+                           (uint32_t)list->chunks, head, accumulate, out);
+    else
+        hipLaunchKernelGGL(k_sumsq<ZPQ_BF16>, grid, dim3(kThreads), 0, st, e, s, list->count,
+                           (uint32_t)list->chunks, head, accumulate, out);
     return after_launch();
 }
 
@@ -640,7 +689,7 @@ zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, i
     int64_t chunks = tiles;
     if (chunks > 0x7FFFFFFF) return ZPQ_ERR_SIZE;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    PlanEntry* entries = static_cast<PlanEntry*>(table);
+    PlanEntry* entries = plan_entries(table);
     int64_t start = 0, base = 0;
     for (int32_t first = 0; first < count; first += kFillPlan) {
         Fill<PlanEntry, kFillPlan> f = {};
@@ -654,7 +703,7 @@ zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, i
             base += (t.n + kStateBlock - 1) / kStateBlock * kStateBlock;
         }
         hipLaunchKernelGGL((k_fill<PlanEntry, kFillPlan>), dim3(1), dim3(128), 0, st, f, first, some, count,
-                           entries, starts_of<PlanEntry>(table, count), (uint32_t)chunks);
+                           entries, starts_of(entries, count), (uint32_t)chunks, (ListHead*)nullptr);
     }
     *plan = zpq_adamw_plan{table, elems, chunks, count, p_dtype, g_dtype, copy_dtype, state_bits,
                            (int32_t)chunk};

@@ -172,12 +172,14 @@ zpq_status zpq_qgz_dequant_reduce_requant_i4(const uint8_t* in_codes, const floa
 
 /* Bytes of device memory that a table of `count` tensors takes, for
  * zpq_list_make and for zpq_adamw_plan_make (16-byte aligned). */
-#define ZPQ_LIST_BYTES(count) ((int64_t)(count) * 32 + 64)
+#define ZPQ_LIST_BYTES(count) ((int64_t)(count) * 32 + 20736)
 #define ZPQ_PLAN_BYTES(count) ((int64_t)(count) * 128 + 64)
 
 /* A list of tensors of one type: a table in the caller's device memory, and
  * what the host has to know of it.  Filled by zpq_list_make; the table's
- * contents (addresses among them) stand until it is made again. */
+ * contents (addresses among them) stand until it is made again.  The table also
+ * holds the partial sums of the zpq_grad_sumsq call that runs on it, so calls on
+ * one list must be ordered (one stream, or events). */
 typedef struct {
     void* table;
     int64_t elems;     /* of all tensors */
@@ -200,12 +202,9 @@ zpq_status zpq_list_make(const void* const* ptrs, const int64_t* sizes, int32_t 
  * Sum of squares over a list (the squared norm that clipping needs; ranks add
  * theirs): out[0] = sum of g^2, or out[0] += with accumulate, in binary64
  * throughout, in an order that depends on the sizes and the number of compute
- * units only.  workspace: ZPQ_SUMSQ_BYTES bytes of device memory, 16-byte
- * aligned, contents irrelevant.
+ * units only.  One launch.
  */
-#define ZPQ_SUMSQ_BYTES 32768
-zpq_status zpq_grad_sumsq(const zpq_list* list, double* out, int32_t accumulate, void* workspace,
-                          int64_t workspace_bytes, zpq_stream stream);
+zpq_status zpq_grad_sumsq(const zpq_list* list, double* out, int32_t accumulate, zpq_stream stream);
 
 /* One tensor of an optimizer step; all device pointers.  The tensors of one
  * plan must not overlap one another, nor a tensor's own parts. */

@@ -26,7 +26,7 @@ def make_list(ptrs=(P, P + 4096), sizes=(10, 20), dtype=2, table=P + (1 << 20), 
     n = len(sizes)
     c = zpq._List()
     return zpq.lib().zpq_list_make(arr(vp, ptrs), arr(ctypes.c_int64, sizes), n, dtype, vp(table),
-                                   n * 32 + 64 if nbytes is None else nbytes,
+                                   n * 32 + 20736 if nbytes is None else nbytes,
                                    ctypes.byref(c) if out else None, NUL)
 
 
@@ -40,30 +40,27 @@ def test_list_refusals():
     assert make_list(out=False) == NULL
     assert make_list(ptrs=(P + 1, P + 4096)) == ALIGN
     assert make_list(table=P + (1 << 20) + 8) == ALIGN
-    assert make_list(nbytes=127) == SIZE
+    assert make_list(nbytes=2 * 32 + 20735) == SIZE
     assert make_list(ptrs=(P, P + (1 << 20) + 16)) == ALIAS   # a tensor inside the table
     assert make_list(ptrs=(), sizes=(), table=0) == OK
     assert zpq.lib().zpq_list_make(None, None, -1, 0, NUL, 0, ctypes.byref(zpq._List()), NUL) == ARG
 
 
-def sumsq(table=P, elems=100, chunks=1, count=1, dtype=0, out=P + (1 << 16), ws=P + (1 << 18), nbytes=32768):
+def sumsq(table=P, elems=100, chunks=1, count=1, dtype=0, out=P + (1 << 16)):
     c = zpq._List(table, elems, chunks, count, dtype)
-    return zpq.lib().zpq_grad_sumsq(ctypes.byref(c), vp(out), 0, vp(ws), nbytes, NUL)
+    return zpq.lib().zpq_grad_sumsq(ctypes.byref(c), vp(out), 0, NUL)
 
 
 def test_sumsq_refusals():
-    assert zpq.lib().zpq_grad_sumsq(None, vp(P), 0, vp(P + 64), 32768, NUL) == NULL
+    assert zpq.lib().zpq_grad_sumsq(None, vp(P), 0, NUL) == NULL
     assert sumsq(dtype=9) == ARG
     assert sumsq(count=-1) == ARG
     assert sumsq(chunks=1 << 31) == ARG
     assert sumsq(table=0) == ARG
     assert sumsq(out=0) == NULL
-    assert sumsq(ws=0) == NULL
-    assert sumsq(nbytes=32767) == SIZE
     assert sumsq(out=P + (1 << 16) + 4) == ALIGN
-    assert sumsq(ws=P + (1 << 18) + 8) == ALIGN
-    assert sumsq(out=P + (1 << 18) + 64) == ALIAS
-    assert sumsq(out=P + 8) == ALIAS
+    assert sumsq(out=P + 8) == ALIAS                        # in the table
+    assert sumsq(out=P + 20736 + 24) == ALIAS
 
 
 FIELDS = dict(p=P, g=P + 0x10000, m=P + 0x20000, v=P + 0x30000, m_exp=0, v_exp=0, copy=0, n=1000,
@@ -220,7 +217,7 @@ def test_structures_match_the_header():
         for f, _ in s._fields_:
             src += f'printf(" %zu", offsetof({n}, {f}));\n'
         src += 'printf("\\n");\n'
-    src += 'printf("%d %d %d\\n", ZPQ_SUMSQ_BYTES, (int)ZPQ_LIST_BYTES(3), (int)ZPQ_PLAN_BYTES(3)); return 0;}\n'
+    src += 'printf("%d %d\\n", (int)ZPQ_LIST_BYTES(3), (int)ZPQ_PLAN_BYTES(3)); return 0;}\n'
     exe = os.path.join(ROOT, "tests", "native", "step_layout.tmp")
     subprocess.run(["gcc", "-x", "c", "-", "-I", os.path.join(ROOT, "include"), "-o", exe], input=src, text=True, check=True)
     try:
@@ -229,7 +226,7 @@ def test_structures_match_the_header():
         os.remove(exe)
     for line, s in zip(lines, names.values()):
         assert [int(x) for x in line.split()] == [ctypes.sizeof(s)] + [getattr(s, f).offset for f, _ in s._fields_]
-    assert lines[-1] == f"{zpq.SUMSQ_BYTES} {3 * 32 + 64} {3 * 128 + 64}"
+    assert lines[-1] == f"{3 * 32 + zpq.LIST_FIXED_BYTES} {3 * 128 + 64}"
 
 
 def test_binding_refuses_host_tensors():
