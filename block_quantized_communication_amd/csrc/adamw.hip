@@ -629,7 +629,7 @@ zpq_status zpq_grad_sumsq(const zpq_list* list, double* out, int32_t accumulate,
         if (!accumulate) hipLaunchKernelGGL(k_zero, dim3(1), dim3(1), 0, st, out);
         return after_launch();
     }
-    int64_t parts = (int64_t)cu_count() * 8;
+    int64_t parts = (int64_t)cu_count() * 4;
     if (parts > kSumParts) parts = kSumParts;
     if (parts > list->chunks) parts = list->chunks;
     ListEntry* e = list_entries(list->table);

@@ -139,16 +139,21 @@ __device__ __forceinline__ uint32_t key_of(const Ids& a, uint32_t t) {
 // Up to kRankTokens: a token's place is the number of tokens that come before
 // it, counted by comparing it with all of them.  A workgroup places 64 tokens, one a
 // lane; its waves share the others, 64 at a time through LDS (a broadcast read
-// gives 4, and each is one compare and one add with carry for 64 tokens).
-constexpr uint32_t kRankTokens = 16384;
+// gives 4, and each is one compare and one add with carry for 64 tokens).  Where
+// rows are few as well, further workgroups count the same way what comes before each
+// row: its first place.
+constexpr uint32_t kRankTokens = 8192;
 constexpr int kRankWaves = 16;
-__global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __restrict__ out) {
+__global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __restrict__ out,
+                                                          uint32_t* __restrict__ starts) {
     __shared__ uint32_t keys[kRankWaves][64];
     __shared__ uint32_t counts[kRankWaves][64];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint32_t own = blockIdx.x, t = own * 64 + lane;
-    const uint32_t key = t < a.tokens ? key_of(a, t) : 0xFFFFFFFEu;
     const uint32_t blocks = (a.tokens + 63) / 64;
+    const bool row_block = blockIdx.x >= blocks;
+    const uint32_t own = row_block ? 0xFFFFFFFFu : blockIdx.x;
+    const uint32_t t = (row_block ? blockIdx.x - blocks : blockIdx.x) * 64 + lane;     // token or row
+    const uint32_t key = row_block ? t : t < a.tokens ? key_of(a, t) : 0xFFFFFFFEu;
     uint32_t before = 0;
     auto key_at = [&](uint32_t b) {
         const uint32_t j = b * 64 + lane;
@@ -164,23 +169,24 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __res
         const u32x4* other = reinterpret_cast<const u32x4*>(keys[wave]);
         if (b != own) {
             // equal rows of earlier tokens come before, those of later ones do not
-            const uint32_t below = b < own ? key + 1 : key;
+            const uint32_t below = !row_block && b < own ? key + 1 : key;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const u32x4 k = other[i];
                 before += (k.x < below) + (k.y < below) + (k.z < below) + (k.w < below);
             }
         } else {
-#pragma unroll
+#pragma unroll 8
             for (int i = 0; i < 64; ++i) before += keys[wave][i] < (i < (int)lane ? key + 1 : key);
         }
     }
     counts[wave][lane] = before;
     __syncthreads();
-    if (wave == 0 && t < a.tokens) {
+    if (wave == 0) {
 #pragma unroll
         for (int w = 1; w < kRankWaves; ++w) before += counts[w][lane];
-        out[before] = (uint64_t)key << 32 | t;
+        if (!row_block && t < a.tokens) out[before] = (uint64_t)key << 32 | t;
+        if (row_block && t <= a.rows) starts[t] = before;
     }
 }
 
@@ -188,7 +194,7 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __res
 // construction.  k_digit_counts counts each tile's digits; k_digit_place gives every
 // token its place: tokens with smaller digits, the same digit in earlier tiles, in
 // earlier waves of the tile, and earlier in its wave (found by ballots).
-constexpr int kMaxDigits = 512, kSortThreads = 1024, kSortTile = 4 * kSortThreads;
+constexpr int kMaxDigits = 512, kSortThreads = 512, kSortTile = 4 * kSortThreads;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kDirectTiles = 64;         // up to this many tiles their counts are summed in place
 
@@ -327,54 +333,54 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint6
 
 // ---------------------------------------------------------------------------
 // Sums.  A frequent token's row may have thousands of terms, so the sorted list
-// is cut into aligned groups of 64, and of 64 * 64, ...: a group that lies
+// is cut into aligned groups of G = 2^log, and of G * G, ...: a group that lies
 // within one row is summed once, by lanes of its own, into the workspace
-// (level 1 from dy, level l from level l - 1); a row then adds at most 2 * 63
+// (level 1 from dy, level l from level l - 1); a row then adds at most 2 (G - 1)
 // terms a level.  Which terms are added in which order depends on the sorted
 // list alone.
-constexpr int kGroupLog = 6, kGroup = 1 << kGroupLog, kMaxLevels = 5;
+constexpr int kMaxLevels = 5;
+// Loads in flight in a row's sum: with 8 pieces of 8 elements the kernel has 5 waves
+// a SIMD and took 204 us for the 16,384 x 8192 gradient, with 4 it took 173.
+template <int E> constexpr int kRowFlight = E == 4 ? 8 : 4;
 
 struct GradArgs {
     const uint64_t* sorted;
     const void* dy;
     void* grad;
     uint32_t* starts;                         // [rows + 1]: each row's first place in `sorted`
-    float* part[kMaxLevels];                  // [tokens >> 6l][dim] sums of level l = 1, 2, ...
+    float* part[kMaxLevels];                  // [tokens >> (log * l)][dim] sums of level l = 1, 2, ...
     int64_t ld_dy, ld_grad, dim, rows;
     uint32_t tokens;
-    int32_t levels;
+    int32_t levels, log;
     float scale;
 };
 
-// acc += `count` rows of E elements; row(j, base) gives the place of the j-th.
-template <int DT, int E, class Row>
+// acc += `count` rows of E elements, FLIGHT loads at a time; row(j, base) gives the
+// place of the j-th.
+template <int DT, int E, int FLIGHT, class Row>
 __device__ __forceinline__ void add_rows(float (&acc)[E], uint32_t count, bool narrow, int dim, Row row) {
-    constexpr int kFlight = 8;                // loads in flight
-    uint32_t j = 0;
     if (!narrow) {
-        for (; j + kFlight <= count; j += kFlight) {
-            Raw<DT, E> r[kFlight];
+        auto batch = [&](uint32_t j, uint32_t n) {
+            Raw<DT, E> r[FLIGHT];
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                const void* base;
-                const int64_t at = row(j + u, base);
-                r[u].template load<false>(base, at);
-            }
+            for (uint32_t u = 0; u < FLIGHT; ++u)
+                if (u < n) {
+                    const void* base;
+                    const int64_t at = row(j + u, base);
+                    r[u].load(base, at);
+                }
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u)
+            for (uint32_t u = 0; u < FLIGHT; ++u)
+                if (u < n) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] += r[u].get(i);
-        }
-        for (; j < count; ++j) {
-            Raw<DT, E> r;
-            const void* base;
-            const int64_t at = row(j, base);
-            r.template load<false>(base, at);
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] += r.get(i);
-        }
+                    for (int i = 0; i < E; ++i) acc[i] += r[u].get(i);
+                }
+        };
+        uint32_t j = 0;
+        for (; j + FLIGHT <= count; j += FLIGHT) batch(j, FLIGHT);
+        if (j < count) batch(j, count - j);
     } else {
-        for (; j < count; ++j) {
+        for (uint32_t j = 0; j < count; ++j) {
             const void* base;
             const int64_t at = row(j, base);
 #pragma unroll
@@ -413,8 +419,8 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
     const uint32_t lane = block * kThreads + threadIdx.x;
     if (lane >= lanes) return;
     const uint32_t group = quotient(lane, pieces);
-    const uint32_t lo = group << (kGroupLog * level);            // whole groups only: in range
-    const uint32_t hi = lo + (1u << (kGroupLog * level)) - 1;
+    const uint32_t lo = group << (a.log * level);            // whole groups only: in range
+    const uint32_t hi = lo + (1u << (a.log * level)) - 1;
     const uint64_t key = a.sorted[lo] >> 32;
     if (key != a.sorted[hi] >> 32 || key >= (uint64_t)a.rows) return;
     const bool narrow = a.dim < E;
@@ -422,13 +428,13 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
     if (!narrow && col > a.dim - E) col = a.dim - E;
     float acc[E] = {};
     if constexpr (FIRST) {
-        add_rows<DT, E>(acc, kGroup, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+        add_rows<DT, E, 8>(acc, 1u << a.log, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
             base = a.dy;
             return (int64_t)(uint32_t)a.sorted[lo + j] * a.ld_dy + col;
         });
     } else {
-        const int64_t below = (int64_t)group << kGroupLog;
-        add_rows<ZPQ_F32, E>(acc, kGroup, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+        const int64_t below = (int64_t)group << a.log;
+        add_rows<ZPQ_F32, E, 8>(acc, 1u << a.log, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
             base = a.part[level - 2];
             return (below + j) * a.dim + col;
         });
@@ -465,14 +471,14 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
     while (at < e) {
         int level = a.levels;
 #pragma unroll 1
-        while (level > 0 && ((at & ((1u << (kGroupLog * level)) - 1)) != 0 ||
-                             e - at < (1u << (kGroupLog * level))))
+        while (level > 0 && ((at & ((1u << (a.log * level)) - 1)) != 0 ||
+                             e - at < (1u << (a.log * level))))
             --level;
         if (level == 0) {
             // up to the next group that could be whole
-            uint32_t stop = a.levels > 0 ? (at | (kGroup - 1)) + 1 : e;
+            uint32_t stop = a.levels > 0 ? (at | ((1u << a.log) - 1)) + 1 : e;
             if (stop > e) stop = e;
-            add_rows<DT, E>(acc, stop - at, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+            add_rows<DT, E, kRowFlight<E>>(acc, stop - at, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
                 base = a.dy;
                 const uint64_t token = UNIFORM ? load_uniform(a.sorted, at + j) : a.sorted[at + j];
                 return (int64_t)(uint32_t)token * a.ld_dy + col;
@@ -480,15 +486,15 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
             at = stop;
         } else {
             // groups of this level up to the end, or to where a larger one starts
-            const uint32_t shift = kGroupLog * level;
+            const uint32_t shift = a.log * level;
             uint32_t groups = (e - at) >> shift;
             if (level < a.levels) {
-                const uint32_t next = kGroup - ((at >> shift) & (kGroup - 1));
+                const uint32_t next = (1u << a.log) - ((at >> shift) & ((1u << a.log) - 1));
                 if (next < groups) groups = next;
             }
             const int64_t g0 = at >> shift;
             const float* part = a.part[level - 1];
-            add_rows<ZPQ_F32, E>(acc, groups, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
+            add_rows<ZPQ_F32, E, kRowFlight<E>>(acc, groups, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
                 base = part;
                 return (g0 + j) * a.dim + col;
             });
@@ -604,11 +610,15 @@ zpq_status lookup(const LookupArgs& a, int32_t t_dtype, int32_t out_dtype, hipSt
 
 struct GradWorkspace {
     int64_t sorted[2], counts, totals, starts, part[kMaxLevels], bytes;
-    int32_t levels;
+    int32_t levels, log;
 };
 
-// Level 1 pays from a few hundred tokens on, a further level (a launch that
+// Groups of 16 where the gradient is small and a frequent row's chain of additions
+// is what takes the time (8000 tokens x 100: 39 us, with 64 56), of 64 where the sums' own
+// traffic tells (131,072 x 2048: 204 us, with 16 216); about even at 2^25.  Level 1 pays from
+// some hundred tokens on (its launch takes 3.5 us), a further level (a launch that
 // mostly finds nothing to sum) only where a row could hold very many groups.
+constexpr int64_t kSmallGrad = 1 << 25;       // tokens * dim
 inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim, int64_t rows) {
     GradWorkspace w = {};
     auto take = [&](int64_t bytes) {
@@ -623,20 +633,26 @@ inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim, int64_t rows) {
         w.counts = take((tokens + kSortTile - 1) / kSortTile * kMaxDigits * 4);
         w.totals = take(kMaxDigits * 4);
     }
-    for (int l = 1; l <= kMaxLevels && (tokens >> (kGroupLog * l)) >= (l == 1 ? 4 : 32); ++l) {
-        w.part[l - 1] = take((tokens >> (kGroupLog * l)) * dim * 4);
+    w.log = tokens * dim <= kSmallGrad ? 4 : 6;
+    for (int l = 1; l <= kMaxLevels && tokens >= 512 && (l == 1 || (tokens >> (w.log * l)) >= 64); ++l) {
+        w.part[l - 1] = take((tokens >> (w.log * l)) * dim * 4);
         w.levels = l;
     }
     return w;
 }
 
-// The sorted list; `list` and `other` are exchanged as the passes need.
-void sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* counts, uint32_t* totals,
-                 hipStream_t st) {
-    if (a.tokens == 0) return;
+// The sorted list; `list` and `other` are exchanged as the passes need.  True where
+// the rows' first places have been found as well: where that takes about 1 us
+// (2^24 comparisons), less than the launch that it saves.
+constexpr int64_t kRankRows = 1 << 24;
+bool sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* counts, uint32_t* totals,
+                 uint32_t* starts, hipStream_t st) {
+    if (a.tokens == 0) return false;
     if (a.tokens <= kRankTokens) {
-        hipLaunchKernelGGL(k_rank, dim3((a.tokens + 63) / 64), dim3(64 * kRankWaves), 0, st, a, list);
-        return;
+        const bool rows = a.rows * a.tokens <= kRankRows;
+        const unsigned blocks = (a.tokens + 63) / 64 + (rows ? (unsigned)(a.rows / 64 + 1) : 0);
+        hipLaunchKernelGGL(k_rank, dim3(blocks), dim3(64 * kRankWaves), 0, st, a, list, starts);
+        return rows;
     }
     int bits = 1;
     while (a.rows >> bits) ++bits;            // of the largest key, `rows`
@@ -654,15 +670,16 @@ void sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* coun
         list = other;
         other = t;
     }
+    return false;
 }
 
 template <int DT>
-void launch_groups(const GradArgs& a, hipStream_t st) {
-    const uint32_t start_blocks = (uint32_t)(a.rows / kThreads + 1);
-    for (int l = 1; l <= (a.levels > 0 ? a.levels : 1); ++l) {
+void launch_groups(const GradArgs& a, bool starts_done, hipStream_t st) {
+    const uint32_t start_blocks = starts_done ? 0 : (uint32_t)(a.rows / kThreads + 1);
+    for (int l = 1; l <= (a.levels > 0 || starts_done ? a.levels : 1); ++l) {
         const int E = l == 1 ? piece_elems<DT, DT>() : 4;
         const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
-        const uint32_t lanes = l <= a.levels ? (a.tokens >> (kGroupLog * l)) * pieces : 0;
+        const uint32_t lanes = l <= a.levels ? (a.tokens >> (a.log * l)) * pieces : 0;
         const unsigned blocks = lanes / kThreads + (lanes % kThreads != 0);
         if (l == 1)
             hipLaunchKernelGGL((k_group_sums<DT, true>), dim3(blocks + start_blocks), dim3(kThreads), 0, st, a, l,
@@ -695,8 +712,8 @@ void launch_rows_add(const GradArgs& a, bool add, hipStream_t st) {
     else launch_rows<DT, OT, false>(a, st);
 }
 template <int DT>
-void launch_grad(const GradArgs& a, int32_t grad_dtype, bool add, hipStream_t st) {
-    launch_groups<DT>(a, st);
+void launch_grad(const GradArgs& a, int32_t grad_dtype, bool add, bool starts_done, hipStream_t st) {
+    launch_groups<DT>(a, starts_done, st);
     if (grad_dtype == ZPQ_F32) launch_rows_add<DT, ZPQ_F32>(a, add, st);
     else if (grad_dtype == ZPQ_F16) launch_rows_add<DT, ZPQ_F16>(a, add, st);
     else launch_rows_add<DT, ZPQ_BF16>(a, add, st);
@@ -706,7 +723,7 @@ void launch_grad(const GradArgs& a, int32_t grad_dtype, bool add, hipStream_t st
 // bits, a launch's rows of pieces in 30.
 bool grad_sizes_ok(int64_t tokens, int64_t dim, int64_t rows) {
     return tokens >= 0 && tokens <= (1LL << 28) && dim >= 1 && dim <= (1 << 28) && rows >= 0 &&
-           rows <= (1LL << 27) && (tokens >> kGroupLog) * ((dim + 3) / 4) < (1LL << 31);
+           rows <= (1LL << 27) && (tokens >> 6) * ((dim + 3) / 4) < (1LL << 31);
 }
 
 }  // namespace
@@ -791,13 +808,13 @@ zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, c
     auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
     uint64_t* list = reinterpret_cast<uint64_t*>(ws + w.sorted[0]);
     uint64_t* other = reinterpret_cast<uint64_t*>(ws + w.sorted[1]);
-    sort_tokens(Ids{ids, first, padding, rows, id_bytes, (uint32_t)tokens}, list, other, words(w.counts),
-                words(w.totals), st);
-    GradArgs a = {list, dy, grad, words(w.starts), {}, ld_dy, ld_grad, dim, rows, (uint32_t)tokens, w.levels, scale};
+    const bool starts_done = sort_tokens(Ids{ids, first, padding, rows, id_bytes, (uint32_t)tokens}, list, other, words(w.counts),
+                words(w.totals), words(w.starts), st);
+    GradArgs a = {list, dy, grad, words(w.starts), {}, ld_dy, ld_grad, dim, rows, (uint32_t)tokens, w.levels, w.log, scale};
     for (int l = 0; l < w.levels; ++l) a.part[l] = reinterpret_cast<float*>(ws + w.part[l]);
-    if (dy_dtype == ZPQ_F32) launch_grad<ZPQ_F32>(a, grad_dtype, accumulate != 0, st);
-    else if (dy_dtype == ZPQ_F16) launch_grad<ZPQ_F16>(a, grad_dtype, accumulate != 0, st);
-    else launch_grad<ZPQ_BF16>(a, grad_dtype, accumulate != 0, st);
+    if (dy_dtype == ZPQ_F32) launch_grad<ZPQ_F32>(a, grad_dtype, accumulate != 0, starts_done, st);
+    else if (dy_dtype == ZPQ_F16) launch_grad<ZPQ_F16>(a, grad_dtype, accumulate != 0, starts_done, st);
+    else launch_grad<ZPQ_BF16>(a, grad_dtype, accumulate != 0, starts_done, st);
     return after_launch();
 }
 
