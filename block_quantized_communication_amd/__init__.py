@@ -64,7 +64,7 @@ class _AdamwPlan(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("elems", ctypes.c_int64), ("chunks", ctypes.c_int64),
                 ("count", ctypes.c_int32), ("p_dtype", ctypes.c_int32),
                 ("g_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32),
-                ("state_bits", ctypes.c_int32), ("chunk_elems", ctypes.c_int32)]
+                ("state_bits", ctypes.c_int32)]
 
 
 class _AdamwHyper(ctypes.Structure):
@@ -421,6 +421,23 @@ class AdamW:
             self._table = torch.empty(count * 128 + 64, dtype=torch.uint8, device=self.device)
         self.set_grads(grads, stream=stream)
 
+    def _check_apart(self, grads):
+        """No memory that the step writes may be written or read through another
+        tensor (tied weights count once)."""
+        spans = []
+        flat = lambda xs: [y for x in xs for y in (x if isinstance(x, tuple) else (x,))]  # noqa: E731
+        for written, ts in ((True, flat(self.params + (self.copies or []) + self.exp_avg + self.exp_avg_sq)),
+                            (False, grads)):
+            spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), written) for t in ts if t.numel()]
+        spans.sort()
+        any_end = written_end = 0
+        for lo, hi, written in spans:
+            if lo < (any_end if written else written_end):
+                raise ValueError("params, copies, moments and grads overlap in memory")
+            any_end = max(any_end, hi)
+            if written:
+                written_end = max(written_end, hi)
+
     def _match(self, tensors, name):
         if len(tensors) != len(self.params):
             raise ValueError(f"{name}: need {len(self.params)} tensors, got {len(tensors)}")
@@ -456,6 +473,7 @@ class AdamW:
         grads = list(grads)
         self._match(grads, "grads")
         gd = _one_dtype(grads, "grads")
+        self._check_apart(grads)
         count = len(self.params)
         rows = (_AdamwTensor * count)()
         for i, (r, p, g) in enumerate(zip(rows, self.params, grads)):

@@ -395,13 +395,12 @@ struct Part {
     }
 };
 
-// Workgroup k of the grid (and k + gridDim.x, ...) takes chunk k: chunk_elems
-// consecutive elements of one tensor, in tiles of kParts parts.
+// Workgroup k of the grid (and k + gridDim.x, ...) takes chunk k: one tile of one
+// tensor.
 template <int PT, int GT, int CT, int BITS>
 __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict__ entries,
                                                     const uint32_t* __restrict__ starts,
-                                                    int32_t count, uint32_t chunks,
-                                                    int32_t chunk_elems, StepArgs a,
+                                                    int32_t count, uint32_t chunks, StepArgs a,
                                                     const double* __restrict__ sumsq) {
     float c = (float)a.grad_scale;
     if (sumsq != nullptr) {
@@ -414,15 +413,12 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict_
         const uint32_t t = find_start(starts, count, k);
         const PlanEntry e = entries[t];
         const float keep = (float)(1.0 - a.lr * e.decay);
-        int64_t at = (int64_t)(k - starts[t]) * chunk_elems;
-        const int64_t end = at + chunk_elems < e.n ? at + chunk_elems : e.n;
-        for (; at < end; at += kTile) {
-            Part<PT, GT, CT, BITS> part[kParts];
+        const int64_t at = (int64_t)(k - starts[t]) * kTile;
+        Part<PT, GT, CT, BITS> part[kParts];
 #pragma unroll
-            for (int u = 0; u < kParts; ++u) part[u].load(e, at + u * kPart);
+        for (int u = 0; u < kParts; ++u) part[u].load(e, at + u * kPart);
 #pragma unroll
-            for (int u = 0; u < kParts; ++u) part[u].step(e, a, c, keep);
-        }
+        for (int u = 0; u < kParts; ++u) part[u].step(e, a, c, keep);
     }
 }
 
@@ -517,7 +513,7 @@ template <int PT, int GT, int CT, int BITS>
 void launch_adamw(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
     hipLaunchKernelGGL((k_adamw<PT, GT, CT, BITS>), dim3(grid_of(q->chunks)), dim3(kThreads), 0, st,
                        plan_entries(q->table), starts_of(plan_entries(q->table), q->count),
-                       q->count, (uint32_t)q->chunks, q->chunk_elems, a, sumsq);
+                       q->count, (uint32_t)q->chunks, a, sumsq);
 }
 template <int PT, int GT, int BITS>
 void launch_adamw_c(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
@@ -662,7 +658,7 @@ zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, i
     if (table_bytes < ZPQ_PLAN_BYTES(count)) return ZPQ_ERR_SIZE;
     if (count > 0 && !aligned(table, 16)) return ZPQ_ERR_ALIGN;
     const int64_t sb = state_bits / 8;
-    int64_t elems = 0, tiles = 0;
+    int64_t elems = 0, chunks = 0;
     for (int32_t i = 0; i < count; ++i)
         if (tensors[i].n < 0 || tensors[i].n > kMaxElems || (elems += tensors[i].n) > kMaxElems)
             return ZPQ_ERR_SIZE;
@@ -683,10 +679,8 @@ zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, i
         for (int x = 0; x < 8; ++x)
             for (int y = x + 1; y < 8; ++y)
                 if (overlaps(at[x], size[x], at[y], size[y])) return ZPQ_ERR_ALIAS;
-        tiles += (t.n + kTile - 1) / kTile;
+        chunks += (t.n + kTile - 1) / kTile;
     }
-    const int64_t chunk = kTile;
-    int64_t chunks = tiles;
     if (chunks > 0x7FFFFFFF) return ZPQ_ERR_SIZE;
     hipStream_t st = static_cast<hipStream_t>(stream);
     PlanEntry* entries = plan_entries(table);
@@ -699,14 +693,13 @@ zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, i
             f.entry[i] = PlanEntry{t.p, t.g, t.m, t.v, t.m_exp, t.v_exp, t.copy, t.n, base,
                                    t.weight_decay};
             f.start[i] = (uint32_t)start;
-            start += (t.n + chunk - 1) / chunk;
+            start += (t.n + kTile - 1) / kTile;
             base += (t.n + kStateBlock - 1) / kStateBlock * kStateBlock;
         }
         hipLaunchKernelGGL((k_fill<PlanEntry, kFillPlan>), dim3(1), dim3(128), 0, st, f, first, some, count,
                            entries, starts_of(entries, count), (uint32_t)chunks, (ListHead*)nullptr);
     }
-    *plan = zpq_adamw_plan{table, elems, chunks, count, p_dtype, g_dtype, copy_dtype, state_bits,
-                           (int32_t)chunk};
+    *plan = zpq_adamw_plan{table, elems, chunks, count, p_dtype, g_dtype, copy_dtype, state_bits};
     return count > 0 ? after_launch() : ZPQ_OK;
 }
 
@@ -715,8 +708,7 @@ zpq_status zpq_adamw_step(const zpq_adamw_plan* plan, const zpq_adamw_hyper* h, 
     if (!plan || !h) return ZPQ_ERR_NULL;
     if (dtype_bytes(plan->p_dtype) == 0 || dtype_bytes(plan->g_dtype) == 0 ||
         (plan->state_bits != 32 && plan->state_bits != 8) || plan->count < 0 || plan->chunks < 0 ||
-        plan->chunks > 0x7FFFFFFF || (plan->chunks > 0 && (!plan->table || plan->chunk_elems % kTile != 0 ||
-                                                          plan->chunk_elems <= 0)))
+        plan->chunks > 0x7FFFFFFF || (plan->chunks > 0 && !plan->table))
         return ZPQ_ERR_ARG;
     if (!finite_at_least(h->lr, 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
         !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !finite_at_least(h->eps, 1e-30) || h->step < 1 ||

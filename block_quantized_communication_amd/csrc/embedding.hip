@@ -532,28 +532,34 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
 
 // WIDE: a wave takes 64 pieces of one row, so that the row's places and positions
 // are scalar; `pieces` counts waves a row.  Otherwise lanes are dealt out row by
-// row, several rows a wave.
-template <int DT, int OT, bool ADD, bool WIDE>
-__global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first_row, uint32_t lanes,
+// row, several rows a wave.  BY_TOKEN: the rows are those that tokens name, each found
+// at its first token; `first` and the lanes count tokens.
+template <int DT, int OT, bool ADD, bool WIDE, bool BY_TOKEN>
+__global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first, uint32_t lanes,
                                                        Divisor pieces) {
     const uint32_t lane = blockIdx.x * kThreads + threadIdx.x;
-    if constexpr (WIDE) {
-        const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lane >> 6));
-        if (wave >= lanes) return;
-        const uint32_t r = quotient(wave, pieces);
-        const int64_t row = first_row + r;
-        const uint32_t at = load_uniform(a.starts, row), e = load_uniform(a.starts, row + 1);
-        const uint32_t piece = (wave - r * pieces.d) * 64 + (threadIdx.x & 63u);
-        if ((ADD && at == e) || (int64_t)piece * piece_elems<DT, OT>() >= a.dim) return;
-        row_sum<DT, OT, ADD, true>(a, row, piece, at, e);
+    const uint32_t item = WIDE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(lane >> 6)) : lane;
+    if (item >= lanes) return;
+    const uint32_t r = quotient(item, pieces);
+    int64_t row = first + r;
+    uint32_t at, e;
+    auto get = [](const auto* p, int64_t i) { return WIDE ? load_uniform(p, i) : p[i]; };
+    if constexpr (BY_TOKEN) {
+        at = (uint32_t)row;
+        row = (int64_t)(get(a.sorted, at) >> 32);
+        if (row >= a.rows || (at > 0 && (int64_t)(get(a.sorted, at - 1) >> 32) == row)) return;
+        e = get(a.starts, row + 1);
     } else {
-        if (lane >= lanes) return;
-        const uint32_t r = quotient(lane, pieces);
-        const int64_t row = first_row + r;
-        const uint32_t at = a.starts[row], e = a.starts[row + 1];
+        at = get(a.starts, row);
+        e = get(a.starts, row + 1);
         if (ADD && at == e) return;
-        row_sum<DT, OT, ADD, false>(a, row, lane - r * pieces.d, at, e);
     }
+    uint32_t piece = item - r * pieces.d;
+    if constexpr (WIDE) {
+        piece = piece * 64 + (threadIdx.x & 63u);
+        if ((int64_t)piece * piece_elems<DT, OT>() >= a.dim) return;
+    }
+    row_sum<DT, OT, ADD, WIDE>(a, row, piece, at, e);
 }
 
 // ---------------------------------------------------------------------------
@@ -617,7 +623,8 @@ struct GradWorkspace {
 // is what takes the time (8000 tokens x 100: 39 us, with 64 56), of 64 where the sums' own
 // traffic tells (131,072 x 2048: 204 us, with 16 216); about even at 2^25.  Level 1 pays from
 // some hundred tokens on (its launch takes 3.5 us), a further level (a launch that
-// mostly finds nothing to sum) only where a row could hold very many groups.
+// mostly finds nothing to sum) only where a row could hold very many groups, or where
+// rows average a group of it.
 constexpr int64_t kSmallGrad = 1 << 25;       // tokens * dim
 inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim, int64_t rows) {
     GradWorkspace w = {};
@@ -634,8 +641,10 @@ inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim, int64_t rows) {
         w.totals = take(kMaxDigits * 4);
     }
     w.log = tokens * dim <= kSmallGrad ? 4 : 6;
-    for (int l = 1; l <= kMaxLevels && tokens >= 512 && (l == 1 || (tokens >> (w.log * l)) >= 64); ++l) {
-        w.part[l - 1] = take((tokens >> (w.log * l)) * dim * 4);
+    for (int l = 1; l <= kMaxLevels && tokens >= 512; ++l) {
+        const int64_t groups = tokens >> (w.log * l);
+        if (l > 1 && (groups < 2 || (groups < 64 && groups < rows))) break;
+        w.part[l - 1] = take(groups * dim * 4);
         w.levels = l;
     }
     return w;
@@ -689,27 +698,32 @@ void launch_groups(const GradArgs& a, bool starts_done, hipStream_t st) {
                                divisor(pieces));
     }
 }
-template <int DT, int OT, bool ADD>
+template <int DT, int OT, bool ADD, bool BY_TOKEN>
 void launch_rows(const GradArgs& a, hipStream_t st) {
     constexpr int E = piece_elems<DT, OT>();
     const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
     const bool wide = pieces >= 33;
     const uint32_t per_row = wide ? (pieces + 63) / 64 : pieces;
     const int64_t some = (1 << (wide ? 24 : 30)) / per_row;       // rows a launch: at most 2^30 lanes
-    for (int64_t first = 0; first < a.rows; first += some) {
-        const uint32_t n = (uint32_t)((a.rows - first < some ? a.rows - first : some) * per_row);
+    const int64_t all = BY_TOKEN ? a.tokens : a.rows;
+    for (int64_t first = 0; first < all; first += some) {
+        const uint32_t n = (uint32_t)((all - first < some ? all - first : some) * per_row);
         if (wide)
-            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, true>), dim3(n / 4 + (n % 4 != 0)), dim3(kThreads), 0, st,
-                               a, first, n, divisor(per_row));
-        else
-            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, false>), dim3(n / kThreads + (n % kThreads != 0)),
+            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, true, BY_TOKEN>), dim3(n / 4 + (n % 4 != 0)),
                                dim3(kThreads), 0, st, a, first, n, divisor(per_row));
+        else
+            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, false, BY_TOKEN>),
+                               dim3(n / kThreads + (n % kThreads != 0)), dim3(kThreads), 0, st, a, first, n,
+                               divisor(per_row));
     }
 }
 template <int DT, int OT>
 void launch_rows_add(const GradArgs& a, bool add, hipStream_t st) {
-    if (add) launch_rows<DT, OT, true>(a, st);
-    else launch_rows<DT, OT, false>(a, st);
+    // rows that get nothing are not touched: a launch over the tokens is smaller where
+    // there are fewer of them
+    if (add && (int64_t)a.tokens < a.rows) launch_rows<DT, OT, true, true>(a, st);
+    else if (add) launch_rows<DT, OT, true, false>(a, st);
+    else launch_rows<DT, OT, false, false>(a, st);
 }
 template <int DT>
 void launch_grad(const GradArgs& a, int32_t grad_dtype, bool add, bool starts_done, hipStream_t st) {

@@ -223,7 +223,7 @@ typedef struct {
 typedef struct {
     void* table;
     int64_t elems, chunks;
-    int32_t count, p_dtype, g_dtype, copy_dtype, state_bits, chunk_elems;
+    int32_t count, p_dtype, g_dtype, copy_dtype, state_bits;
 } zpq_adamw_plan;
 
 /*

@@ -287,3 +287,37 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(g, grad), rep
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("tokens,rows,dim", [(53280, 4, 24), (8192, 2048, 12), (8192, 2049, 12), (8193, 3, 520),
+                                             (511, 70, 9), (512, 70, 9), (20000, 90000, 132), (300000, 5, 7),
+                                             (3000, 40, 12000), (2500, 200000, 3)])
+def test_grad_sizes_of_the_sums(tokens, rows, dim, accumulate):
+    """Both sides of the rules on group sizes and levels, on where the rows' places
+    are found and on launches over tokens: exact sums of small integers."""
+    import torch
+    rng = np.random.default_rng(tokens + rows)
+    ids, t = draw_ids(tokens, rows, rows)
+    y = rng.integers(-2, 3, (tokens, dim))
+    g = torch.full((rows, dim), 3.0, device="cuda")
+    zpq.embedding_grad(t, torch.from_numpy(y.astype(np.float32)).cuda().half(), rows, scale=2.0, out=g,
+                       accumulate=accumulate)
+    want, _, _ = ref.grad64(ids, y.astype(np.float64), rows, 2.0)
+    assert np.array_equal(host(g), want + (3.0 if accumulate else 0.0))
+
+
+def test_grad_past_32_bits():
+    """dy and the gradient beyond 2^32 elements."""
+    import torch
+    rows = tokens = (1 << 20) + 9
+    dim = 4100
+    y = torch.zeros(tokens, dim, dtype=torch.bfloat16, device="cuda")
+    y[-1], y[-2], y[3] = 3.0, 5.0, 7.0
+    t = torch.full((tokens,), -1, device="cuda")
+    t[-1] = t[3] = rows - 1
+    t[-2] = rows - 2
+    g = zpq.embedding_grad(t, y, rows)
+    assert bool((g[-1] == 10).all()) and bool((g[-2] == 5).all()) and not bool(g[:-2].any())
+    zpq.embedding_grad(t, y, rows, out=g, accumulate=True)
+    assert bool((g[-1] == 20).all()) and bool((g[-2] == 10).all()) and not bool(g[5:9].any())

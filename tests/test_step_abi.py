@@ -108,8 +108,8 @@ def test_plan_refusals():
     assert plan(rows=[], count=-1) == ARG
 
 
-def step(count=1, chunks=1, table=P, chunk=2048, bits=32, sumsq=None, **h):
-    q = zpq._AdamwPlan(table, 100, chunks, count, 0, 2, -1, bits, chunk)
+def step(count=1, chunks=1, table=P, bits=32, sumsq=None, **h):
+    q = zpq._AdamwPlan(table, 100, chunks, count, 0, 2, -1, bits)
     v = dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, grad_scale=1.0, max_norm=float("inf"), step=1, seed=0)
     return zpq.lib().zpq_adamw_step(ctypes.byref(q), ctypes.byref(zpq._AdamwHyper(**dict(v, **h))),
                                     vp(sumsq), NUL)
@@ -120,7 +120,7 @@ def test_step_refusals():
     for bad in (dict(lr=-1.0), dict(lr=nan), dict(lr=inf), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=nan),
                 dict(beta2=1.0), dict(eps=0.0), dict(eps=nan), dict(eps=inf), dict(grad_scale=0.0),
                 dict(grad_scale=nan), dict(grad_scale=inf), dict(max_norm=0.0), dict(max_norm=nan),
-                dict(max_norm=1.0), dict(step=0), dict(bits=4), dict(table=0), dict(chunk=100), dict(chunk=0),
+                dict(max_norm=1.0), dict(step=0), dict(bits=4), dict(table=0),
                 dict(chunks=1 << 31), dict(count=-1)):
         assert step(**bad) == ARG, bad
     assert step(sumsq=P + 4) == ALIGN
