@@ -339,9 +339,9 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint6
 // terms a level.  Which terms are added in which order depends on the sorted
 // list alone.
 constexpr int kMaxLevels = 5;
-// Loads in flight in a row's sum: with 8 pieces of 8 elements the kernel has 5 waves
-// a SIMD and took 204 us for the 16,384 x 8192 gradient, with 4 it took 173.
-template <int E> constexpr int kRowFlight = E == 4 ? 8 : 4;
+// Loads in flight in a row's sum: with 8 (of 8 elements) the kernel has 5 waves a SIMD
+// and took 204 us for the 16,384 x 8192 gradient, with 4 it took 173.
+constexpr int kRowFlight = 4;
 
 struct GradArgs {
     const uint64_t* sorted;
@@ -355,20 +355,17 @@ struct GradArgs {
     float scale;
 };
 
-// acc += `count` rows of E elements, FLIGHT loads at a time; row(j, base) gives the
-// place of the j-th.
+// acc += the E elements from `col` of `count` rows, FLIGHT rows' loads at a time;
+// row(j) is the address of the j-th row.  `narrow`: rows of dim < E elements, whole.
 template <int DT, int E, int FLIGHT, class Row>
-__device__ __forceinline__ void add_rows(float (&acc)[E], uint32_t count, bool narrow, int dim, Row row) {
+__device__ __forceinline__ void add_rows(float (&acc)[E], uint32_t col, uint32_t count, bool narrow, int dim,
+                                         Row row) {
     if (!narrow) {
         auto batch = [&](uint32_t j, uint32_t n) {
             Raw<DT, E> r[FLIGHT];
 #pragma unroll
             for (uint32_t u = 0; u < FLIGHT; ++u)
-                if (u < n) {
-                    const void* base;
-                    const int64_t at = row(j + u, base);
-                    r[u].load(base, at);
-                }
+                if (u < n) r[u].load(row(j + u), col);
 #pragma unroll
             for (uint32_t u = 0; u < FLIGHT; ++u)
                 if (u < n) {
@@ -381,13 +378,61 @@ __device__ __forceinline__ void add_rows(float (&acc)[E], uint32_t count, bool n
         if (j < count) batch(j, count - j);
     } else {
         for (uint32_t j = 0; j < count; ++j) {
-            const void* base;
-            const int64_t at = row(j, base);
+            const void* base = row(j);
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                if (i < dim) acc[i] += load1<DT>(base, at + i);
+                if (i < dim) acc[i] += load1<DT>(base, i);
         }
     }
+}
+
+// Reads of wave-uniform addresses through the scalar cache, of what earlier
+// launches wrote.
+template <class T>
+__device__ __forceinline__ T load_uniform(const T* p, int64_t i) {
+    typedef const T __attribute__((address_space(4))) scalar_t;
+    return reinterpret_cast<scalar_t*>(reinterpret_cast<uintptr_t>(p))[i];
+}
+template <bool UNIFORM, class T>
+__device__ __forceinline__ T load_from(const T* p, int64_t i) {
+    if constexpr (UNIFORM) return load_uniform(p, i);
+    else return p[i];
+}
+
+// How rows (or groups) are dealt out.  WIDE, for rows of more than 32 pieces: a wave
+// takes 64 pieces of one row, so that the row's places and positions are scalars
+// (131,072 x 2048: row sums 144 us, lane by lane 191).  Otherwise lanes one after the
+// other, a piece each, several rows a wave.  `per` counts items a row, waves or lanes.
+// (Two pieces a lane and row: 0 to 7% slower.)
+struct Share {
+    uint32_t items;
+    Divisor per;
+};
+inline bool wide_rows(uint32_t pieces) { return pieces > 32; }
+inline Share share_of(int64_t rows, uint32_t pieces) {
+    const uint32_t per = wide_rows(pieces) ? (pieces + 63) / 64 : pieces;
+    return Share{(uint32_t)(rows * per), divisor(per)};
+}
+
+// This lane's row and first column; false past the end.
+template <bool WIDE, int E>
+__device__ __forceinline__ bool my_share(const Share& s, uint32_t block, uint32_t& row, uint32_t& col) {
+    const uint32_t lane = block * kThreads + threadIdx.x;
+    const uint32_t item = WIDE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(lane >> 6)) : lane;
+    if (item >= s.items) return false;
+    row = quotient(item, s.per);
+    const uint32_t rest = item - row * s.per.d;
+    col = (WIDE ? rest * 64 + (threadIdx.x & 63u) : rest) * E;
+    return true;
+}
+// Elements that a piece from `col` writes (0: past the row); a short piece is moved
+// back to end with the row.
+template <int E>
+__device__ __forceinline__ int piece_count(int64_t dim, bool narrow, uint32_t& col) {
+    const int64_t left = dim - (int64_t)col;
+    const int count = left >= E ? E : left > 0 ? (int)left : 0;
+    if (!narrow && count < E) col = (uint32_t)(dim - E);
+    return count;
 }
 
 // First place of the sorted list whose row is not below r.
@@ -400,12 +445,12 @@ __device__ __forceinline__ uint32_t lower_bound(const uint64_t* __restrict__ s, 
     return lo;
 }
 
-// Level `level` sums: lane L takes piece L % pieces of group L / pieces.  On level 1
-// the workgroups from `start_blocks` on; those before find the rows' first places, a
-// row a lane.
-template <int DT, bool FIRST>
-__global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t level, uint32_t lanes,
-                                                         uint32_t start_blocks, Divisor pieces) {
+// Level `level` sums of whole groups that lie within one row.  On level 1 the
+// workgroups from `start_blocks` on; those before find the rows' first places, a row a
+// lane.
+template <int DT, bool FIRST, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t level, uint32_t start_blocks,
+                                                         Share share) {
     constexpr int E = FIRST ? piece_elems<DT, DT>() : 4;
     uint32_t block = blockIdx.x;
     if constexpr (FIRST) {
@@ -416,56 +461,65 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
         }
         block -= start_blocks;
     }
-    const uint32_t lane = block * kThreads + threadIdx.x;
-    if (lane >= lanes) return;
-    const uint32_t group = quotient(lane, pieces);
-    const uint32_t lo = group << (a.log * level);            // whole groups only: in range
+    uint32_t group, col;
+    if (!my_share<WIDE, E>(share, block, group, col)) return;
+    const uint32_t lo = group << (a.log * level);
     const uint32_t hi = lo + (1u << (a.log * level)) - 1;
-    const uint64_t key = a.sorted[lo] >> 32;
-    if (key != a.sorted[hi] >> 32 || key >= (uint64_t)a.rows) return;
-    const bool narrow = a.dim < E;
-    int64_t col = (int64_t)(lane - group * pieces.d) * E;
-    if (!narrow && col > a.dim - E) col = a.dim - E;
+    const uint32_t key = (uint32_t)(load_from<WIDE>(a.sorted, lo) >> 32);
+    if (key != (uint32_t)(load_from<WIDE>(a.sorted, hi) >> 32) || key >= a.rows) return;
+    const bool narrow = !WIDE && a.dim < E;
+    const int count = piece_count<E>(a.dim, narrow, col);
+    if (count == 0) return;
     float acc[E] = {};
     if constexpr (FIRST) {
-        add_rows<DT, E, 8>(acc, 1u << a.log, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
-            base = a.dy;
-            return (int64_t)(uint32_t)a.sorted[lo + j] * a.ld_dy + col;
+        add_rows<DT, E, 8>(acc, col, 1u << a.log, narrow, (int)a.dim, [&](uint32_t j) {
+            return from<DT>(a.dy, (int64_t)(uint32_t)load_from<WIDE>(a.sorted, lo + j) * a.ld_dy);
         });
     } else {
         const int64_t below = (int64_t)group << a.log;
-        add_rows<ZPQ_F32, E, 8>(acc, 1u << a.log, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
-            base = a.part[level - 2];
-            return (below + j) * a.dim + col;
+        add_rows<ZPQ_F32, E, 8>(acc, col, 1u << a.log, narrow, (int)a.dim, [&](uint32_t j) {
+            return from<ZPQ_F32>((const void*)a.part[level - 2], (below + j) * a.dim);
         });
     }
-    float* to = a.part[level - 1];
+    float* to = a.part[level - 1] + (int64_t)group * a.dim;
     if (narrow) {
-        for (int i = 0; i < (int)a.dim; ++i) to[(int64_t)group * a.dim + i] = acc[i];
+        for (int i = 0; i < (int)a.dim; ++i) to[i] = acc[i];
     } else {
-        Raw<ZPQ_F32, E> o;
+        Raw<ZPQ_F32, E> o;                    // a piece that was moved back writes the same again
         o.set(acc);
-        o.template store<false>(to, (int64_t)group * a.dim + col);
+        o.template store<false>(to, col);
     }
 }
 
-// Reads of wave-uniform addresses through the scalar cache, of what earlier
-// launches wrote.
-template <class T>
-__device__ __forceinline__ T load_uniform(const T* p, int64_t i) {
-    typedef const T __attribute__((address_space(4))) scalar_t;
-    return reinterpret_cast<scalar_t*>(reinterpret_cast<uintptr_t>(p))[i];
-}
-
-// Piece `piece` of row `row`, whose tokens are the places [at, e) of the list;
-// UNIFORM: the same row in the whole wave.
-template <int DT, int OT, bool ADD, bool UNIFORM>
-__device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t piece, uint32_t at, uint32_t e) {
+// Rows: each lane sums its piece over the row's places [at, e) of the list.
+// BY_TOKEN: the rows are those that tokens name, each found at its first token; `first`
+// and the shares count tokens.
+template <int DT, int OT, bool ADD, bool BY_TOKEN, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first, Share share) {
     constexpr int E = piece_elems<DT, OT>();
-    const bool narrow = !UNIFORM && a.dim < E;         // a wave's 64 pieces are more than one
-    int64_t col = (int64_t)piece * E;
-    const int count = (int)(a.dim - col < E ? a.dim - col : E);    // elements this lane writes
-    if (!narrow && count < E) col = a.dim - E;
+    uint32_t r, col;
+    if (!my_share<WIDE, E>(share, blockIdx.x, r, col)) return;
+    int64_t row = first + r;
+    uint32_t at, e;
+    if constexpr (BY_TOKEN) {
+        at = (uint32_t)row;
+        row = (int64_t)(load_from<WIDE>(a.sorted, at) >> 32);
+        if (row >= a.rows || (at > 0 && (int64_t)(load_from<WIDE>(a.sorted, at - 1) >> 32) == row)) return;
+        e = load_from<WIDE>(a.starts, row + 1);
+    } else {
+        at = load_from<WIDE>(a.starts, row);
+        e = load_from<WIDE>(a.starts, row + 1);
+        if (ADD && at == e) return;
+    }
+    const bool narrow = !WIDE && a.dim < E;
+    const int count = piece_count<E>(a.dim, narrow, col);
+    if (count == 0) return;
+    void* grad = from<OT>(a.grad, row * a.ld_grad);
+    Raw<OT, E> old;
+    if constexpr (ADD) {                      // early: it depends on nothing below
+        if (!narrow) old.load(grad, col);
+        else old.load_some(grad, 0, count);
+    }
     float acc[E] = {};
 #pragma unroll 1
     while (at < e) {
@@ -478,10 +532,8 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
             // up to the next group that could be whole
             uint32_t stop = a.levels > 0 ? (at | ((1u << a.log) - 1)) + 1 : e;
             if (stop > e) stop = e;
-            add_rows<DT, E, kRowFlight<E>>(acc, stop - at, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
-                base = a.dy;
-                const uint64_t token = UNIFORM ? load_uniform(a.sorted, at + j) : a.sorted[at + j];
-                return (int64_t)(uint32_t)token * a.ld_dy + col;
+            add_rows<DT, E, kRowFlight>(acc, col, stop - at, narrow, (int)a.dim, [&](uint32_t j) {
+                return from<DT>(a.dy, (int64_t)(uint32_t)load_from<WIDE>(a.sorted, at + j) * a.ld_dy);
             });
             at = stop;
         } else {
@@ -492,74 +544,29 @@ __device__ __forceinline__ void row_sum(const GradArgs& a, int64_t row, uint32_t
                 const uint32_t next = (1u << a.log) - ((at >> shift) & ((1u << a.log) - 1));
                 if (next < groups) groups = next;
             }
-            const int64_t g0 = at >> shift;
-            const float* part = a.part[level - 1];
-            add_rows<ZPQ_F32, E, kRowFlight<E>>(acc, groups, narrow, (int)a.dim, [&](uint32_t j, const void*& base) {
-                base = part;
-                return (g0 + j) * a.dim + col;
+            const void* part = from<ZPQ_F32>((const void*)a.part[level - 1], (int64_t)(at >> shift) * a.dim);
+            add_rows<ZPQ_F32, E, kRowFlight>(acc, col, groups, narrow, (int)a.dim, [&](uint32_t j) {
+                return from<ZPQ_F32>(part, (int64_t)j * a.dim);
             });
             at += groups << shift;
         }
     }
-    const int64_t o = row * a.ld_grad + col;
-    if (!narrow) {
-        Raw<OT, E> old;
-        if constexpr (ADD) old.load(a.grad, o);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            acc[i] *= a.scale;
-            if constexpr (ADD) acc[i] = old.get(i) + acc[i];
-        }
-        if (count == E) {
-            Raw<OT, E> out;
-            out.set(acc);
-            out.store(a.grad, o);
-        } else {
+    for (int i = 0; i < E; ++i) {
+        acc[i] *= a.scale;
+        if constexpr (ADD) acc[i] = old.get(i) + acc[i];
+    }
+    Raw<OT, E> out;
+    out.set(acc);
+    if (count == E) {
+        out.store(grad, col);
+    } else if (narrow) {
+        out.store_some(grad, 0, count);
+    } else {                                  // the last elements of a piece that was moved back
 #pragma unroll
-            for (int i = 1; i < E; ++i)
-                if (i >= E - count) store1<OT>(a.grad, o + i, acc[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (i < count) {
-                float x = acc[i] * a.scale;
-                if constexpr (ADD) x = load1<OT>(a.grad, o + i) + x;
-                store1<OT>(a.grad, o + i, x);
-            }
+        for (int i = 1; i < E; ++i)
+            if (i >= E - count) store1<OT>(grad, (int64_t)col + i, acc[i]);
     }
-}
-
-// WIDE: a wave takes 64 pieces of one row, so that the row's places and positions
-// are scalar; `pieces` counts waves a row.  Otherwise lanes are dealt out row by
-// row, several rows a wave.  BY_TOKEN: the rows are those that tokens name, each found
-// at its first token; `first` and the lanes count tokens.
-template <int DT, int OT, bool ADD, bool WIDE, bool BY_TOKEN>
-__global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first, uint32_t lanes,
-                                                       Divisor pieces) {
-    const uint32_t lane = blockIdx.x * kThreads + threadIdx.x;
-    const uint32_t item = WIDE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(lane >> 6)) : lane;
-    if (item >= lanes) return;
-    const uint32_t r = quotient(item, pieces);
-    int64_t row = first + r;
-    uint32_t at, e;
-    auto get = [](const auto* p, int64_t i) { return WIDE ? load_uniform(p, i) : p[i]; };
-    if constexpr (BY_TOKEN) {
-        at = (uint32_t)row;
-        row = (int64_t)(get(a.sorted, at) >> 32);
-        if (row >= a.rows || (at > 0 && (int64_t)(get(a.sorted, at - 1) >> 32) == row)) return;
-        e = get(a.starts, row + 1);
-    } else {
-        at = get(a.starts, row);
-        e = get(a.starts, row + 1);
-        if (ADD && at == e) return;
-    }
-    uint32_t piece = item - r * pieces.d;
-    if constexpr (WIDE) {
-        piece = piece * 64 + (threadIdx.x & 63u);
-        if ((int64_t)piece * piece_elems<DT, OT>() >= a.dim) return;
-    }
-    row_sum<DT, OT, ADD, WIDE>(a, row, piece, at, e);
 }
 
 // ---------------------------------------------------------------------------
@@ -682,39 +689,47 @@ bool sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* coun
     return false;
 }
 
+// Workgroups of a share.
+inline unsigned share_blocks(const Share& s, bool wide) {
+    const unsigned items = wide ? kThreads / 64 : kThreads;
+    return s.items / items + (s.items % items != 0);
+}
+
+template <int DT, bool FIRST>
+void launch_group_level(const GradArgs& a, int32_t level, int64_t groups, uint32_t start_blocks, hipStream_t st) {
+    constexpr int E = FIRST ? piece_elems<DT, DT>() : 4;
+    const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
+    const bool wide = wide_rows(pieces);
+    const Share s = share_of(groups, pieces);
+    const dim3 grid(share_blocks(s, wide) + start_blocks), block(kThreads);
+    if (wide)
+        hipLaunchKernelGGL((k_group_sums<DT, FIRST, true>), grid, block, 0, st, a, level, start_blocks, s);
+    else
+        hipLaunchKernelGGL((k_group_sums<DT, FIRST, false>), grid, block, 0, st, a, level, start_blocks, s);
+}
 template <int DT>
 void launch_groups(const GradArgs& a, bool starts_done, hipStream_t st) {
     const uint32_t start_blocks = starts_done ? 0 : (uint32_t)(a.rows / kThreads + 1);
-    for (int l = 1; l <= (a.levels > 0 || starts_done ? a.levels : 1); ++l) {
-        const int E = l == 1 ? piece_elems<DT, DT>() : 4;
-        const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
-        const uint32_t lanes = l <= a.levels ? (a.tokens >> (a.log * l)) * pieces : 0;
-        const unsigned blocks = lanes / kThreads + (lanes % kThreads != 0);
-        if (l == 1)
-            hipLaunchKernelGGL((k_group_sums<DT, true>), dim3(blocks + start_blocks), dim3(kThreads), 0, st, a, l,
-                               lanes, start_blocks, divisor(pieces));
-        else
-            hipLaunchKernelGGL((k_group_sums<DT, false>), dim3(blocks), dim3(kThreads), 0, st, a, l, lanes, 0,
-                               divisor(pieces));
-    }
+    if (a.levels > 0 || start_blocks > 0)
+        launch_group_level<DT, true>(a, 1, a.levels > 0 ? a.tokens >> a.log : 0, start_blocks, st);
+    for (int l = 2; l <= a.levels; ++l) launch_group_level<DT, false>(a, l, a.tokens >> (a.log * l), 0, st);
 }
+
+// In launches of at most 2^30 lanes.
 template <int DT, int OT, bool ADD, bool BY_TOKEN>
 void launch_rows(const GradArgs& a, hipStream_t st) {
     constexpr int E = piece_elems<DT, OT>();
     const uint32_t pieces = (uint32_t)((a.dim + E - 1) / E);
-    const bool wide = pieces >= 33;
-    const uint32_t per_row = wide ? (pieces + 63) / 64 : pieces;
-    const int64_t some = (1 << (wide ? 24 : 30)) / per_row;       // rows a launch: at most 2^30 lanes
+    const bool wide = wide_rows(pieces);
     const int64_t all = BY_TOKEN ? a.tokens : a.rows;
+    const int64_t some = (wide ? 1 << 24 : 1 << 30) / share_of(1, pieces).items;
     for (int64_t first = 0; first < all; first += some) {
-        const uint32_t n = (uint32_t)((all - first < some ? all - first : some) * per_row);
+        const Share s = share_of(all - first < some ? all - first : some, pieces);
+        const dim3 grid(share_blocks(s, wide)), block(kThreads);
         if (wide)
-            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, true, BY_TOKEN>), dim3(n / 4 + (n % 4 != 0)),
-                               dim3(kThreads), 0, st, a, first, n, divisor(per_row));
+            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, BY_TOKEN, true>), grid, block, 0, st, a, first, s);
         else
-            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, false, BY_TOKEN>),
-                               dim3(n / kThreads + (n % kThreads != 0)), dim3(kThreads), 0, st, a, first, n,
-                               divisor(per_row));
+            hipLaunchKernelGGL((k_row_sums<DT, OT, ADD, BY_TOKEN, false>), grid, block, 0, st, a, first, s);
     }
 }
 template <int DT, int OT>
