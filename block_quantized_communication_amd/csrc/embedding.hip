@@ -36,7 +36,7 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int32_t id_bytes, in
 }
 
 // ---------------------------------------------------------------------------
-// Lookup.  Lane L of the grid takes piece L % pieces of token L / pieces.
+// Lookup.  Number L of the grid's lanes is piece L % pieces of token L / pieces.
 struct LookupArgs {
     const void* table;
     const float* scales;
@@ -49,9 +49,13 @@ struct LookupArgs {
     Divisor pieces;
 };
 
-template <int TT, int OT, int U>
+// Two pieces a lane: the way from id to row to store takes about 3 us, so the waves
+// in flight have to carry more than one access each (16,384 x 8192: INT8 to bf16 55 us
+// with one, 49 with two, 55 with four; bf16 82, 66, 64; fp32 to bf16 124, 98, 90).
+constexpr int kLookupPieces = 2;
+template <int TT, int OT>
 __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a) {
-    constexpr int E = piece_elems<TT, OT>();
+    constexpr int E = piece_elems<TT, OT>(), U = kLookupPieces;
     uint32_t lane[U], token[U];
     int64_t row[U];
     int32_t col[U];
@@ -585,8 +589,8 @@ void launch_lookup(LookupArgs a, hipStream_t st) {
         a.ids = ids + t * a.id_bytes;
         a.out = out + t * a.ld_out * elem_bytes<OT>();
         a.lanes = (uint32_t)(n * pieces);
-        const unsigned grid = (a.lanes + kThreads - 1) / kThreads;
-        hipLaunchKernelGGL((k_lookup<TT, OT, 1>), dim3(grid), dim3(kThreads), 0, st, a);
+        const unsigned grid = (a.lanes + kLookupPieces * kThreads - 1) / (kLookupPieces * kThreads);
+        hipLaunchKernelGGL((k_lookup<TT, OT>), dim3(grid), dim3(kThreads), 0, st, a);
     }
 }
 template <int TT>
