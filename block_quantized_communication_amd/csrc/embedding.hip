@@ -145,7 +145,8 @@ __device__ __forceinline__ uint32_t key_of(const Ids& a, uint32_t t) {
 // lane; its waves share the others, 64 at a time through LDS (a broadcast read
 // gives 4, and each is one compare and one add with carry for 64 tokens).  Where
 // rows are few as well, further workgroups count the same way what comes before each
-// row: its first place.
+// row: its first place.  300 tokens 3.8 us, 8000 13 us; 16,384 would take 25, with the
+// radix sort 22.
 constexpr uint32_t kRankTokens = 8192;
 constexpr int kRankWaves = 16;
 __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __restrict__ out,
@@ -197,7 +198,9 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __res
 // More tokens: a radix sort from the lowest digit, `bits` (at most 9) a pass, stable by
 // construction.  k_digit_counts counts each tile's digits; k_digit_place gives every
 // token its place: tokens with smaller digits, the same digit in earlier tiles, in
-// earlier waves of the tile, and earlier in its wave (found by ballots).
+// earlier waves of the tile, and earlier in its wave (found by ballots).  131,072
+// tokens 4.7 and 9.8 us a pass, 16,384 4.7 and 6.3: latency, of the launches and of a few
+// dependent accesses.
 constexpr int kMaxDigits = 512, kSortThreads = 512, kSortTile = 4 * kSortThreads;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kDirectTiles = 64;         // up to this many tiles their counts are summed in place
@@ -449,7 +452,8 @@ __device__ __forceinline__ uint32_t lower_bound(const uint64_t* __restrict__ s, 
     return lo;
 }
 
-// Level `level` sums of whole groups that lie within one row.  On level 1 the
+// Level `level` sums of whole groups that lie within one row: 39 us of 195 for 131,072 x
+// 2048 (200 MB read), 17 of 205 for 16,384 x 8192.  On level 1 the
 // workgroups from `start_blocks` on; those before find the rows' first places, a row a
 // lane.
 template <int DT, bool FIRST, bool WIDE>
@@ -495,7 +499,11 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
     }
 }
 
-// Rows: each lane sums its piece over the row's places [at, e) of the list.
+// Rows: each lane sums its piece over the row's places [at, e) of the list.  Rows without
+// a token are written at 6.6 TB/s (non-temporal stores; plain ones 4.5); where rows have
+// a few tokens each the chain of place, token, dy and store is what takes the time, and
+// the waves in flight: 168 us for 16,384 x 8192 into 50,021 rows of bf16 (1.03 GB), 130 us
+// for 131,072 x 2048 added to 65,536 rows of fp32 (762 MB).
 // BY_TOKEN: the rows are those that tokens name, each found at its first token; `first`
 // and the shares count tokens.
 template <int DT, int OT, bool ADD, bool BY_TOKEN, bool WIDE>
