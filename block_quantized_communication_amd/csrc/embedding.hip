@@ -151,7 +151,7 @@ constexpr uint32_t kRankTokens = 8192;
 constexpr int kRankWaves = 16;
 __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __restrict__ out,
                                                           uint32_t* __restrict__ starts) {
-    __shared__ uint32_t keys[kRankWaves][64];
+    __shared__ __align__(16) uint32_t keys[kRankWaves][64];
     __shared__ uint32_t counts[kRankWaves][64];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint32_t blocks = (a.tokens + 63) / 64;
@@ -619,8 +619,8 @@ zpq_status rows_ok(int64_t rows, int64_t tokens, int64_t dim, int64_t ld_a, int6
     if (rows < 0 || rows > kMaxRows || tokens < 0 || tokens > kMaxRows || dim < 1 || dim > (1 << 30) ||
         ld_a < dim || ld_b < dim || ld_a > kMaxElems || ld_b > kMaxElems)
         return ZPQ_ERR_SIZE;
-    // element offsets within 2^62
-    if ((rows > 0 && ld_a > (1LL << 62) / rows) || (tokens > 0 && ld_b > (1LL << 62) / tokens))
+    // element offsets within 2^60, bytes within 2^62
+    if ((rows > 0 && ld_a > (1LL << 60) / rows) || (tokens > 0 && ld_b > (1LL << 60) / tokens))
         return ZPQ_ERR_SIZE;
     return ZPQ_OK;
 }
@@ -849,9 +849,11 @@ zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, c
     auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
     uint64_t* list = reinterpret_cast<uint64_t*>(ws + w.sorted[0]);
     uint64_t* other = reinterpret_cast<uint64_t*>(ws + w.sorted[1]);
-    const bool starts_done = sort_tokens(Ids{ids, first, padding, rows, id_bytes, (uint32_t)tokens}, list, other, words(w.counts),
-                words(w.totals), words(w.starts), st);
-    GradArgs a = {list, dy, grad, words(w.starts), {}, ld_dy, ld_grad, dim, rows, (uint32_t)tokens, w.levels, w.log, scale};
+    const Ids sorted = {ids, first, padding, rows, id_bytes, (uint32_t)tokens};
+    const bool starts_done = sort_tokens(sorted, list, other, words(w.counts), words(w.totals),
+                                         words(w.starts), st);
+    GradArgs a = {list, dy, grad, words(w.starts), {}, ld_dy, ld_grad, dim, rows, (uint32_t)tokens,
+                  w.levels, w.log, scale};
     for (int l = 0; l < w.levels; ++l) a.part[l] = reinterpret_cast<float*>(ws + w.part[l]);
     if (dy_dtype == ZPQ_F32) launch_grad<ZPQ_F32>(a, grad_dtype, accumulate != 0, starts_done, st);
     else if (dy_dtype == ZPQ_F16) launch_grad<ZPQ_F16>(a, grad_dtype, accumulate != 0, starts_done, st);

@@ -324,6 +324,23 @@ def test_more_than_2_to_32_elements():
     assert not bool(p[: 1 << 20].any()) and not bool(opt.exp_avg_sq[0][0][: 1 << 20].any())
 
 
+def test_random_numbers_cross_2_to_32_between_waves():
+    """A tensor whose counters pass 2^32 in its third block, inside a part."""
+    import torch
+    big, n = (1 << 32) - 512, 2000
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    p = [torch.zeros(big, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")]
+    g = [torch.zeros(big, dtype=torch.bfloat16, device="cuda"),
+         torch.randn(n, generator=gen, device="cuda").bfloat16()]
+    opt = zpq.AdamW(p, g, state_bits=8, seed=11, **HYPER)
+    opt.step(2)
+    ms, vs = ref.adamw32_moments(host(g[1]), np.zeros(n), np.zeros(n), 1.0, HYPER["betas"])
+    r = ref.random32(big, n, 11, 2)
+    for x, moment, rnd, (codes, exps) in ((ms, 1, r & 0xFFFF, opt.exp_avg[1]), (vs, 2, r >> 16, opt.exp_avg_sq[1])):
+        want_c, want_e = ref.encode8(x, moment, rnd)
+        assert np.array_equal(exps.cpu().numpy(), want_e) and np.array_equal(codes.cpu().numpy(), want_c)
+
+
 def test_captured_step_replays_equal_eager():
     import torch
     d, e = make([70000, 33], bits=8, seed=4), make([70000, 33], bits=8, seed=4)

@@ -105,18 +105,29 @@ def test_lookup_int8(out, block, rows, dim):
 
 
 def test_lookup_past_32_bits():
-    """Table and output offsets beyond 2^32 elements."""
+    """Table and output offsets beyond 2^32 elements, more lanes than one launch
+    takes."""
     import torch
-    rows, dim = (1 << 20) + 8, 4096
+    rows, dim, n = (1 << 20) + 8, 4096, (1 << 21) + 3
     codes = torch.zeros(rows * dim, dtype=torch.int8, device="cuda")
     scales = torch.full((rows * dim // 256,), 0.5, device="cuda")
     codes.view(rows, dim)[-1] = 3
     codes.view(rows, dim)[1] = 5
-    t = torch.full(((1 << 20) + 3,), rows - 1, device="cuda")
+    t = torch.full((n,), rows - 1, device="cuda")
     t[:2] = 1
+    t[-2] = 1
     y = zpq.embedding_i8(t, codes, scales, rows, dim, scale=2.0)
-    assert bool((y[:2] == 5).all()) and bool((y[2] == 3).all()) and bool((y[-1] == 3).all())
-    assert int((y[:, 0] != 3).sum()) == 2
+    assert bool((y[:2] == 5).all()) and bool((y[-2] == 5).all()) and bool((y[-1] == 3).all())
+    assert int((y[:, 0] != 3).sum()) == 3 and int((y[:, -1] != 3).sum()) == 3
+
+
+def test_lookup_without_rows():
+    import torch
+    t = torch.arange(5, device="cuda")
+    y = zpq.embedding(t, torch.empty(0, 24, device="cuda").half())
+    assert y.shape == (5, 24) and not bool(y.any())
+    y = zpq.embedding_i8(t, torch.empty(0, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda"), 0, 24)
+    assert y.shape == (5, 24) and not bool(y.any())
 
 
 def terms_off(n):
@@ -292,7 +303,7 @@ def test_other_stream_and_graph():
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("tokens,rows,dim", [(53280, 4, 24), (8192, 2048, 12), (8192, 2049, 12), (8193, 3, 520),
                                              (511, 70, 9), (512, 70, 9), (20000, 90000, 132), (300000, 5, 7),
-                                             (3000, 40, 12000), (2500, 200000, 3)])
+                                             (3000, 40, 12000), (2500, 200000, 3), (9000, 300000, 6)])
 def test_grad_sizes_of_the_sums(tokens, rows, dim, accumulate):
     """Both sides of the rules on group sizes and levels, on where the rows' places
     are found and on launches over tokens: exact sums of small integers."""
@@ -308,9 +319,9 @@ def test_grad_sizes_of_the_sums(tokens, rows, dim, accumulate):
 
 
 def test_grad_past_32_bits():
-    """dy and the gradient beyond 2^32 elements."""
+    """dy and the gradient beyond 2^32 elements, more waves than one launch takes."""
     import torch
-    rows = tokens = (1 << 20) + 9
+    rows = tokens = (1 << 21) + 9
     dim = 4100
     y = torch.zeros(tokens, dim, dtype=torch.bfloat16, device="cuda")
     y[-1], y[-2], y[3] = 3.0, 5.0, 7.0
@@ -321,3 +332,14 @@ def test_grad_past_32_bits():
     assert bool((g[-1] == 10).all()) and bool((g[-2] == 5).all()) and not bool(g[:-2].any())
     zpq.embedding_grad(t, y, rows, out=g, accumulate=True)
     assert bool((g[-1] == 20).all()) and bool((g[-2] == 10).all()) and not bool(g[5:9].any())
+
+
+def test_grad_of_more_lanes_than_one_launch():
+    """Short rows, dealt out lane by lane."""
+    import torch
+    rows, dim = (1 << 26) + 5, 136
+    t = torch.tensor([rows - 1, 0, rows - 1, 1 << 25, rows - 2], device="cuda")
+    y = torch.arange(1, 6, device="cuda").bfloat16()[:, None].expand(5, dim).contiguous()
+    g = zpq.embedding_grad(t, y, rows)
+    assert bool((g[-1] == 4).all()) and bool((g[0] == 2).all()) and bool((g[1 << 25] == 4).all())
+    assert bool((g[-2] == 5).all()) and not bool(g[1:1 << 25].any()) and not bool(g[(1 << 25) + 1:-2].any())
