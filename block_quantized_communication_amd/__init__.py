@@ -524,7 +524,8 @@ def state8_unpack(codes, exps, moment, dtype=None, out=None, stream=None):
     torch = _torch()
     dev = _gpu(codes, "codes")
     n = codes.numel()
-    _need(codes, torch.uint8, n, "codes", dev)
+    if codes.dtype != torch.uint8:
+        raise ValueError(f"codes: need uint8, got {codes.dtype}")
     _need(exps, torch.uint8, -(-n // STATE_BLOCK), "exps", dev)
     st, ctx = _on(stream, dev)
     with ctx:
@@ -565,18 +566,27 @@ def _ids(ids):
     raise ValueError(f"ids: need int32 or int64, got {ids.dtype}")
 
 
-def _rows(t, name, device, rows=None, dim=None):
+def _rows(t, name, device):
     """t as rows: a 2-D tensor on `device` whose rows are contiguous (they may
-    lie further apart); returns the distance."""
-    if t.dim() != 2 or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: need a 2-D tensor on {device} with contiguous rows, got "
-                         f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
-    n, d = t.shape
-    if (rows is not None and n != rows) or (dim is not None and d != dim):
+    lie further apart); returns (rows, dim, distance of rows)."""
+    if t.dim() == 2 and t.device == device:
+        n, d = t.shape
+        ld, step = t.stride()
+        if step == 1 or d <= 1:
+            if n <= 1:
+                return n, d, d
+            if ld >= d:
+                return n, d, ld
+            raise ValueError(f"{name}: rows overlap (strides {tuple(t.stride())})")
+    raise ValueError(f"{name}: need a 2-D tensor on {device} with contiguous rows, got "
+                     f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+
+
+def _rows_of(t, name, device, rows, dim):
+    """The distance of t's rows; t must be [rows, dim]."""
+    n, d, ld = _rows(t, name, device)
+    if n != rows or d != dim:
         raise ValueError(f"{name}: need {rows} x {dim}, got {tuple(t.shape)}")
-    ld = t.stride(0) if n > 1 else d
-    if ld < d:
-        raise ValueError(f"{name}: rows overlap (strides {tuple(t.stride())})")
     return ld
 
 
@@ -584,7 +594,7 @@ def _lookup_out(ids, dim, out, dtype, dev):
     """(output, distance of its rows)."""
     if out is None:
         return _torch().empty(ids.shape + (dim,), dtype=dtype, device=dev), dim
-    return out, _rows(out if out.dim() == 2 else out.view(-1, out.shape[-1]), "out", dev, ids.numel(), dim)
+    return out, _rows_of(out if out.dim() == 2 else out.view(-1, out.shape[-1]), "out", dev, ids.numel(), dim)
 
 
 def embedding(ids, table, scale=1.0, first=0, out_dtype=None, out=None, stream=None):
@@ -592,8 +602,7 @@ def embedding(ids, table, scale=1.0, first=0, out_dtype=None, out=None, stream=N
     not a row (padding, another shard's rows).  table [rows, dim]: float32,
     float16 or bfloat16, rows may lie apart."""
     dev, ib = _ids(ids)
-    ld = _rows(table, "table", dev)
-    rows, dim = table.shape
+    rows, dim, ld = _rows(table, "table", dev)
     st, ctx = _on(stream, dev)
     with ctx:
         out, lo = _lookup_out(ids, dim, out, out_dtype or table.dtype, dev)
@@ -643,13 +652,14 @@ def embedding_grad(ids, dy, rows, scale=1.0, first=0, padding=None, out_dtype=No
     if dy.dim() != 2:
         _gpu(dy, "dy", dev)
         dy = dy.view(-1, dy.shape[-1])
-    n, dim = ids.numel(), dy.shape[1]
-    ld = _rows(dy, "dy", dev, n, dim)
+    n, dim, ld = _rows(dy, "dy", dev)
+    if n != ids.numel():
+        raise ValueError(f"dy: need {ids.numel()} rows, got {n}")
     need = _grad_bytes(n, rows, dim)
     st, ctx = _on(stream, dev)
     with ctx:
         if out is not None:
-            lo = _rows(out, "out", dev, rows, dim)
+            lo = _rows_of(out, "out", dev, rows, dim)
         elif accumulate:
             raise ValueError("accumulate needs out")
         else:

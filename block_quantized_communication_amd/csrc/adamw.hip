@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
     // are carried out where all XCDs' accesses meet, and one whose old value has come
     // back is done.  So a workgroup counts itself (waiting for its exchange) after
     // its sum can be read by all, and the one that counts to the end reads every sum.
-    // Counting is in groups of 32, then the groups: with one count for 2048 workgroups
+    // Counting is in groups of 32 (where there are more), then the groups: with one count for 2048 workgroups
     // 50.3 M elements took 36 us, so 21, and 23 with a second launch to join.  (A release
     // and an acquire write back and invalidate the L2 for each workgroup: 107 us.)
     __shared__ bool last;
@@ -162,7 +162,8 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
         asm volatile("s_waitcnt vmcnt(0)" : "+v"(old) : : "memory");
         const uint32_t g = blockIdx.x / kSumGroup, groups = (gridDim.x + kSumGroup - 1) / kSumGroup;
         const uint32_t members = g + 1 < groups ? kSumGroup : gridDim.x - g * kSumGroup;
-        last = count_to(&head->group[g].n, members) && count_to(&head->all.n, groups);
+        last = groups == 1 ? count_to(&head->all.n, gridDim.x)
+                           : count_to(&head->group[g].n, members) && count_to(&head->all.n, groups);
     }
     __syncthreads();
     if (!last) return;

@@ -199,10 +199,11 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __res
 // construction.  k_digit_counts counts each tile's digits; k_digit_place gives every
 // token its place: tokens with smaller digits, the same digit in earlier tiles, in
 // earlier waves of the tile, and earlier in its wave (found by ballots).  131,072
-// tokens 4.7 and 9.8 us a pass, 16,384 4.7 and 6.3: latency, of the launches and of a few
+// tokens 4.9 and 8.4 us a pass, 16,384 4.7 and 5.7: latency, of the launches and of a few
 // dependent accesses.
 constexpr int kMaxDigits = 512, kSortThreads = 512, kSortTile = 4 * kSortThreads;
 constexpr int kSortWaves = kSortThreads / 64;
+static_assert(kSortThreads == kMaxDigits, "a digit a thread");
 constexpr uint32_t kDirectTiles = 64;         // up to this many tiles their counts are summed in place
 
 struct Pass {
@@ -221,7 +222,7 @@ template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void k_digit_counts(Ids a, const uint64_t* __restrict__ in,
                                                                Pass p, uint32_t* __restrict__ counts) {
     __shared__ uint32_t n[kMaxDigits];
-    if (threadIdx.x < kMaxDigits) n[threadIdx.x] = 0;
+    n[threadIdx.x] = 0;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kSortTile / kSortThreads; ++k) {
@@ -260,7 +261,7 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint6
                                                               const uint32_t* __restrict__ totals,
                                                               uint64_t* __restrict__ out) {
     __shared__ uint32_t seen[kSortWaves][kMaxDigits];      // of each wave, then before each wave
-    __shared__ uint32_t scan[2][kMaxDigits];
+    __shared__ uint32_t waves[kSortWaves];                 // totals of 64 digits each
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     constexpr int kEach = kSortTile / kSortThreads;
     uint64_t x[kEach];
@@ -271,17 +272,19 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint6
         x[k] = t < a.tokens ? sort_item<FIRST>(a, in, t) : ~0ull;
     }
     for (uint32_t i = lane; i < kMaxDigits; i += 64) seen[wave][i] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
     // the digit's share of earlier tiles, and its total
     uint32_t total = 0, earlier = 0;
     if (threadIdx.x < (1u << p.bits)) {
         const uint32_t* row = counts + threadIdx.x;
         if (p.tiles <= kDirectTiles) {
-            for (uint32_t b = 0; b < p.tiles; b += 16) {
-                uint32_t n[16];               // loaded together
+            for (uint32_t b = 0; b < p.tiles; b += 32) {
+                uint32_t n[32];               // loaded together
 #pragma unroll
-                for (uint32_t u = 0; u < 16; ++u) n[u] = b + u < p.tiles ? row[(b + u) << p.bits] : 0;
+                for (uint32_t u = 0; u < 32; ++u) n[u] = b + u < p.tiles ? row[(b + u) << p.bits] : 0;
 #pragma unroll
-                for (uint32_t u = 0; u < 16; ++u) {
+                for (uint32_t u = 0; u < 32; ++u) {
                     total += n[u];
                     earlier += b + u < blockIdx.x ? n[u] : 0;
                 }
@@ -291,8 +294,14 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint6
             earlier = row[(uint64_t)blockIdx.x << p.bits];
         }
     }
-    if (threadIdx.x < kMaxDigits) scan[0][threadIdx.x] = total;
-    __syncthreads();
+    // exclusive sum of the totals over the digits, a digit a thread: within the wave ...
+    uint32_t sum = total;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(sum, d);
+        if ((int)lane >= d) sum += y;
+    }
+    if (lane == 63) waves[wave] = sum;
     const uint64_t lower = (1ull << lane) - 1;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
@@ -311,24 +320,16 @@ __global__ __launch_bounds__(kSortThreads) void k_digit_place(Ids a, const uint6
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
-    // exclusive sums: over the digits of the totals, over the waves of a digit
-    int from = 0;
-    for (int d = 1; d < (1 << p.bits); d <<= 1) {
-        if (threadIdx.x < kMaxDigits)
-            scan[from ^ 1][threadIdx.x] =
-                scan[from][threadIdx.x] + ((int)threadIdx.x >= d ? scan[from][threadIdx.x - d] : 0);
-        from ^= 1;
-        __syncthreads();
-    }
-    __syncthreads();                          // the waves' counts
-    if (threadIdx.x < kMaxDigits) {
-        uint32_t at = scan[from][threadIdx.x] - total + earlier;
+    __syncthreads();
+    // ... and over the waves; then over the tile's waves of each digit
+    uint32_t at = sum - total + earlier;
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
-            const uint32_t n = seen[w][threadIdx.x];
-            seen[w][threadIdx.x] = at;
-            at += n;
-        }
+    for (uint32_t w = 0; w < kSortWaves; ++w) at += w < wave ? waves[w] : 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t n = seen[w][threadIdx.x];
+        seen[w][threadIdx.x] = at;
+        at += n;
     }
     __syncthreads();
 #pragma unroll
