@@ -2,7 +2,7 @@
 // clips by, and the 8-bit states' conversions.
 //
 // One launch covers all tensors: a table in device memory (written by
-// k_fill_* from kernel arguments, so that it is ordered with the stream, can be
+// k_fill from kernel arguments, so that it is ordered with the stream, can be
 // captured and needs no host memory to outlive the call) lists the tensors
 // and where each one's share of workgroups starts; a workgroup finds its
 // tensor by one or two 64-lane looks (find_start).
@@ -126,25 +126,26 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
         while (k >= starts[t + 1]) ++t;       // starts[count] = chunks > k: ends
         const ListEntry e = entries[t];
         const int64_t at = (int64_t)(k - starts[t]) * kSumChunk;
+        constexpr int E = kSumEach<DT>, N = kSumChunk / (kThreads * E);
+        Raw<DT, E> r[N];
         if (at + kSumChunk <= e.n) {
-            constexpr int E = kSumEach<DT>, N = kSumChunk / (kThreads * E);
-            Raw<DT, E> r[N];
 #pragma unroll
             for (int u = 0; u < N; ++u) r[u].template load<!KEEP>(e.ptr, at + (u * kThreads + threadIdx.x) * E);
-#pragma unroll
-            for (int u = 0; u < N; ++u)
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const double x = (double)r[u].get(i);
-                    s[i & 3] = __builtin_fma(x, x, s[i & 3]);
-                }
         } else {
-            const int64_t end = at + kSumChunk < e.n ? at + kSumChunk : e.n;
-            for (int64_t i = at + threadIdx.x; i < end; i += kThreads) {
-                const double x = (double)load1<DT>(e.ptr, i);
-                s[0] = __builtin_fma(x, x, s[0]);
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                const int64_t i = at + (u * kThreads + threadIdx.x) * E, left = e.n - i;
+                if (left >= E) r[u].template load<!KEEP>(e.ptr, i);
+                else r[u].load_some(e.ptr, i, left > 0 ? (int)left : 0);
             }
         }
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const double x = (double)r[u].get(i);
+                s[i & 3] = __builtin_fma(x, x, s[i & 3]);
+            }
     }
     const double sum = wg_sum((s[0] + s[1]) + (s[2] + s[3]));
     // The workgroup that finishes last adds the partial sums, always in the same
@@ -152,9 +153,10 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
     // are carried out where all XCDs' accesses meet, and one whose old value has come
     // back is done.  So a workgroup counts itself (waiting for its exchange) after
     // its sum can be read by all, and the one that counts to the end reads every sum.
-    // Counting is in groups of 32 (where there are more), then the groups: with one count for 2048 workgroups
-    // 50.3 M elements took 36 us, so 21, and 23 with a second launch to join.  (A release
-    // and an acquire write back and invalidate the L2 for each workgroup: 107 us.)
+    // Counting is in groups of 32 (where there are more), then the groups: with one count
+    // for 2048 workgroups 50.3 M elements took 36 us, so 21, and 23 with a second launch to
+    // join.  (A release and an acquire write back and invalidate the L2 for each workgroup:
+    // 107 us.)
     __shared__ bool last;
     if (threadIdx.x == 0) {
         unsigned long long old = __hip_atomic_exchange(&head->part[blockIdx.x], __double_as_longlong(sum),
@@ -181,9 +183,7 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
         for (int u = 0; u < 8; ++u) all += __longlong_as_double((long long)x[u]);
     }
     all = wg_sum(all);
-    if (threadIdx.x == 0) {
-        out[0] = accumulate ? out[0] + all : all;
-    }
+    if (threadIdx.x == 0) out[0] = accumulate ? out[0] + all : all;
 }
 
 __global__ void k_zero(double* out) { out[0] = 0.0; }
