@@ -25,6 +25,7 @@ Around the communication path (tensors need their element's alignment only):
   embedding(ids, table, scale)               -> scaled rows; embedding_i8: from qwZ codes and scales
   embedding_grad(ids, dy, rows, scale)       -> dense gradient of the table
 """
+import bisect
 import contextlib
 import ctypes
 import functools
@@ -338,26 +339,28 @@ def _one_dtype(tensors, name):
 class TensorList:
     """Tensors of one type on one GPU, laid out once for grad_sumsq.  Keeps the
     tensors; their storage must not be replaced (set_, resize_) meanwhile.  The
-    list's table also holds the partial sums of the call that runs: one call at
-    a time, in stream order."""
+    table is written on `stream` (the current one by default) and also holds the
+    partial sums of the call that runs: later calls must come after it and one
+    after the other, in stream order."""
 
     def __init__(self, tensors, stream=None):
-        torch = _torch()
         self.tensors = list(tensors)
         if not self.tensors:
             raise ValueError("tensors: need at least one")
         self.device = _one_device(self.tensors, "tensors")
-        dt = _one_dtype(self.tensors, "tensors")
-        n = len(self.tensors)
-        ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
-        sizes = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
+        self._lay_out([t.data_ptr() for t in self.tensors], [t.numel() for t in self.tensors],
+                      _one_dtype(self.tensors, "tensors"), stream)
+
+    def _lay_out(self, ptrs, sizes, dt, stream):
+        n = len(ptrs)
         st, ctx = _on(stream, self.device)
         self._c = _List()
         self._ref = ctypes.byref(self._c)
         with ctx:
-            self._table = torch.empty(n * 32 + LIST_FIXED_BYTES, dtype=torch.uint8, device=self.device)
-            _check(lib().zpq_list_make(ptrs, sizes, n, dt, self._table.data_ptr(), self._table.numel(),
-                                       self._ref, st), "zpq_list_make")
+            self._table = _torch().empty(n * 32 + LIST_FIXED_BYTES, dtype=_torch().uint8, device=self.device)
+            _check(lib().zpq_list_make((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), n, dt,
+                                       self._table.data_ptr(), self._table.numel(), self._ref, st),
+                   "zpq_list_make")
 
 
 def grad_sumsq(tensors, out=None, accumulate=False, stream=None):
@@ -390,8 +393,9 @@ class AdamW:
                   uint8 [n], exponents uint8 [ceil(n / 256)]); zeros are made where not given
     seed          of the random rounding of 8-bit states
 
-    Tensors are kept and their addresses laid out once: storage must not be
-    replaced meanwhile; set_grads() takes other gradients."""
+    Tensors are kept and their addresses laid out once, on `stream` (the current
+    one by default; later calls must come after it in stream order): storage must
+    not be replaced meanwhile; set_grads() takes other gradients."""
 
     def __init__(self, params, grads, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, state_bits=32, exp_avg=None, exp_avg_sq=None, seed=0, stream=None):
@@ -419,24 +423,27 @@ class AdamW:
             self.exp_avg = self._state(exp_avg, "exp_avg")
             self.exp_avg_sq = self._state(exp_avg_sq, "exp_avg_sq")
             self._table = torch.empty(count * 128 + 64, dtype=torch.uint8, device=self.device)
-        self.set_grads(grads, stream=stream)
-
-    def _check_apart(self, grads):
-        """No memory that the step writes may be written or read through another
-        tensor (tied weights count once)."""
-        spans = []
-        flat = lambda xs: [y for x in xs for y in (x if isinstance(x, tuple) else (x,))]  # noqa: E731
-        for written, ts in ((True, flat(self.params + (self.copies or []) + self.exp_avg + self.exp_avg_sq)),
-                            (False, grads)):
-            spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), written) for t in ts if t.numel()]
+        self._sizes = [p.numel() for p in self.params]
+        self._rows = (_AdamwTensor * count)()
+        spans = []                                     # of what the step writes
+        for i, (r, p) in enumerate(zip(self._rows, self.params)):
+            m, v = self.exp_avg[i], self.exp_avg_sq[i]
+            written = [p] if self.copies is None else [p, self.copies[i]]
+            if self.state_bits == 8:
+                (m, me), (v, ve) = m, v
+                r.m_exp, r.v_exp = me.data_ptr(), ve.data_ptr()
+                written += [me, ve]
+            r.p, r.m, r.v, r.n = p.data_ptr(), m.data_ptr(), v.data_ptr(), self._sizes[i]
+            if self.copies is not None:
+                r.copy = self.copies[i].data_ptr()
+            r.weight_decay = self.weight_decay[i]
+            if self._sizes[i]:
+                spans += [(a, a + t.numel() * t.element_size()) for t in written + [m, v] for a in (t.data_ptr(),)]
         spans.sort()
-        any_end = written_end = 0
-        for lo, hi, written in spans:
-            if lo < (any_end if written else written_end):
-                raise ValueError("params, copies, moments and grads overlap in memory")
-            any_end = max(any_end, hi)
-            if written:
-                written_end = max(written_end, hi)
+        self._starts, self._ends = [a for a, _ in spans], [b for _, b in spans]
+        if any(b > a for b, a in zip(self._ends, self._starts[1:])):
+            raise ValueError("params, copies and moments overlap in memory (tied weights are one tensor)")
+        self.set_grads(grads, stream=stream)
 
     def _match(self, tensors, name):
         if len(tensors) != len(self.params):
@@ -469,30 +476,28 @@ class AdamW:
         return given
 
     def set_grads(self, grads, stream=None):
-        """Take these gradients from the next call on."""
+        """Take these gradients from the next call on (in stream order)."""
         grads = list(grads)
         self._match(grads, "grads")
         gd = _one_dtype(grads, "grads")
-        self._check_apart(grads)
-        count = len(self.params)
-        rows = (_AdamwTensor * count)()
-        for i, (r, p, g) in enumerate(zip(rows, self.params, grads)):
-            m, v = self.exp_avg[i], self.exp_avg_sq[i]
-            if self.state_bits == 8:
-                (m, me), (v, ve) = m, v
-                r.m_exp, r.v_exp = me.data_ptr(), ve.data_ptr()
-            r.p, r.g, r.m, r.v, r.n = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), p.numel()
-            if self.copies is not None:
-                r.copy = self.copies[i].data_ptr()
-            r.weight_decay = self.weight_decay[i]
+        width = grads[0].element_size()
+        ptrs = [g.data_ptr() for g in grads]
+        starts, ends = self._starts, self._ends
+        for r, a, n in zip(self._rows, ptrs, self._sizes):
+            r.g = a
+            j = bisect.bisect_right(starts, a)
+            if n and ((j and ends[j - 1] > a) or (j < len(starts) and starts[j] < a + n * width)):
+                raise ValueError("grads overlap what the step writes")
         st, ctx = _on(stream, self.device)
         plan = _AdamwPlan()
         with ctx:
-            _check(lib().zpq_adamw_plan_make(rows, count, self._pd, gd, self._cd, self.state_bits,
+            _check(lib().zpq_adamw_plan_make(self._rows, len(grads), self._pd, gd, self._cd, self.state_bits,
                                              self._table.data_ptr(), self._table.numel(), ctypes.byref(plan), st),
                    "zpq_adamw_plan_make")
             self._plan, self._ref, self.grads = plan, ctypes.byref(plan), grads
-            self._list = TensorList(grads, stream=stream)
+            self._list = TensorList.__new__(TensorList)
+            self._list.tensors, self._list.device = grads, self.device
+            self._list._lay_out(ptrs, self._sizes, gd, stream)
 
     def grad_sumsq(self, out=None, accumulate=False, stream=None):
         """Sum of squares of the gradients -> float64 [1] (see grad_sumsq)."""

@@ -431,8 +431,9 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict_
 
 // ---------------------------------------------------------------------------
 // 8-bit states to floats and back.  Floats are written 16 bytes a lane: 201 M codes to
-// bf16 107 us (604 MB, 5.6 TB/s), with 8 bytes a lane 140.
-constexpr int kConvParts = 2;
+// bf16 102 us (604 MB, 5.9 TB/s; with one or two loads at once 127 and 107), with 8
+// bytes a lane 140.
+constexpr int kConvParts = 4;
 template <int DT> constexpr int kConvEach = DT == ZPQ_F32 ? 4 : 8;
 template <int DT, int MOMENT>
 __global__ __launch_bounds__(kThreads) void k_unpack8(const uint8_t* __restrict__ codes,

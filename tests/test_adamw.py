@@ -398,6 +398,12 @@ def test_refusals_on_the_gpu():
     with pytest.raises(ValueError):
         zpq.AdamW([d["p"][0], d["p"][0]], [d["g"][0], d["g"][0]])          # tied weights twice
     zpq.AdamW(d["p"], [d["g"][0], d["g"][0][:20]])                         # gradients are only read
+    buf = torch.zeros(240, device="cuda")
+    for at in (81, 99, 119):                                               # in the weights: both ends
+        with pytest.raises(ValueError):
+            zpq.AdamW([buf[100:120]], [buf[at:at + 20]])
+    for at in (80, 120):                                                   # beside them
+        zpq.AdamW([buf[100:120]], [buf[at:at + 20]])
     opt = zpq.AdamW(d["p"], d["g"], **ok)
     with pytest.raises(ValueError):
         opt.step(1, max_norm=1.0)
