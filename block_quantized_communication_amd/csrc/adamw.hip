@@ -86,7 +86,7 @@ inline ListEntry* list_entries(void* table) {
 // v_fma_f64 issues like v_fma_f32 here, so binary64 sums cost one conversion a
 // value and no range checks.  Workgroup b of G takes the chunks
 // [K*b/G, K*(b+1)/G): consecutive, so that the tensor is looked up once and
-// then followed.  Bound by reading: 906 M fp16 elements 271 us, 6.7 TB/s (a bare read
+// then followed.  Bound by reading: 906 M fp16 elements 265 us, 6.8 TB/s (a bare read
 // stream reaches 7.2).
 template <int DT> constexpr int kSumEach = DT == ZPQ_F32 ? 4 : 8;       // elements a lane
 constexpr int kSumChunk = 8192;               // elements of a workgroup's share
