@@ -140,16 +140,17 @@ __device__ __forceinline__ uint32_t key_of(const Ids& a, uint32_t t) {
     return r < (uint64_t)a.rows && id != a.padding ? (uint32_t)r : (uint32_t)a.rows;
 }
 
-// Up to kRankTokens: a token's place is the number of tokens that come before
-// it, counted by comparing it with all of them.  A workgroup places 64 tokens, one a
-// lane; its waves share the others, 64 at a time through LDS (a broadcast read
-// gives 4, and each is one compare and one add with carry for 64 tokens).  Where
-// rows are few as well, further workgroups count the same way what comes before each
-// row: its first place.  300 tokens 3.8 us, 8000 13 us; 16,384 would take 25, with the
-// radix sort 22.
-constexpr uint32_t kRankTokens = 8192;
+// A token's place in a tile is the number of the tile's tokens that come before it,
+// counted by comparing it with all of them.  A workgroup places 64 tokens, one a
+// lane; its waves share the tile's others, 64 at a time through LDS (a broadcast read
+// gives 4, and each is one compare and one add with carry for 64 tokens).  Up to
+// kRankTokens there is one tile and this is the whole sort; where rows are few as well,
+// further workgroups count the same way what comes before each row: its first place.
+// 300 tokens 3.8 us; of 4000 the whole gradient takes 21.6 us this way, with two tiles or
+// more and a merge 22.5, of 6000 26.0 and 24.4.
+constexpr uint32_t kRankTokens = 4096;
 constexpr int kRankWaves = 16;
-__global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __restrict__ out,
+__global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint32_t tile, uint64_t* __restrict__ out,
                                                           uint32_t* __restrict__ starts) {
     __shared__ __align__(16) uint32_t keys[kRankWaves][64];
     __shared__ uint32_t counts[kRankWaves][64];
@@ -159,13 +160,15 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __res
     const uint32_t own = row_block ? 0xFFFFFFFFu : blockIdx.x;
     const uint32_t t = (row_block ? blockIdx.x - blocks : blockIdx.x) * 64 + lane;     // token or row
     const uint32_t key = row_block ? t : t < a.tokens ? key_of(a, t) : 0xFFFFFFFEu;
+    const uint32_t base = row_block ? 0 : blockIdx.x * 64 / tile * tile;                // of the tile
+    const uint32_t first = base / 64, last = min(blocks, (base + tile) / 64);           // its blocks
     uint32_t before = 0;
     auto key_at = [&](uint32_t b) {
         const uint32_t j = b * 64 + lane;
-        return b < blocks && j < a.tokens ? key_of(a, j) : 0xFFFFFFFFu;
+        return b < last && j < a.tokens ? key_of(a, j) : 0xFFFFFFFFu;
     };
-    uint32_t next = key_at(wave);
-    for (uint32_t b = wave; b < blocks; b += kRankWaves) {
+    uint32_t next = key_at(first + wave);
+    for (uint32_t b = first + wave; b < last; b += kRankWaves) {
         __builtin_amdgcn_wave_barrier();
         keys[wave][lane] = next;
         next = key_at(b + kRankWaves);
@@ -190,17 +193,41 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(Ids a, uint64_t* __res
     if (wave == 0) {
 #pragma unroll
         for (int w = 1; w < kRankWaves; ++w) before += counts[w][lane];
-        if (!row_block && t < a.tokens) out[before] = (uint64_t)key << 32 | t;
+        if (!row_block && t < a.tokens) out[base + before] = (uint64_t)key << 32 | t;
         if (row_block && t <= a.rows) starts[t] = before;
     }
+}
+
+// Up to kMergeTokens: sorted tiles (runs of 2^log) are merged at once by places: a token's
+// is its place in its own run plus, for each other run, how many there are smaller.
+// kRuns lanes search for one token, a run each.  16,384 tokens: ranks and merge 11.5 us,
+// radix sort 21; with the gradient of 24,000 x 1024 44.4 us, by radix sort 47.1, even at
+// 32,768.
+constexpr uint32_t kRuns = 16, kMergeTokens = 24576;
+inline uint32_t run_log(uint32_t tokens) { return tokens <= kRuns * 1024 ? 10 : 11; }
+__global__ __launch_bounds__(kThreads) void k_merge(const uint64_t* __restrict__ in, uint32_t tokens,
+                                                    uint32_t log, uint64_t* __restrict__ out) {
+    const uint32_t lane = blockIdx.x * kThreads + threadIdx.x, t = lane / kRuns, r = lane % kRuns;
+    if (t >= tokens) return;                  // whole groups of kRuns lanes
+    const uint64_t x = in[t];
+    uint32_t at = r << log, n = at >= tokens ? 0 : min(tokens - at, 1u << log), less = 0;
+    if (r == t >> log) { less = t - at; n = 0; }
+    for (uint32_t left = 1u << log; left > 0; left >>= 1)          // n halves at least as fast
+        if (n > 0) {
+            const uint32_t half = n >> 1;
+            if (in[at + half] < x) { at += half + 1; less += half + 1; n -= half + 1; }
+            else n = half;
+        }
+#pragma unroll
+    for (uint32_t d = 1; d < kRuns; d <<= 1) less += __shfl_xor(less, d);
+    if (r == 0) out[less] = x;
 }
 
 // More tokens: a radix sort from the lowest digit, `bits` (at most 9) a pass, stable by
 // construction.  k_digit_counts counts each tile's digits; k_digit_place gives every
 // token its place: tokens with smaller digits, the same digit in earlier tiles, in
 // earlier waves of the tile, and earlier in its wave (found by ballots).  131,072
-// tokens 4.9 and 8.4 us a pass, 16,384 4.7 and 5.7: latency, of the launches and of a few
-// dependent accesses.
+// tokens 4.9 and 8.8 us a pass: latency, of the launches and of a few dependent accesses.
 constexpr int kMaxDigits = 512, kSortThreads = 512, kSortTile = 4 * kSortThreads;
 constexpr int kSortWaves = kSortThreads / 64;
 static_assert(kSortThreads == kMaxDigits, "a digit a thread");
@@ -655,8 +682,8 @@ inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim, int64_t rows) {
     };
     w.starts = take((rows + 1) * 4);
     w.sorted[0] = take(tokens * 8);
-    if (tokens > kRankTokens) {
-        w.sorted[1] = take(tokens * 8);
+    if (tokens > kRankTokens) w.sorted[1] = take(tokens * 8);
+    if (tokens > kMergeTokens) {
         w.counts = take((tokens + kSortTile - 1) / kSortTile * kMaxDigits * 4);
         w.totals = take(kMaxDigits * 4);
     }
@@ -680,8 +707,16 @@ bool sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* coun
     if (a.tokens <= kRankTokens) {
         const bool rows = a.rows * a.tokens <= kRankRows;
         const unsigned blocks = (a.tokens + 63) / 64 + (rows ? (unsigned)(a.rows / 64 + 1) : 0);
-        hipLaunchKernelGGL(k_rank, dim3(blocks), dim3(64 * kRankWaves), 0, st, a, list, starts);
+        hipLaunchKernelGGL(k_rank, dim3(blocks), dim3(64 * kRankWaves), 0, st, a, kRankTokens, list, starts);
         return rows;
+    }
+    if (a.tokens <= kMergeTokens) {
+        const uint32_t log = run_log(a.tokens);
+        hipLaunchKernelGGL(k_rank, dim3((a.tokens + 63) / 64), dim3(64 * kRankWaves), 0, st, a, 1u << log, other,
+                           starts);
+        hipLaunchKernelGGL(k_merge, dim3((a.tokens * kRuns + kThreads - 1) / kThreads), dim3(kThreads), 0, st,
+                           other, a.tokens, log, list);
+        return false;
     }
     int bits = 1;
     while (a.rows >> bits) ++bits;            // of the largest key, `rows`

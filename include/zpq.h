@@ -314,7 +314,8 @@ zpq_status zpq_embedding_i8(const int8_t* codes, const float* scales, int64_t ro
  * (with accumulate the fp32 sum of both is rounded once, and rows without a
  * token are not touched; without, they become zeros).  The sum is in binary32,
  * in an order that depends on the ids and the sizes only: the tokens are sorted by
- * row, equal rows in token order, and long rows are summed in parts; no atomics.  Ids outside [first, first + rows) and ids
+ * row, equal rows in token order, and long rows are summed in parts; no
+ * floating-point atomics.  Ids outside [first, first + rows) and ids
  * equal to `padding` count for nothing (give padding = -1, or any id outside,
  * for none).
  *   dy    [tokens] rows of dim elements of type dy_dtype, ld_dy apart

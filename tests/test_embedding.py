@@ -167,7 +167,8 @@ def test_grad(dy, out, accumulate, tokens, rows, dim):
     check_grad(host(g), base, ids, host(y), rows, 0.7, out)
 
 
-@pytest.mark.parametrize("tokens", [255, 256, 257, 1024, 1025, 4096, 32768, 32769, 140000])
+@pytest.mark.parametrize("tokens", [255, 256, 257, 1024, 1025, 4095, 4096, 4097, 5119, 5121, 16384, 16385, 20481, 24576,
+                                    24577, 32768, 32769, 140000])
 @pytest.mark.parametrize("kind", ["frequent", "one", "spread"])
 def test_grad_sizes_of_the_sort(tokens, kind):
     """Every number of runs and group levels: exact sums of small integers."""
@@ -301,7 +302,7 @@ def test_other_stream_and_graph():
 
 
 @pytest.mark.parametrize("accumulate", [False, True])
-@pytest.mark.parametrize("tokens,rows,dim", [(53280, 4, 24), (8192, 2048, 12), (8192, 2049, 12), (8193, 3, 520),
+@pytest.mark.parametrize("tokens,rows,dim", [(53280, 4, 24), (8192, 2048, 12), (4096, 4096, 12), (4096, 4097, 12), (8193, 3, 520),
                                              (511, 70, 9), (512, 70, 9), (20000, 90000, 132), (300000, 5, 7),
                                              (3000, 40, 12000), (2500, 200000, 3), (9000, 300000, 6)])
 def test_grad_sizes_of_the_sums(tokens, rows, dim, accumulate):
