@@ -480,8 +480,8 @@ __device__ __forceinline__ uint32_t lower_bound(const uint64_t* __restrict__ s, 
     return lo;
 }
 
-// Level `level` sums of whole groups that lie within one row: 39 us of 195 for 131,072 x
-// 2048 (200 MB read), 17 of 205 for 16,384 x 8192.  On level 1 the
+// Level `level` sums of whole groups that lie within one row: 39 us of 192 for 131,072 x
+// 2048 (200 MB read), 17 of 196 for 16,384 x 8192.  On level 1 the
 // workgroups from `start_blocks` on; those before find the rows' first places, a row a
 // lane.
 template <int DT, bool FIRST, bool WIDE>
