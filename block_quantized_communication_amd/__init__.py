@@ -42,6 +42,7 @@ STATUS = {0: "ok", 1: "null pointer", 2: "bad size", 3: "bad block", 4: "misalig
 EXPORTS = ("zpq_quant_i8", "zpq_dequant_i8", "zpq_quant_i8_tensor", "zpq_qgz_reorder_quant_i4",
            "zpq_qgz_dequant_reduce_requant_i4", "zpq_status_str", "zpq_abi_version",
            "zpq_list_make", "zpq_grad_sumsq", "zpq_adamw_plan_make", "zpq_adamw_step",
+           "zpq_adamw_step_at",
            "zpq_state8_unpack", "zpq_state8_pack", "zpq_embedding", "zpq_embedding_i8",
            "zpq_embedding_grad_bytes", "zpq_embedding_grad")
 
@@ -104,6 +105,7 @@ def lib():
         L.zpq_adamw_plan_make.argtypes = [ctypes.POINTER(_AdamwTensor), i32, i32, i32, i32, i32, vp,
                                           i64, ctypes.POINTER(_AdamwPlan), vp]
         L.zpq_adamw_step.argtypes = [ctypes.POINTER(_AdamwPlan), ctypes.POINTER(_AdamwHyper), vp, vp]
+        L.zpq_adamw_step_at.argtypes = [ctypes.POINTER(_AdamwPlan), vp, vp, vp]
         L.zpq_state8_unpack.argtypes = [vp, vp, i64, i32, vp, i32, vp]
         L.zpq_state8_pack.argtypes = [vp, i32, i64, i32, vp, vp, vp]
         L.zpq_embedding.argtypes = [vp, i32, i64, i64, i64, vp, i32, i64, i64, f32, vp, i32, i64, vp]
@@ -115,7 +117,7 @@ def lib():
         for f in (L.zpq_quant_i8, L.zpq_dequant_i8, L.zpq_quant_i8_tensor,
                   L.zpq_qgz_reorder_quant_i4, L.zpq_qgz_dequant_reduce_requant_i4,
                   L.zpq_list_make, L.zpq_grad_sumsq, L.zpq_adamw_plan_make, L.zpq_adamw_step,
-                  L.zpq_state8_unpack, L.zpq_state8_pack, L.zpq_embedding, L.zpq_embedding_i8,
+                  L.zpq_adamw_step_at, L.zpq_state8_unpack, L.zpq_state8_pack, L.zpq_embedding, L.zpq_embedding_i8,
                   L.zpq_embedding_grad_bytes, L.zpq_embedding_grad):
             f.restype = ctypes.c_int
         L.zpq_status_str.argtypes = [ctypes.c_int]
@@ -504,7 +506,7 @@ class AdamW:
         return grad_sumsq(self._list, out=out, accumulate=accumulate, stream=stream)
 
     def step(self, step, lr=None, grad_scale=1.0, sumsq=None, max_norm=None, stream=None):
-        """Step number `step` (from 1).  sumsq: float64 [1] on the GPU, the
+        """Step number `step` (from 1), or a DeviceHyper.  sumsq: float64 [1] on the GPU, the
         squared norm of the unscaled gradients over all ranks; where it is not
         finite nothing changes.  max_norm: clip the scaled gradients to it
         (needs sumsq)."""
@@ -512,13 +514,46 @@ class AdamW:
         if sumsq is not None:
             _need(sumsq, _torch().float64, 1, "sumsq", self.device)
             norm = sumsq.data_ptr()
-        elif max_norm is not None:
+        if isinstance(step, DeviceHyper):
+            if lr is not None or max_norm is not None or grad_scale != 1.0:
+                raise ValueError("lr, grad_scale and max_norm come from the DeviceHyper")
+            if step.clips and norm is None:
+                raise ValueError("max_norm needs sumsq")
+            if step.data.device != self.device:
+                raise ValueError(f"step: need a DeviceHyper on {self.device}, got one on {step.data.device}")
+            st, ctx = _on(stream, self.device)
+            with ctx:
+                _check(lib().zpq_adamw_step_at(self._ref, step.data.data_ptr(), norm, st), "zpq_adamw_step_at")
+            return
+        if norm is None and max_norm is not None:
             raise ValueError("max_norm needs sumsq")
-        h = _AdamwHyper(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, grad_scale,
-                        _INF if max_norm is None else max_norm, step, self.seed)
+        h = self._hyper(step, lr, grad_scale, max_norm)
         st, ctx = _on(stream, self.device)
         with ctx:
             _check(lib().zpq_adamw_step(self._ref, ctypes.byref(h), norm, st), "zpq_adamw_step")
+
+    def _hyper(self, step, lr, grad_scale, max_norm):
+        return _AdamwHyper(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, grad_scale,
+                           _INF if max_norm is None else max_norm, step, self.seed)
+
+    def device_hyper(self, step=1, lr=None, grad_scale=1.0, max_norm=None):
+        """These hyperparameters in GPU memory, for step() in a captured graph."""
+        return DeviceHyper(self._hyper(step, lr, grad_scale, max_norm), self.device, max_norm is not None)
+
+
+class DeviceHyper:
+    """A step's hyperparameters in GPU memory, read when the step runs: lr,
+    grad_scale and max_norm are float64 [1] tensors, step an int64 [1] one, to be
+    written in stream order (h.step.add_(1) in the graph, h.lr.fill_(x) before a
+    replay).  Values out of range make the step do nothing.  From
+    AdamW.device_hyper, not during a capture."""
+
+    def __init__(self, values, device, clips):
+        torch = _torch()
+        self.data = torch.frombuffer(bytearray(values), dtype=torch.float64).to(device)
+        self.clips = clips
+        self.lr, self.grad_scale, self.max_norm = self.data[0:1], self.data[4:5], self.data[5:6]
+        self.step = self.data[6:7].view(torch.int64)
 
 
 _INF = float("inf")

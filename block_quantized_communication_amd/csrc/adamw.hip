@@ -271,7 +271,7 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     x = (x ^ (x >> 15)) * 0x243F6A89u;
     return x ^ (x >> 16);
 }
-inline uint32_t random_key(uint64_t seed, uint64_t step) {
+__host__ __device__ inline uint32_t random_key(uint64_t seed, uint64_t step) {
     uint64_t z = seed + step * 0x9E3779B97F4A7C15ull;
     z = (z ^ (z >> 31)) * 0xB7E151628AED2A6Bull;
     z = (z ^ (z >> 29)) * 0x243F6A8885A308D3ull;
@@ -288,6 +288,55 @@ struct StepArgs {
     float b1, ob1, b2, ob2, eps, rbc2, rate;  // ob: 1 - b; rbc2: 1/sqrt(1 - b2^t); rate: lr/(1 - b1^t)
     uint32_t key;
 };
+
+// The constants from the hyperparameters, in the same operations on the host and on
+// the device (b^t by squaring, off by t * 2^-53 of itself, which 1 - b^t has to
+// its rounding to 24 bits as long as 1 - b > 2^-29).
+__host__ __device__ inline double power(double b, int64_t t) {
+    double x = 1.0;
+    for (; t > 0; t >>= 1, b *= b)
+        if (t & 1) x *= b;
+    return x;
+}
+__host__ __device__ inline bool finite_at_least(double x, double least) {
+    return x >= least && x <= 1.7976931348623157e308;
+}
+__host__ __device__ inline bool hyper_ok(const zpq_adamw_hyper& h) {
+    return finite_at_least(h.lr, 0.0) && h.beta1 >= 0.0 && h.beta1 < 1.0 && h.beta2 >= 0.0 && h.beta2 < 1.0 &&
+           finite_at_least(h.eps, 1e-30) && h.step >= 1 && h.grad_scale > 0.0 &&
+           h.grad_scale <= 3.4028234663852886e38 && h.max_norm > 0.0;
+}
+__host__ __device__ inline StepArgs step_args(const zpq_adamw_hyper& h) {
+    StepArgs a;
+    a.lr = h.lr;
+    a.grad_scale = h.grad_scale;
+    a.max_norm = h.max_norm;
+    a.b1 = (float)h.beta1;
+    a.ob1 = (float)(1.0 - h.beta1);
+    a.b2 = (float)h.beta2;
+    a.ob2 = (float)(1.0 - h.beta2);
+    a.eps = (float)h.eps;
+    a.rbc2 = (float)(1.0 / sqrt(1.0 - power(h.beta2, h.step)));
+    a.rate = (float)(h.lr / (1.0 - power(h.beta1, h.step)));
+    a.key = random_key(h.seed, (uint64_t)h.step);
+    return a;
+}
+
+// Hyperparameters in device memory: a launch of its own turns them into the constants,
+// in the plan's table behind the starts (lr -1 where they are out of range): norm and step
+// 2 us more (50.3 M elements 249.6 -> 251.1, 12.5 K 10.9 -> 13.1).
+static_assert(sizeof(PlanEntry) + 4 + 4 + 8 + sizeof(StepArgs) <= ZPQ_PLAN_BYTES(1) &&
+              sizeof(PlanEntry) + 4 <= 128, "ZPQ_PLAN_BYTES");
+inline StepArgs* args_of(void* table, int32_t count) {
+    const uintptr_t end = reinterpret_cast<uintptr_t>(starts_of(plan_entries(table), count) + count + 1);
+    return reinterpret_cast<StepArgs*>((end + 7) / 8 * 8);
+}
+__global__ void k_step_args(const zpq_adamw_hyper* __restrict__ h, StepArgs* __restrict__ to) {
+    StepArgs a = {};
+    a.lr = -1.0;
+    if (hyper_ok(*h)) a = step_args(*h);
+    *to = a;
+}
 
 // 4 elements a lane of one part: loaded together, stepped, stored.  A wave holds
 // 256 consecutive elements, which is a state block: the exponents of 8-bit
@@ -408,7 +457,12 @@ template <int PT, int GT, int CT, int BITS>
 __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict__ entries,
                                                     const uint32_t* __restrict__ starts,
                                                     int32_t count, uint32_t chunks, StepArgs a,
+                                                    const StepArgs* __restrict__ device_args,
                                                     const double* __restrict__ sumsq) {
+    if (device_args != nullptr) {
+        a = *device_args;
+        if (a.lr < 0.0) return;
+    }
     float c = (float)a.grad_scale;
     if (sumsq != nullptr) {
         const double norm = __builtin_sqrt(*sumsq) * a.grad_scale;
@@ -535,37 +589,52 @@ void launch_sumsq(const zpq_list* list, int64_t parts, double* out, int32_t accu
 
 bool list_ok(const zpq_list* l) {
     return l && l->count >= 0 && l->chunks >= 0 && l->chunks <= 0x7FFFFFFF && l->elems >= 0 &&
-           dtype_bytes(l->dtype) != 0 && (l->chunks == 0 || l->table);
+           dtype_bytes(l->dtype) != 0 && (l->chunks == 0 || (l->table && l->count > 0));
 }
 
 template <int PT, int GT, int CT, int BITS>
-void launch_adamw(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
+void launch_adamw(const zpq_adamw_plan* q, const StepArgs& a, const StepArgs* at, const double* sumsq,
+                  hipStream_t st) {
     hipLaunchKernelGGL((k_adamw<PT, GT, CT, BITS>), dim3(grid_of(q->chunks)), dim3(kThreads), 0, st,
                        plan_entries(q->table), starts_of(plan_entries(q->table), q->count),
-                       q->count, (uint32_t)q->chunks, a, sumsq);
+                       q->count, (uint32_t)q->chunks, a, at, sumsq);
 }
 template <int PT, int GT, int BITS>
-void launch_adamw_c(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
+void launch_adamw_c(const zpq_adamw_plan* q, const StepArgs& a, const StepArgs* at, const double* sumsq,
+                  hipStream_t st) {
     if constexpr (PT == ZPQ_F32) {
-        if (q->copy_dtype == ZPQ_F16) return launch_adamw<PT, GT, ZPQ_F16, BITS>(q, a, sumsq, st);
-        if (q->copy_dtype == ZPQ_BF16) return launch_adamw<PT, GT, ZPQ_BF16, BITS>(q, a, sumsq, st);
+        if (q->copy_dtype == ZPQ_F16) return launch_adamw<PT, GT, ZPQ_F16, BITS>(q, a, at, sumsq, st);
+        if (q->copy_dtype == ZPQ_BF16) return launch_adamw<PT, GT, ZPQ_BF16, BITS>(q, a, at, sumsq, st);
     }
-    launch_adamw<PT, GT, -1, BITS>(q, a, sumsq, st);
+    launch_adamw<PT, GT, -1, BITS>(q, a, at, sumsq, st);
 }
 template <int PT, int BITS>
-void launch_adamw_g(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
-    if (q->g_dtype == ZPQ_F32) launch_adamw_c<PT, ZPQ_F32, BITS>(q, a, sumsq, st);
-    else if (q->g_dtype == ZPQ_F16) launch_adamw_c<PT, ZPQ_F16, BITS>(q, a, sumsq, st);
-    else launch_adamw_c<PT, ZPQ_BF16, BITS>(q, a, sumsq, st);
+void launch_adamw_g(const zpq_adamw_plan* q, const StepArgs& a, const StepArgs* at, const double* sumsq,
+                  hipStream_t st) {
+    if (q->g_dtype == ZPQ_F32) launch_adamw_c<PT, ZPQ_F32, BITS>(q, a, at, sumsq, st);
+    else if (q->g_dtype == ZPQ_F16) launch_adamw_c<PT, ZPQ_F16, BITS>(q, a, at, sumsq, st);
+    else launch_adamw_c<PT, ZPQ_BF16, BITS>(q, a, at, sumsq, st);
 }
 template <int BITS>
-void launch_adamw_p(const zpq_adamw_plan* q, const StepArgs& a, const double* sumsq, hipStream_t st) {
-    if (q->p_dtype == ZPQ_F32) launch_adamw_g<ZPQ_F32, BITS>(q, a, sumsq, st);
-    else if (q->p_dtype == ZPQ_F16) launch_adamw_g<ZPQ_F16, BITS>(q, a, sumsq, st);
-    else launch_adamw_g<ZPQ_BF16, BITS>(q, a, sumsq, st);
+void launch_adamw_p(const zpq_adamw_plan* q, const StepArgs& a, const StepArgs* at, const double* sumsq,
+                  hipStream_t st) {
+    if (q->p_dtype == ZPQ_F32) launch_adamw_g<ZPQ_F32, BITS>(q, a, at, sumsq, st);
+    else if (q->p_dtype == ZPQ_F16) launch_adamw_g<ZPQ_F16, BITS>(q, a, at, sumsq, st);
+    else launch_adamw_g<ZPQ_BF16, BITS>(q, a, at, sumsq, st);
 }
 
-bool finite_at_least(double x, double least) { return x >= least && x <= 1.7976931348623157e308; }
+zpq_status adamw(const zpq_adamw_plan* plan, const StepArgs& a, const StepArgs* at, const double* sumsq,
+                 hipStream_t st) {
+    if (plan->state_bits == 32) launch_adamw_p<32>(plan, a, at, sumsq, st);
+    else launch_adamw_p<8>(plan, a, at, sumsq, st);
+    return after_launch();
+}
+
+bool plan_ok(const zpq_adamw_plan* q) {
+    return dtype_bytes(q->p_dtype) != 0 && dtype_bytes(q->g_dtype) != 0 &&
+           (q->state_bits == 32 || q->state_bits == 8) && q->count >= 0 && q->chunks >= 0 &&
+           q->chunks <= 0x7FFFFFFF && (q->chunks == 0 || (q->table && q->count > 0));
+}
 
 template <int DT>
 void launch_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t moment,
@@ -725,33 +794,24 @@ zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, i
 zpq_status zpq_adamw_step(const zpq_adamw_plan* plan, const zpq_adamw_hyper* h, const double* sumsq,
                           zpq_stream stream) {
     if (!plan || !h) return ZPQ_ERR_NULL;
-    if (dtype_bytes(plan->p_dtype) == 0 || dtype_bytes(plan->g_dtype) == 0 ||
-        (plan->state_bits != 32 && plan->state_bits != 8) || plan->count < 0 || plan->chunks < 0 ||
-        plan->chunks > 0x7FFFFFFF || (plan->chunks > 0 && !plan->table))
-        return ZPQ_ERR_ARG;
-    if (!finite_at_least(h->lr, 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
-        !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !finite_at_least(h->eps, 1e-30) || h->step < 1 ||
-        !(h->grad_scale > 0.0 && h->grad_scale <= 3.4028234663852886e38) || !(h->max_norm > 0.0))
-        return ZPQ_ERR_ARG;
+    if (!plan_ok(plan) || !hyper_ok(*h)) return ZPQ_ERR_ARG;
     if (!sumsq && h->max_norm <= 1.7976931348623157e308) return ZPQ_ERR_ARG;
     if (!aligned(sumsq, 8)) return ZPQ_ERR_ALIGN;
     if (plan->chunks == 0) return ZPQ_OK;
-    StepArgs a;
-    a.lr = h->lr;
-    a.grad_scale = h->grad_scale;
-    a.max_norm = h->max_norm;
-    a.b1 = (float)h->beta1;
-    a.ob1 = (float)(1.0 - h->beta1);
-    a.b2 = (float)h->beta2;
-    a.ob2 = (float)(1.0 - h->beta2);
-    a.eps = (float)h->eps;
-    a.rbc2 = (float)(1.0 / sqrt(1.0 - pow(h->beta2, (double)h->step)));
-    a.rate = (float)(h->lr / (1.0 - pow(h->beta1, (double)h->step)));
-    a.key = random_key(h->seed, (uint64_t)h->step);
+    return adamw(plan, step_args(*h), nullptr, sumsq, static_cast<hipStream_t>(stream));
+}
+
+zpq_status zpq_adamw_step_at(const zpq_adamw_plan* plan, const zpq_adamw_hyper* h, const double* sumsq,
+                             zpq_stream stream) {
+    if (!plan || !h) return ZPQ_ERR_NULL;
+    if (!plan_ok(plan)) return ZPQ_ERR_ARG;
+    if (!aligned(h, 8) || !aligned(sumsq, 8)) return ZPQ_ERR_ALIGN;
+    if (overlaps(h, sizeof *h, plan->table, ZPQ_PLAN_BYTES(plan->count))) return ZPQ_ERR_ALIAS;
+    if (plan->chunks == 0) return ZPQ_OK;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (plan->state_bits == 32) launch_adamw_p<32>(plan, a, sumsq, st);
-    else launch_adamw_p<8>(plan, a, sumsq, st);
-    return after_launch();
+    StepArgs* at = args_of(plan->table, plan->count);
+    hipLaunchKernelGGL(k_step_args, dim3(1), dim3(1), 0, st, h, at);
+    return adamw(plan, StepArgs{}, at, sumsq, st);
 }
 
 zpq_status zpq_state8_unpack(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t moment,

@@ -279,6 +279,17 @@ typedef struct {
 zpq_status zpq_adamw_step(const zpq_adamw_plan* plan, const zpq_adamw_hyper* hyper,
                           const double* sumsq, zpq_stream stream);
 
+/*
+ * The same with the hyperparameters in device memory, read when the step runs: a
+ * captured graph replays zpq_adamw_step with the step number that it was captured
+ * with, and this one with whatever *hyper holds by then (an earlier node may count
+ * hyper->step up).  Values out of range leave every output as it was; max_norm is
+ * not looked at where sumsq is NULL.  Two launches; the first writes into the plan's
+ * table, so calls on one plan must be ordered.
+ */
+zpq_status zpq_adamw_step_at(const zpq_adamw_plan* plan, const zpq_adamw_hyper* hyper,
+                             const double* sumsq, zpq_stream stream);
+
 /* 8-bit states to and from float tensors (checkpoints); moment: 1 (m) or 2
  * (v).  Packing rounds to nearest even, magnitudes of v (its sign is lost);
  * blocks as above, of one tensor of n elements. */
