@@ -343,23 +343,28 @@ class TensorList:
     tensors; their storage must not be replaced (set_, resize_) meanwhile.  The
     table is written on `stream` (the current one by default) and also holds the
     partial sums of the call that runs: later calls must come after it and one
-    after the other, in stream order."""
+    after the other, in stream order.  A captured graph holds the table's address:
+    keep the list as long as the graph."""
 
     def __init__(self, tensors, stream=None):
         self.tensors = list(tensors)
         if not self.tensors:
             raise ValueError("tensors: need at least one")
         self.device = _one_device(self.tensors, "tensors")
-        self._lay_out([t.data_ptr() for t in self.tensors], [t.numel() for t in self.tensors],
-                      _one_dtype(self.tensors, "tensors"), stream)
+        dt = _one_dtype(self.tensors, "tensors")
+        self._allocate(len(self.tensors), stream)
+        self._lay_out([t.data_ptr() for t in self.tensors], [t.numel() for t in self.tensors], dt, stream)
+
+    def _allocate(self, count, stream):
+        self._c = _List()
+        self._ref = ctypes.byref(self._c)
+        with _on(stream, self.device)[1]:
+            self._table = _torch().empty(count * 32 + LIST_FIXED_BYTES, dtype=_torch().uint8, device=self.device)
 
     def _lay_out(self, ptrs, sizes, dt, stream):
         n = len(ptrs)
         st, ctx = _on(stream, self.device)
-        self._c = _List()
-        self._ref = ctypes.byref(self._c)
         with ctx:
-            self._table = _torch().empty(n * 32 + LIST_FIXED_BYTES, dtype=_torch().uint8, device=self.device)
             _check(lib().zpq_list_make((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), n, dt,
                                        self._table.data_ptr(), self._table.numel(), self._ref, st),
                    "zpq_list_make")
@@ -397,7 +402,8 @@ class AdamW:
 
     Tensors are kept and their addresses laid out once, on `stream` (the current
     one by default; later calls must come after it in stream order): storage must
-    not be replaced meanwhile; set_grads() takes other gradients."""
+    not be replaced meanwhile; set_grads() takes other gradients.  A captured graph
+    holds addresses of this object's memory: keep it as long as the graph."""
 
     def __init__(self, params, grads, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, state_bits=32, exp_avg=None, exp_avg_sq=None, seed=0, stream=None):
@@ -424,7 +430,7 @@ class AdamW:
         with _on(stream, self.device)[1]:
             self.exp_avg = self._state(exp_avg, "exp_avg")
             self.exp_avg_sq = self._state(exp_avg_sq, "exp_avg_sq")
-            self._table = torch.empty(count * 128 + 64, dtype=torch.uint8, device=self.device)
+        self._tables = {}                              # of each gradient type: the plan's table, the norm's list
         self._sizes = [p.numel() for p in self.params]
         self._rows = (_AdamwTensor * count)()
         spans = []                                     # of what the step writes
@@ -478,7 +484,11 @@ class AdamW:
         return given
 
     def set_grads(self, grads, stream=None):
-        """Take these gradients from the next call on (in stream order)."""
+        """Take these gradients from the next call on (in stream order).  A captured
+        norm or step takes them too, from its next replay on: the tables stay where
+        they are.  Gradients of another type have tables of their own; a graph that
+        was captured with the earlier type goes on with its last gradients, which
+        are kept for it."""
         grads = list(grads)
         self._match(grads, "grads")
         gd = _one_dtype(grads, "grads")
@@ -493,13 +503,18 @@ class AdamW:
         st, ctx = _on(stream, self.device)
         plan = _AdamwPlan()
         with ctx:
+            if gd not in self._tables:
+                made = TensorList.__new__(TensorList)
+                made.device = self.device
+                made._allocate(len(grads), stream)
+                self._tables[gd] = _torch().empty(len(grads) * 128 + 64, dtype=_torch().uint8, device=self.device), made
+            table, made = self._tables[gd]
             _check(lib().zpq_adamw_plan_make(self._rows, len(grads), self._pd, gd, self._cd, self.state_bits,
-                                             self._table.data_ptr(), self._table.numel(), ctypes.byref(plan), st),
+                                             table.data_ptr(), table.numel(), ctypes.byref(plan), st),
                    "zpq_adamw_plan_make")
-            self._plan, self._ref, self.grads = plan, ctypes.byref(plan), grads
-            self._list = TensorList.__new__(TensorList)
-            self._list.tensors, self._list.device = grads, self.device
-            self._list._lay_out(ptrs, self._sizes, gd, stream)
+            made._lay_out(ptrs, self._sizes, gd, stream)
+            made.tensors = grads
+            self._plan, self._ref, self._list, self.grads = plan, ctypes.byref(plan), made, grads
 
     def grad_sumsq(self, out=None, accumulate=False, stream=None):
         """Sum of squares of the gradients -> float64 [1] (see grad_sumsq)."""
