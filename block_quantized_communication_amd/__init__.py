@@ -323,6 +323,29 @@ def _on(stream, device):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
+class _Held:
+    """Memory that a handle owns, with the stream that it was allocated on.  `used` tells
+    the allocator of every other stream, so that memory of a handle that goes is
+    not given out again while work there is under way."""
+
+    def __init__(self):
+        self.tensors, self.on = [], {}
+
+    def add(self, tensors, home):
+        for t in tensors:
+            self.tensors.append((t, home))
+            for raw, s in self.on.items():
+                if raw != home:
+                    t.record_stream(s)
+
+    def used(self, raw, stream, device):
+        if raw not in self.on:
+            s = self.on[raw] = _torch().cuda.current_stream(device) if stream is None else stream
+            for t, home in self.tensors:
+                if raw != home:
+                    t.record_stream(s)
+
+
 def _one_device(tensors, name):
     """The tensors' common GPU; each must be contiguous and there."""
     dev = None
@@ -358,12 +381,16 @@ class TensorList:
     def _allocate(self, count, stream):
         self._c = _List()
         self._ref = ctypes.byref(self._c)
-        with _on(stream, self.device)[1]:
+        self._held = _Held()
+        st, ctx = _on(stream, self.device)
+        with ctx:
             self._table = _torch().empty(count * 32 + LIST_FIXED_BYTES, dtype=_torch().uint8, device=self.device)
+        self._held.add([self._table], st)
 
     def _lay_out(self, ptrs, sizes, dt, stream):
         n = len(ptrs)
         st, ctx = _on(stream, self.device)
+        self._held.used(st, stream, self.device)
         with ctx:
             _check(lib().zpq_list_make((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), n, dt,
                                        self._table.data_ptr(), self._table.numel(), self._ref, st),
@@ -376,6 +403,7 @@ def grad_sumsq(tensors, out=None, accumulate=False, stream=None):
     torch = _torch()
     tl = tensors if isinstance(tensors, TensorList) else TensorList(tensors, stream=stream)
     st, ctx = _on(stream, tl.device)
+    tl._held.used(st, stream, tl.device)
     with ctx:
         if out is not None:
             _need(out, torch.float64, 1, "out", tl.device)
@@ -427,9 +455,14 @@ class AdamW:
             self._cd = _one_dtype(self.copies, "copies")
             if self._cd == ZPQ_F32 or self._pd != ZPQ_F32:
                 raise ValueError("copies: need float16 or bfloat16 tensors beside float32 params")
-        with _on(stream, self.device)[1]:
+        self._held = _Held()
+        st, ctx = _on(stream, self.device)
+        with ctx:
             self.exp_avg = self._state(exp_avg, "exp_avg")
             self.exp_avg_sq = self._state(exp_avg_sq, "exp_avg_sq")
+        for given, made in ((exp_avg, self.exp_avg), (exp_avg_sq, self.exp_avg_sq)):
+            if given is None:
+                self._held.add([t for x in made for t in (x if state_bits == 8 else (x,))], st)
         self._tables = {}                              # of each gradient type: the plan's table, the norm's list
         self._sizes = [p.numel() for p in self.params]
         self._rows = (_AdamwTensor * count)()
@@ -501,6 +534,7 @@ class AdamW:
             if n and ((j and ends[j - 1] > a) or (j < len(starts) and starts[j] < a + n * width)):
                 raise ValueError("grads overlap what the step writes")
         st, ctx = _on(stream, self.device)
+        self._held.used(st, stream, self.device)
         plan = _AdamwPlan()
         with ctx:
             if gd not in self._tables:
@@ -508,6 +542,7 @@ class AdamW:
                 made.device = self.device
                 made._allocate(len(grads), stream)
                 self._tables[gd] = _torch().empty(len(grads) * 128 + 64, dtype=_torch().uint8, device=self.device), made
+                self._held.add([self._tables[gd][0]], st)
             table, made = self._tables[gd]
             _check(lib().zpq_adamw_plan_make(self._rows, len(grads), self._pd, gd, self._cd, self.state_bits,
                                              table.data_ptr(), table.numel(), ctypes.byref(plan), st),
@@ -537,6 +572,8 @@ class AdamW:
             if step.data.device != self.device:
                 raise ValueError(f"step: need a DeviceHyper on {self.device}, got one on {step.data.device}")
             st, ctx = _on(stream, self.device)
+            self._held.used(st, stream, self.device)
+            step._held.used(st, stream, self.device)
             with ctx:
                 _check(lib().zpq_adamw_step_at(self._ref, step.data.data_ptr(), norm, st), "zpq_adamw_step_at")
             return
@@ -544,6 +581,7 @@ class AdamW:
             raise ValueError("max_norm needs sumsq")
         h = self._hyper(step, lr, grad_scale, max_norm)
         st, ctx = _on(stream, self.device)
+        self._held.used(st, stream, self.device)
         with ctx:
             _check(lib().zpq_adamw_step(self._ref, ctypes.byref(h), norm, st), "zpq_adamw_step")
 
@@ -567,6 +605,8 @@ class DeviceHyper:
         torch = _torch()
         self.data = torch.frombuffer(bytearray(values), dtype=torch.float64).to(device)
         self.clips = clips
+        self._held = _Held()
+        self._held.add([self.data], _on(None, self.data.device)[0])
         self.lr, self.grad_scale, self.max_norm = self.data[0:1], self.data[4:5], self.data[5:6]
         self.step = self.data[6:7].view(torch.int64)
 

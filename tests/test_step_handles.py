@@ -27,6 +27,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(zpq, "lib", lambda: fake)
     monkeypatch.setattr(zpq, "_gpu", lambda t, name, device=None: t.device)
     monkeypatch.setattr(zpq, "_on", lambda stream, device: (0, contextlib.nullcontext()))
+    monkeypatch.setattr("torch.cuda.current_stream", lambda device=None: None)
     return fake
 
 
@@ -103,3 +104,64 @@ def test_a_captured_norm_and_step_take_new_gradients(bits):
     torch.cuda.synchronize()
     assert torch.equal(total, want)
     assert all(torch.equal(a, b) for a, b in zip(flat(d), flat(e)))
+
+
+class Memory:
+    """A tensor that takes note of the streams it is recorded on."""
+
+    def __init__(self):
+        self.on = []
+
+    def record_stream(self, s):
+        self.on.append(s)
+
+
+def test_memory_is_recorded_once_on_each_other_stream():
+    home, other, third = (type("Stream", (), {"cuda_stream": i})() for i in (10, 11, 12))
+    a, b = Memory(), Memory()
+    held = zpq._Held()
+    held.add([a], home.cuda_stream)
+    for s in (home, other, other, third, home, third):
+        held.used(s.cuda_stream, s, None)
+    held.add([b], third.cuda_stream)                   # may be used on any of them from now on
+    held.used(other.cuda_stream, other, None)
+    assert a.on == [other, third] and b.on == [home, other]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["list", "optimizer", "hyper"])
+def test_handles_may_go_while_another_stream_uses_their_memory(what):
+    """Made on the current stream, used on another that is still busy, dropped: the
+    current stream's next allocations must not get that memory.  Nothing is written
+    there meanwhile."""
+    import torch
+    n = 1 << 20
+    p, g = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    total = torch.zeros(1, dtype=torch.float64, device="cuda")
+    handle = zpq.TensorList([g]) if what == "list" else zpq.AdamW([p], [g])
+    hyper = handle.device_hyper() if what == "hyper" else None
+    mine = [handle._table] if what == "list" else \
+        [hyper.data] if what == "hyper" else [handle.exp_avg[0], handle.exp_avg_sq[0]] + \
+        [t for table, made in handle._tables.values() for t in (table, made._table)]
+    sizes = [t.numel() * t.element_size() for t in mine]
+    at = {t.untyped_storage().data_ptr() for t in mine}
+    del mine
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)                 # some tenths of a second
+        if what == "hyper":
+            handle.step(hyper)
+        elif what == "optimizer":
+            handle.step(1, sumsq=handle.grad_sumsq(out=total))
+        else:
+            zpq.grad_sumsq(handle, out=total)
+    del hyper
+    if what != "hyper":
+        del handle
+    new = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in sizes for _ in range(4)]
+    busy = not side.query()
+    got = {t.untyped_storage().data_ptr() for t in new}
+    torch.cuda.synchronize()
+    assert busy, "the other stream had ended: nothing was tested"
+    assert not at & got
