@@ -598,7 +598,8 @@ class DeviceHyper:
     """A step's hyperparameters in GPU memory, read when the step runs: lr,
     grad_scale and max_norm are float64 [1] tensors, step an int64 [1] one, to be
     written in stream order (h.step.add_(1) in the graph, h.lr.fill_(x) before a
-    replay).  Values out of range make the step do nothing.  From
+    replay).  Values out of range make the step do nothing.  max_norm counts only
+    where step() gets a sumsq (one made with max_norm insists on it).  From
     AdamW.device_hyper, not during a capture."""
 
     def __init__(self, values, device, clips):

@@ -301,10 +301,11 @@ __host__ __device__ inline double power(double b, int64_t t) {
 __host__ __device__ inline bool finite_at_least(double x, double least) {
     return x >= least && x <= 1.7976931348623157e308;
 }
-__host__ __device__ inline bool hyper_ok(const zpq_adamw_hyper& h) {
+// max_norm counts only where there is a norm.
+__host__ __device__ inline bool hyper_ok(const zpq_adamw_hyper& h, bool norm) {
     return finite_at_least(h.lr, 0.0) && h.beta1 >= 0.0 && h.beta1 < 1.0 && h.beta2 >= 0.0 && h.beta2 < 1.0 &&
            finite_at_least(h.eps, 1e-30) && h.step >= 1 && h.grad_scale > 0.0 &&
-           h.grad_scale <= 3.4028234663852886e38 && h.max_norm > 0.0;
+           h.grad_scale <= 3.4028234663852886e38 && (!norm || h.max_norm > 0.0);
 }
 __host__ __device__ inline StepArgs step_args(const zpq_adamw_hyper& h) {
     StepArgs a;
@@ -331,10 +332,10 @@ inline StepArgs* args_of(void* table, int32_t count) {
     const uintptr_t end = reinterpret_cast<uintptr_t>(starts_of(plan_entries(table), count) + count + 1);
     return reinterpret_cast<StepArgs*>((end + 7) / 8 * 8);
 }
-__global__ void k_step_args(const zpq_adamw_hyper* __restrict__ h, StepArgs* __restrict__ to) {
+__global__ void k_step_args(const zpq_adamw_hyper* __restrict__ h, int32_t norm, StepArgs* __restrict__ to) {
     StepArgs a = {};
     a.lr = -1.0;
-    if (hyper_ok(*h)) a = step_args(*h);
+    if (hyper_ok(*h, norm != 0)) a = step_args(*h);
     *to = a;
 }
 
@@ -794,7 +795,7 @@ zpq_status zpq_adamw_plan_make(const zpq_adamw_tensor* tensors, int32_t count, i
 zpq_status zpq_adamw_step(const zpq_adamw_plan* plan, const zpq_adamw_hyper* h, const double* sumsq,
                           zpq_stream stream) {
     if (!plan || !h) return ZPQ_ERR_NULL;
-    if (!plan_ok(plan) || !hyper_ok(*h)) return ZPQ_ERR_ARG;
+    if (!plan_ok(plan) || !hyper_ok(*h, true)) return ZPQ_ERR_ARG;
     if (!sumsq && h->max_norm <= 1.7976931348623157e308) return ZPQ_ERR_ARG;
     if (!aligned(sumsq, 8)) return ZPQ_ERR_ALIGN;
     if (plan->chunks == 0) return ZPQ_OK;
@@ -810,7 +811,7 @@ zpq_status zpq_adamw_step_at(const zpq_adamw_plan* plan, const zpq_adamw_hyper* 
     if (plan->chunks == 0) return ZPQ_OK;
     hipStream_t st = static_cast<hipStream_t>(stream);
     StepArgs* at = args_of(plan->table, plan->count);
-    hipLaunchKernelGGL(k_step_args, dim3(1), dim3(1), 0, st, h, at);
+    hipLaunchKernelGGL(k_step_args, dim3(1), dim3(1), 0, st, h, (int32_t)(sumsq != nullptr), at);
     return adamw(plan, StepArgs{}, at, sumsq, st);
 }
 

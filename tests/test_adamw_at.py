@@ -120,3 +120,20 @@ def test_captured_graph_counts_its_steps(bits):
         torch.cuda.synchronize()
         assert h.step.item() == 5 + rep
         all_equal(d, e, rep)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_without_a_norm_max_norm_is_not_looked_at(bits):
+    """And it is, whenever it is written, where the step gets a norm."""
+    d, e, od, oe = pair([4097, 12], bits)
+    h = od.device_hyper(step=4)
+    for i, x in enumerate((0.0, -1.0, float("nan"), 1e-3)):
+        h.max_norm.fill_(x)
+        h.step.fill_(4 + i)
+        od.step(h)
+        oe.step(4 + i)
+        all_equal(d, e, x)
+    od.step(h, sumsq=od.grad_sumsq())
+    oe.step(7, sumsq=oe.grad_sumsq(), max_norm=1e-3)
+    all_equal(d, e, "clipped")
