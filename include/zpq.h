@@ -253,10 +253,10 @@ typedef struct {
  *   v' = beta2 * v + ((1 - beta2) * g') * g'
  *   p' = p * (1 - lr * weight_decay)
  *        - lr / (1 - beta1^step) * (m' / (sqrt(v') / sqrt(1 - beta2^step) + eps))
- * in binary32, one rounding an operation (the root within 1 ulp and 0 below
- * 2^-126, the quotient as a product with a reciprocal within 1 ulp), the
- * constants rounded once from binary64; p' is rounded to nearest even into
- * p_dtype and copy_dtype.
+ * in binary32, one rounding an operation (the root within 1 ulp, the quotient
+ * as a product with a reciprocal within 1 ulp), the constants rounded once from
+ * binary64; p' is rounded to nearest even into p_dtype and copy_dtype.  (A v'
+ * that rounds to 0 in binary32, below 2^-150, leaves eps alone in the quotient.)
  *
  * sumsq: device pointer to the squared norm of the unscaled gradients (all
  * ranks'), or NULL: c = fl32(grad_scale), and max_norm must be infinite
