@@ -560,6 +560,7 @@ __global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first
         if (!narrow) old.load(grad, col);
         else old.load_some(grad, 0, count);
     }
+    const float scale = at < e ? a.scale : 0.0f;          // no token: zeros, whatever the scale
     float acc[E] = {};
 #pragma unroll 1
     while (at < e) {
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(kThreads) void k_row_sums(GradArgs a, int64_t first
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        acc[i] *= a.scale;
+        acc[i] *= scale;
         if constexpr (ADD) acc[i] = old.get(i) + acc[i];
     }
     Raw<OT, E> out;
