@@ -699,14 +699,18 @@ inline GradWorkspace grad_workspace(int64_t tokens, int64_t dim, int64_t rows) {
 }
 
 // The sorted list; `list` and `other` are exchanged as the passes need.  True where
-// the rows' first places have been found as well: where that takes about 1 us
-// (2^24 comparisons), less than the launch that it saves.
-constexpr int64_t kRankRows = 1 << 24;
+// the rows' first places have been found as well, by comparing every row with every
+// token, which saves a launch (or, from 512 tokens on, binary searches in one).  That
+// takes a workgroup of 16 waves for 64 rows whatever the tokens, 1024 such workgroups
+// about as long as the launch: 5 tokens added to 65,000 rows of 64 6.8 us, by search 7.8;
+// to 131,072 9.9 and 7.7, to 1,000,000 42.9 and 9.2.  And it takes the comparisons: 1000
+// tokens into 16,000 rows (2^24) 9.9 and 11.8 us, 4000 into 16,000 (2^26) 16.9 and 16.1.
+constexpr int64_t kRankRows = 1 << 16, kRankCompares = 1 << 24;
 bool sort_tokens(const Ids& a, uint64_t*& list, uint64_t*& other, uint32_t* counts, uint32_t* totals,
                  uint32_t* starts, hipStream_t st) {
     if (a.tokens == 0) return false;
     if (a.tokens <= kRankTokens) {
-        const bool rows = a.rows * a.tokens <= kRankRows;
+        const bool rows = a.rows <= kRankRows && a.rows * a.tokens <= kRankCompares;
         const unsigned blocks = (a.tokens + 63) / 64 + (rows ? (unsigned)(a.rows / 64 + 1) : 0);
         hipLaunchKernelGGL(k_rank, dim3(blocks), dim3(64 * kRankWaves), 0, st, a, kRankTokens, list, starts);
         return rows;

@@ -344,3 +344,20 @@ def test_grad_of_more_lanes_than_one_launch():
     g = zpq.embedding_grad(t, y, rows)
     assert bool((g[-1] == 4).all()) and bool((g[0] == 2).all()) and bool((g[1 << 25] == 4).all())
     assert bool((g[-2] == 5).all()) and not bool(g[1:1 << 25].any()) and not bool(g[(1 << 25) + 1:-2].any())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("tokens", [1, 5, 64, 65, 255, 257, 600])
+@pytest.mark.parametrize("rows", [(1 << 16) - 1, 1 << 16, (1 << 16) + 1, 1 << 20])
+def test_grad_of_few_tokens_into_many_rows(tokens, rows, accumulate):
+    """Both sides of the rule on where the rows' places are found that goes by the
+    rows alone: exact sums of small integers, first and last rows among them."""
+    import torch
+    rng = np.random.default_rng(tokens)
+    ids = rng.choice([0, 1, rows // 2, rows - 2, rows - 1, rows, -1, 63, 64, 65], tokens)
+    y = rng.integers(-2, 3, (tokens, 8))
+    g = torch.full((rows, 8), 3.0, device="cuda")
+    zpq.embedding_grad(torch.from_numpy(ids).cuda(), torch.from_numpy(y.astype(np.float32)).cuda(), rows, scale=2.0,
+                       out=g, accumulate=accumulate)
+    want, _, _ = ref.grad64(ids, y.astype(np.float64), rows, 2.0)
+    assert np.array_equal(host(g), want + (3.0 if accumulate else 0.0))
