@@ -361,3 +361,24 @@ def test_grad_of_few_tokens_into_many_rows(tokens, rows, accumulate):
                        out=g, accumulate=accumulate)
     want, _, _ = ref.grad64(ids, y.astype(np.float64), rows, 2.0)
     assert np.array_equal(host(g), want + (3.0 if accumulate else 0.0))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("tokens,rows", [(900, 300), (3000, 300), (3000, 90000), (20000, 300), (24576, 70000), (50000, 300),
+                                         (140000, 70000)])
+def test_grad_with_ids_of_4_bytes(tokens, rows, accumulate):
+    """Every way of sorting, from both widths of the same ids (negative and too large
+    ones among them): the same bits, and the exact sums of small integers."""
+    import torch
+    ids, t = draw_ids(tokens, rows, 5, width="i32")
+    assert t.dtype == torch.int32 and ids.min() == -(1 << 31) and ids.max() >= rows
+    y = np.random.default_rng(6).integers(-8, 9, (tokens, 12))
+    dy = torch.from_numpy(y.astype(np.float32)).cuda()
+    g = [torch.full((rows, 12), 5.0, device="cuda") for _ in range(2)]
+    zpq.embedding_grad(t, dy, rows, padding=7, out=g[0], accumulate=accumulate)
+    zpq.embedding_grad(t.long(), dy, rows, padding=7, out=g[1], accumulate=accumulate)
+    assert torch.equal(g[0], g[1])
+    want, _, _ = ref.grad64(ids, y.astype(np.float64), rows, 1.0, padding=7)
+    assert np.array_equal(host(g[0]), want + (5.0 if accumulate else 0.0))
+    z = torch.randn(tokens, 40, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda")
+    assert torch.equal(zpq.embedding_grad(t, z, rows), zpq.embedding_grad(t.long(), z, rows))
