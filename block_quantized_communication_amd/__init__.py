@@ -308,13 +308,22 @@ def _code(dt):
     return c
 
 
+@functools.lru_cache(maxsize=None)
+def _raw_stream():
+    """Device index -> pointer of its current stream: torch's short way, which is not
+    public, where it is there."""
+    torch = _torch()
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(stream, device):
     """(stream pointer, context): what a call allocates comes from the pool of
     the stream that it runs on, so that freeing it is ordered with its use."""
     torch = _torch()
     if stream is None:
         index = device.index
-        raw = torch._C._cuda_getCurrentRawStream(index)
+        raw = _raw_stream()(index)
         if index == torch.cuda.current_device():
             return raw, _here
         return raw, torch.cuda.stream(torch.cuda.current_stream(device))

@@ -106,6 +106,23 @@ def test_a_captured_norm_and_step_take_new_gradients(bits):
     assert all(torch.equal(a, b) for a, b in zip(flat(d), flat(e)))
 
 
+@pytest.mark.parametrize("short", [True, False])
+def test_the_current_stream_without_torch_s_short_way(short, monkeypatch):
+    import torch
+    stream = type("Stream", (), {"cuda_stream": 1234})()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    if short:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    zpq._raw_stream.cache_clear()
+    try:
+        assert zpq._on(None, torch.device("cuda", 3))[0] == (1003 if short else 1234)
+    finally:
+        zpq._raw_stream.cache_clear()
+
+
 class Memory:
     """A tensor that takes note of the streams it is recorded on."""
 
