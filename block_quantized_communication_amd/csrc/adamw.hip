@@ -154,9 +154,9 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(const ListEntry* __restrict_
     // back is done.  So a workgroup counts itself (waiting for its exchange) after
     // its sum can be read by all, and the one that counts to the end reads every sum.
     // Counting is in groups of 32 (where there are more), then the groups: with one count
-    // for 2048 workgroups 50.3 M elements took 36 us, so 21, and 23 with a second launch to
-    // join.  (A release and an acquire write back and invalidate the L2 for each workgroup:
-    // 107 us.)
+    // for the 1024 workgroups of 256 compute units 50.3 M elements take 27.9 us, so 20.3, and
+    // about 2 more with a second launch to join.  (A release and an acquire write back and
+    // invalidate the L2 for each workgroup: 107 us.)
     __shared__ bool last;
     if (threadIdx.x == 0) {
         unsigned long long old = __hip_atomic_exchange(&head->part[blockIdx.x], __double_as_longlong(sum),
@@ -460,7 +460,9 @@ struct Part {
 // tensor.  Bound by HBM, every tensor read and written once: 50.3 M elements with fp32
 // states 228 us (1.41 GB, 6.2 TB/s), 201 M with 8-bit states 493 us (3.22 GB, 6.5 TB/s).
 // Two parts a tile: with one 266 and 545 us, with four 241 and 536, when two took 244 and
-// 527.
+// 527.  16-bit weights without a copy, 50.3 M elements with 16-bit gradients: 181 us with
+// fp32 states (1.11 GB, 6.1 TB/s), 108 with 8-bit ones (505 MB, 4.7 TB/s: 8 bytes a lane and
+// access for weights and gradients, and the arithmetic).
 template <int PT, int GT, int CT, int BITS>
 __global__ __launch_bounds__(kThreads) void k_adamw(const PlanEntry* __restrict__ entries,
                                                     const uint32_t* __restrict__ starts,
@@ -530,6 +532,8 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(const uint8_t* __restrict_
     }
 }
 
+// 201 M values from fp32 177 us (1.01 GB, 5.7 TB/s), from bf16 150 (605 MB, 4.0 TB/s): one access
+// of 16 or 8 bytes in flight a lane.
 template <int DT, int MOMENT>
 __global__ __launch_bounds__(kThreads) void k_pack8(const void* __restrict__ x, int64_t n,
                                                     uint8_t* __restrict__ codes,
@@ -576,9 +580,10 @@ inline unsigned cu_count() {
 inline unsigned grid_of(int64_t work) { return (unsigned)(work < (1 << 22) ? work : 1 << 22); }
 
 // Gradients up to this size are left in the last-level cache for the step that
-// follows: norm and step of 50.3 M elements 263 -> 252 us, 68.8 M fp32 ones 372 -> 342, 201 M
-// 16-bit ones (403 MB) 803 -> 780; the norm alone 20 -> 24 us.  Of 1.8 GB nothing would be
-// left, and the norm takes 280 us, with plain loads 329.
+// follows: norm and step of 50.3 M elements 263 -> 250 us, 68.8 M fp32 ones 370 -> 336, 201 M
+// 16-bit ones (403 MB, with both states read out) 796 -> 771.  Where no step follows the norm
+// pays for it all the same: 18.9 -> 20.3 us, 46.0 -> 51.7, 66.9 -> 74.9.  Of 1.8 GB nothing would
+// be left, and the norm takes 280 us, with plain loads 329.
 constexpr int64_t kKeepBytes = 512LL << 20;
 
 template <int DT>

@@ -51,7 +51,8 @@ struct LookupArgs {
 
 // Two pieces a lane: the way from id to row to store takes about 3 us, so the waves
 // in flight have to carry more than one access each (16,384 x 8192: INT8 to bf16 55 us
-// with one, 49 with two, 55 with four; bf16 82, 66, 64; fp32 to bf16 124, 98, 90).
+// with one, 49 with two, 49 with four; fp32 to bf16 118, 95, 88; fp32 155, 130, 121; but
+// bf16 54, 60, 64).  One number for all types, INT8's; 4-byte ids take the same times.
 constexpr int kLookupPieces = 2;
 template <int TT, int OT>
 __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a) {
@@ -231,7 +232,11 @@ __global__ __launch_bounds__(kThreads) void k_merge(const uint64_t* __restrict__
 constexpr int kMaxDigits = 512, kSortThreads = 512, kSortTile = 4 * kSortThreads;
 constexpr int kSortWaves = kSortThreads / 64;
 static_assert(kSortThreads == kMaxDigits, "a digit a thread");
-constexpr uint32_t kDirectTiles = 64;         // up to this many tiles their counts are summed in place
+// Up to this many tiles k_digit_place sums their counts by itself; more take k_digit_scan, a
+// third launch a pass.  The gradient of 65,536 x 8 into 50,000 rows (32 tiles) takes 32.6 us,
+// with the scan 35.3; of 131,072 (64 tiles) 39.2 and 39.9; of 200,000 48.3 and 46.0, of
+// 1,048,576 109 and 88.
+constexpr uint32_t kDirectTiles = 64;
 
 struct Pass {
     int32_t shift, bits;
@@ -528,7 +533,8 @@ __global__ __launch_bounds__(kThreads) void k_group_sums(GradArgs a, int32_t lev
 }
 
 // Rows: each lane sums its piece over the row's places [at, e) of the list.  Rows without
-// a token are written at 6.6 TB/s (non-temporal stores; plain ones 4.5); where rows have
+// a token are written at 6.6 TB/s where they are long (8192 bf16; non-temporal stores; plain
+// ones 4.5), at 5.0 in 100,000 rows of 2000 bf16 (80 us); where rows have
 // a few tokens each the chain of place, token, dy and store is what takes the time, and
 // the waves in flight: 168 us for 16,384 x 8192 into 50,021 rows of bf16 (1.03 GB), 130 us
 // for 131,072 x 2048 added to 65,536 rows of fp32 (762 MB).
