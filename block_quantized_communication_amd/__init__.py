@@ -376,7 +376,8 @@ class TensorList:
     table is written on `stream` (the current one by default) and also holds the
     partial sums of the call that runs: later calls must come after it and one
     after the other, in stream order.  A captured graph holds the table's address:
-    keep the list as long as the graph."""
+    keep the list as long as the graph.  Of a list made during a capture the table is
+    written by each replay, not before the first."""
 
     def __init__(self, tensors, stream=None):
         self.tensors = list(tensors)
@@ -440,7 +441,8 @@ class AdamW:
     Tensors are kept and their addresses laid out once, on `stream` (the current
     one by default; later calls must come after it in stream order): storage must
     not be replaced meanwhile; set_grads() takes other gradients.  A captured graph
-    holds addresses of this object's memory: keep it as long as the graph."""
+    holds addresses of this object's memory: keep it as long as the graph.  Made, or
+    given gradients, during a capture, it has them from the first replay on."""
 
     def __init__(self, params, grads, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, state_bits=32, exp_avg=None, exp_avg_sq=None, seed=0, stream=None):
