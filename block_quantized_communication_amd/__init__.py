@@ -24,6 +24,9 @@ Around the communication path (tensors need their element's alignment only):
   state8_unpack / state8_pack                8-bit states to and from floats
   embedding(ids, table, scale)               -> scaled rows; embedding_i8: from qwZ codes and scales
   embedding_grad(ids, dy, rows, scale)       -> dense gradient of the table
+  quant_f8(x, tile, along)                   8-bit floats in blocks of 128 along rows, columns or both, or in tiles
+  dequant_f8, transpose_f8                   their values; the transposed matrix of tiles
+  matmul_f8(a, b)                            a @ b.T of two such matrices
 """
 import bisect
 import contextlib
@@ -44,7 +47,8 @@ EXPORTS = ("zpq_quant_i8", "zpq_dequant_i8", "zpq_quant_i8_tensor", "zpq_qgz_reo
            "zpq_list_make", "zpq_grad_sumsq", "zpq_adamw_plan_make", "zpq_adamw_step",
            "zpq_adamw_step_at",
            "zpq_state8_unpack", "zpq_state8_pack", "zpq_embedding", "zpq_embedding_i8",
-           "zpq_embedding_grad_bytes", "zpq_embedding_grad")
+           "zpq_embedding_grad_bytes", "zpq_embedding_grad", "zpq_quant_f8", "zpq_dequant_f8",
+           "zpq_transpose_f8", "zpq_matmul_f8_bytes", "zpq_matmul_f8")
 
 STATE_BLOCK = 256          # elements that share an exponent byte in 8-bit optimizer states
 LIST_FIXED_BYTES = 20736   # ZPQ_LIST_BYTES(0)
@@ -74,6 +78,11 @@ class _AdamwHyper(ctypes.Structure):
                 ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double),
                 ("max_norm", ctypes.c_double), ("step", ctypes.c_int64),
                 ("seed", ctypes.c_uint64)]
+
+
+class _F8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("kind", ctypes.c_int32),
+                ("tile", ctypes.c_int32)]
 
 
 class ZpqError(RuntimeError):
@@ -114,11 +123,18 @@ def lib():
         L.zpq_embedding_grad_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
         L.zpq_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, i64, i64, f32, vp,
                                          i32, i64, i32, vp, i64, vp]
+        L.zpq_quant_f8.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp]
+        L.zpq_dequant_f8.argtypes = [vp, i32, vp, i64, i64, i32, vp, i32, i64, vp]
+        L.zpq_transpose_f8.argtypes = [vp, vp, i64, i64, vp, vp, vp]
+        L.zpq_matmul_f8_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+        L.zpq_matmul_f8.argtypes = [ctypes.POINTER(_F8), ctypes.POINTER(_F8), i64, i64, i64, vp, i32, i64, i32, vp,
+                                    i64, vp]
         for f in (L.zpq_quant_i8, L.zpq_dequant_i8, L.zpq_quant_i8_tensor,
                   L.zpq_qgz_reorder_quant_i4, L.zpq_qgz_dequant_reduce_requant_i4,
                   L.zpq_list_make, L.zpq_grad_sumsq, L.zpq_adamw_plan_make, L.zpq_adamw_step,
                   L.zpq_adamw_step_at, L.zpq_state8_unpack, L.zpq_state8_pack, L.zpq_embedding, L.zpq_embedding_i8,
-                  L.zpq_embedding_grad_bytes, L.zpq_embedding_grad):
+                  L.zpq_embedding_grad_bytes, L.zpq_embedding_grad, L.zpq_quant_f8, L.zpq_dequant_f8,
+                  L.zpq_transpose_f8, L.zpq_matmul_f8_bytes, L.zpq_matmul_f8):
             f.restype = ctypes.c_int
         L.zpq_status_str.argtypes = [ctypes.c_int]
         L.zpq_status_str.restype = ctypes.c_char_p
@@ -776,4 +792,166 @@ def embedding_grad(ids, dy, rows, scale=1.0, first=0, padding=None, out_dtype=No
                                         first - 1 if padding is None else padding, rows, dim, scale,
                                         out.data_ptr(), _code(out.dtype), lo, accumulate, ws.data_ptr(), need,
                                         st), "zpq_embedding_grad")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Matrix products of the step, from 8-bit floating-point blocks of 128.  A matrix
+# [rows, cols] is a pair: codes [rows, 128 * kb] of torch.float8_e4m3fn or float8_e5m2, and
+# exponent bytes, uint8 [rows, kb4], or [ceil(rows / 128), kb4] of tiles (zpq.h).
+F8_BLOCK = 128
+
+
+@functools.lru_cache(maxsize=None)
+def _kinds():
+    torch = _torch()
+    return {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _kind(dtype, name):
+    k = _kinds().get(dtype)
+    if k is None:
+        raise ValueError(f"{name}: need float8_e4m3fn or float8_e5m2, got {dtype}")
+    return k
+
+
+def _f8_shapes(rows, cols, tile):
+    """Shapes of the codes and the exponent bytes of a [rows, cols] matrix."""
+    kb = -(-cols // F8_BLOCK)
+    return (rows, kb * F8_BLOCK), (-(-rows // F8_BLOCK) if tile else rows, -(-kb // 4) * 4)
+
+
+def _f8_pair(pair, name, device=None):
+    """Checks codes and scales; (device, kind, rows, blocks of a row, tile)."""
+    codes, scales = pair
+    dev = _gpu(codes, f"{name} codes", device)
+    kind = _kind(codes.dtype, f"{name} codes")
+    _gpu(scales, f"{name} scales", dev)
+    if codes.dim() != 2 or codes.shape[1] % F8_BLOCK or scales.dim() != 2 or scales.dtype != _torch().uint8:
+        raise ValueError(f"{name}: need codes [rows, 128 * blocks] and uint8 scales [rows, blocks4], got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)} of {scales.dtype}")
+    rows, width = codes.shape
+    of_rows, of_tiles = _f8_shapes(rows, width, False)[1], _f8_shapes(rows, width, True)[1]
+    if tuple(scales.shape) not in (of_rows, of_tiles):
+        raise ValueError(f"{name} scales: need {of_rows} or, of tiles, {of_tiles}, got {tuple(scales.shape)}")
+    return dev, kind, rows, width // F8_BLOCK, tuple(scales.shape) != of_rows
+
+
+def _f8_cols(cols, blocks, name):
+    """The matrix's columns: all of its blocks unless given."""
+    if cols is None:
+        return blocks * F8_BLOCK
+    if cols < 0 or -(-cols // F8_BLOCK) != blocks:
+        raise ValueError(f"{name}: {cols} columns are not {blocks} blocks")
+    return cols
+
+
+def _f8_new(out, name, rows, cols, tile, dtype, dev):
+    """Codes and scales to be written: checked, or made."""
+    torch = _torch()
+    c, s = _f8_shapes(rows, cols, tile)
+    if out is None:
+        return torch.empty(c, dtype=dtype, device=dev), torch.empty(s, dtype=torch.uint8, device=dev)
+    codes, scales = out
+    _gpu(codes, f"{name} codes", dev)
+    _gpu(scales, f"{name} scales", dev)
+    if codes.dtype != dtype or tuple(codes.shape) != c or scales.dtype != torch.uint8 or tuple(scales.shape) != s:
+        raise ValueError(f"{name}: need {c} of {dtype} and {s} of uint8, got {tuple(codes.shape)} of {codes.dtype} and "
+                         f"{tuple(scales.shape)} of {scales.dtype}")
+    return codes, scales
+
+
+def quant_f8(x, tile=False, along="rows", dtype=None, out=None, stream=None):
+    """x [rows, cols] (float32, float16 or bfloat16; rows may lie apart) as 8-bit floats
+    with a power-of-two scale for each 128 elements of a row, or with tile for each 128 x 128.
+
+    along  "rows": -> (codes, scales); "cols": those of the transposed matrix; "both": ((codes,
+           scales), (codes, scales) of the transposed matrix), reading x once.  What a
+           weight gradient sums over is the tokens: it takes "cols" of both its operands
+    dtype  torch.float8_e4m3fn (default) or torch.float8_e5m2
+    out    what is returned, to be written into"""
+    torch = _torch()
+    if along not in ("rows", "cols", "both"):
+        raise ValueError(f"along: rows, cols or both, got {along!r}")
+    if not x.is_cuda:
+        raise ValueError(f"x: need a tensor on a GPU, got one on {x.device}")
+    dtype = dtype or torch.float8_e4m3fn
+    kind, dev = _kind(dtype, "dtype"), x.device
+    rows, cols, ld = _rows(x, "x", dev)
+    st, ctx = _on(stream, dev)
+    with ctx:
+        first, second = out if along == "both" and out is not None else (out, out)
+        a = b = (None, None)
+        if along != "cols":
+            a = _f8_new(first, "out", rows, cols, tile, dtype, dev)
+        if along != "rows":
+            b = _f8_new(second, "out", cols, rows, tile, dtype, dev)
+        ptrs = [None if t is None else t.data_ptr() for t in a + b]
+        _check(lib().zpq_quant_f8(x.data_ptr(), _code(x.dtype), rows, cols, ld, kind, tile, *ptrs, st), "zpq_quant_f8")
+    return (a, b) if along == "both" else a if along == "rows" else b
+
+
+def dequant_f8(codes, scales, cols=None, dtype=None, out=None, stream=None):
+    """The values of an 8-bit matrix -> [rows, cols] of dtype (bfloat16 by default); cols: of
+    the matrix, where they are not whole blocks."""
+    torch = _torch()
+    dev, kind, rows, blocks, tile = _f8_pair((codes, scales), "matrix")
+    cols = _f8_cols(cols, blocks, "cols")
+    st, ctx = _on(stream, dev)
+    with ctx:
+        if out is None:
+            out, ld = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=dev), cols
+        else:
+            ld = _rows_of(out, "out", dev, rows, cols)
+        _check(lib().zpq_dequant_f8(codes.data_ptr(), kind, scales.data_ptr(), rows, cols, tile, out.data_ptr(),
+                                    _code(out.dtype), ld, st), "zpq_dequant_f8")
+    return out
+
+
+def transpose_f8(codes, scales, cols=None, out=None, stream=None):
+    """The transposed matrix of one in tiles -> (codes, scales), the same values."""
+    dev, kind, rows, blocks, tile = _f8_pair((codes, scales), "matrix")
+    if not tile and scales.shape != _f8_shapes(rows, blocks * F8_BLOCK, True)[1]:
+        raise ValueError("scales: need those of tiles")
+    cols = _f8_cols(cols, blocks, "cols")
+    st, ctx = _on(stream, dev)
+    with ctx:
+        to = _f8_new(out, "out", cols, rows, True, codes.dtype, dev)
+        _check(lib().zpq_transpose_f8(codes.data_ptr(), scales.data_ptr(), rows, cols, to[0].data_ptr(),
+                                      to[1].data_ptr(), st), "zpq_transpose_f8")
+    return to
+
+
+@functools.lru_cache(maxsize=1024)
+def _matmul_bytes(m, n, k):
+    need = ctypes.c_int64()
+    _check(lib().zpq_matmul_f8_bytes(m, n, k, ctypes.byref(need)), "zpq_matmul_f8_bytes")
+    return need.value
+
+
+def matmul_f8(a, b, out_dtype=None, out=None, accumulate=False, stream=None):
+    """a @ b.T for 8-bit matrices a [m, k] and b [n, k], pairs as quant_f8 gives them (of either
+    type, along rows or in tiles) -> [m, n] of out_dtype (bfloat16 by default), or
+    out, added to it with accumulate.  Sums are in binary32.  With x, dy [tokens, .] and w
+    [outputs, inputs]: y = x w^T; dx = dy w = matmul_f8(dy, transpose_f8(*w)); dw = dy^T x, of
+    both along their columns."""
+    torch = _torch()
+    dev, ka, m, blocks, ta = _f8_pair(a, "a")
+    _, kb, n, blocks_b, tb = _f8_pair(b, "b", dev)
+    if blocks != blocks_b:
+        raise ValueError(f"a has {blocks} blocks in a row, b has {blocks_b}")
+    k = blocks * F8_BLOCK
+    need = _matmul_bytes(m, n, k)
+    st, ctx = _on(stream, dev)
+    with ctx:
+        if out is not None:
+            ld = _rows_of(out, "out", dev, m, n)
+        elif accumulate:
+            raise ValueError("accumulate needs out")
+        else:
+            out, ld = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev), n
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(lib().zpq_matmul_f8(_F8(a[0].data_ptr(), a[1].data_ptr(), ka, ta), _F8(b[0].data_ptr(), b[1].data_ptr(), kb, tb),
+                                   m, n, k, out.data_ptr(), _code(out.dtype), ld, accumulate,
+                                   None if ws is None else ws.data_ptr(), need, st), "zpq_matmul_f8")
     return out

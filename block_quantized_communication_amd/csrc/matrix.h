@@ -1,0 +1,436 @@
+// matrix.h -- the tile loop of matrix products D = A * B^T on the matrix cores, for
+// operands whose rows are consecutive along the sum: 8-bit floats with a power-of-two
+// scale for each block of 128, or 16-bit floats.
+//
+// The unit along the sum is a slab, 128 bytes of a row: 128 8-bit or 64 16-bit
+// elements.  Either way a lane's share of 16 rows is two 16-byte pieces and one
+// slab of a 16 x 16 tile keeps the matrix core busy for 32 cycles, so both kinds
+// share everything but the instruction.
+//
+// In LDS a slab is [row][128 bytes], the 16-byte piece c of row r at place c ^ (r & 7):
+// 8 lanes that read the same piece of 8 rows then cover all banks.  The
+// copy from global memory to LDS writes 16 bytes a lane in lane order, so the lanes'
+// addresses are permuted instead.
+#ifndef ZPQ_MATRIX_H
+#define ZPQ_MATRIX_H
+
+#include "step.h"
+
+namespace zpq_matrix {
+
+using namespace zpq_step;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kSlab = 128;                    // bytes of a row that one step takes
+constexpr int kF16 = -1;                      // operand kind besides ZPQ_E4M3 and ZPQ_E5M2
+
+// Rows of an operand: `rows` rows of `pitch` bytes (a multiple of 128, at most 2^23),
+// and for 8-bit ones a row of exponent bytes, scale_pitch long (a multiple of 4),
+// for each 2^scale_shift rows.
+struct Operand {
+    const uint8_t* data;
+    const uint8_t* scale;
+    int64_t rows;
+    uint32_t pitch, scale_pitch, scale_shift;
+};
+
+// A buffer descriptor for reading [p, p + bytes): accesses past the end read nothing.
+__device__ __forceinline__ i32x4 descriptor(const void* p, int64_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t n = bytes < 0 ? 0u : bytes > 0xFFFFFFFFll ? 0xFFFFFFFFu : (uint32_t)bytes;
+    i32x4 d;
+    d.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    d.y = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu));
+    d.z = __builtin_amdgcn_readfirstlane((int)n);
+    d.w = 0x00020000;
+    return d;
+}
+
+__device__ __forceinline__ uint32_t scalar(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+
+// Copies 16 (or 4) bytes a lane from global memory to LDS at `to` (of the wave) + 16 (4) *
+// lane.  Not the builtin: the compiler waits for it before any later LDS read.  These
+// have no result register; whoever reads the bytes waits by wait_copies() and a barrier.
+// `offset` and `to` are the same in all lanes.  (Five wait states: a scalar register that a vector
+// instruction has written may be an operand.)  Nothing else in these kernels uses m0.
+__device__ __forceinline__ void copy16(i32x4 from, uint32_t lane_offset, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(scalar(to)), "v"(lane_offset), "s"(from), "s"(scalar(offset)) : "memory");
+}
+__device__ __forceinline__ void copy4(i32x4 from, uint32_t lane_offset, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :: "s"(scalar(to)), "v"(lane_offset), "s"(from), "s"(scalar(offset)) : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Own LDS reads done, then all waves here.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// acc + one slab of 16 rows of B (rows of the result) times 16 rows of A (columns).
+// Lane l gets rows 4 * (l / 16) .. + 3 of column l % 16.  The order of the slab's
+// elements over the lanes does not matter as long as both operands share it, and
+// the one scale of 128 elements is the instruction's four of 32.
+template <int KA, int KB, int SEL>
+__device__ __forceinline__ f32x4 product(i32x8 b, i32x8 a, f32x4 acc, int scale_b, int scale_a) {
+    if constexpr (KA == kF16) {
+        const i32x4 b0 = {b[0], b[1], b[2], b[3]}, b1 = {b[4], b[5], b[6], b[7]};
+        const i32x4 a0 = {a[0], a[1], a[2], a[3]}, a1 = {a[4], a[5], a[6], a[7]};
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b0), __builtin_bit_cast(f16x8, a0),
+                                                     acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b1), __builtin_bit_cast(f16x8, a1),
+                                                      acc, 0, 0, 0);
+    } else {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc, KB, KA, SEL, scale_b, SEL, scale_a);
+    }
+}
+
+// 8 codes with their block's scale as bf16, which holds them exactly.
+template <int KIND>
+__device__ __forceinline__ bf16x8 widen8(int w0, int w1, float scale) {
+    u32x4 r;
+    if constexpr (KIND == ZPQ_E4M3) {
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w0, scale, false));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w0, scale, true));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w1, scale, false));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)w1, scale, true));
+    } else {
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)w0, scale, false));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)w0, scale, true));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)w1, scale, false));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)w1, scale, true));
+    }
+    return __builtin_bit_cast(bf16x8, r);
+}
+// Byte SEL of a word of exponent bytes in the place where widen8 takes a scale's exponent from.
+template <int SEL>
+__device__ __forceinline__ float scale_byte(int word) {
+    const uint32_t e = SEL == 3 ? (uint32_t)word >> 24 : ((uint32_t)word >> (8 * SEL)) & 0xFFu;
+    return __uint_as_float(e << 23);
+}
+
+// acc[i][j] += one slab of a's 16 rows i times b's 16 rows j.  FULL: the 8-bit matrix
+// instructions align their products before they add them and drop what lies more
+// than about 2^-19 below the largest (1.2e-5 of a sum of 128 normal values, whichever instruction
+// and whatever is in acc); the 16-bit ones keep binary32 (5e-8).  So with FULL the codes
+// become bf16 with their scale, which is exact, at half the rate.
+template <int KA, int KB, int SEL, bool FULL, int NA, int NB>
+__device__ __forceinline__ void products(f32x4 (*acc)[NB], const i32x8 (&a)[NA], const i32x8 (&b)[NB], const int* sa,
+                                         const int (&sb)[NB]) {
+    if constexpr (FULL) {
+        float fa[NA], fb[NB];
+#pragma unroll
+        for (int i = 0; i < NA; ++i) fa[i] = scale_byte<SEL>(sa[i]);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) fb[j] = scale_byte<SEL>(sb[j]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            bf16x8 wb[NB];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) wb[j] = widen8<KB>(b[j][2 * q], b[j][2 * q + 1], fb[j]);
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const bf16x8 wa = widen8<KA>(a[i][2 * q], a[i][2 * q + 1], fa[i]);
+#pragma unroll
+                for (int j = 0; j < NB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, acc[i][j], 0, 0, 0);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                acc[i][j] = product<KA, KB, SEL>(b[j], a[i], acc[i][j], KA == kF16 ? 0 : sb[j], KA == kF16 ? 0 : sa[i]);
+    }
+}
+
+// The loop of a 256 x 256 tile: 8 waves, each 128 rows of A by 64 of B, two waves on a
+// SIMD.  Two buffers of one slab of both operands (128 KB of LDS).  The waves of
+// a SIMD take turns: while one reads its pieces of a slab from LDS (and starts the copy of
+// a later slab), the other one multiplies, so the matrix core is fed without a pause
+// although the LDS needs about three quarters of the time.
+//
+// A turn is half a slab: M1 reads 4 pieces of B and 4 of A, C1 multiplies them, M2 reads the
+// other 4 of A, C2 multiplies.  Waves 4-7 are one turn behind.  Slab k + 2 goes into
+// the buffer of slab k, which both are done with 4 turns after the first began to read it:
+// waves 0-3 start their part of the copy in M1 of slab k + 1, waves 4-7 in C2 of slab k,
+// which is the same turn; it has to be there 4 turns (about 2000 cycles) later.
+template <int KA, int KB, bool FULL = false>
+struct Tile256 {
+    static constexpr int BM = 256, BN = 256, kThreadsWg = 512, MI = 8, NI = 4;
+    static constexpr int kSide = 256 * kSlab, kBuffer = 2 * kSide;
+    static constexpr bool kScaled = KA != kF16;
+    static constexpr int kLds = 2 * kBuffer + (kScaled ? 2048 : 0);
+
+    const uint8_t* lds;
+    uint32_t base, wave, lane;
+    i32x4 ra, rb, rs;
+    uint32_t off[4], off_s;                    // both operands' rows have one pitch
+    f32x4 acc[MI][NI];
+    int sa[MI], sb[NI];
+
+    __device__ __forceinline__ uint32_t wm() const { return wave >> 2; }
+    __device__ __forceinline__ uint32_t wn() const { return wave & 3; }
+
+    __device__ __forceinline__ void start_copy(int slab, int buffer) {
+        const uint32_t to = base + buffer * kBuffer + wave * 4096;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            copy16(ra, off[i], (uint32_t)slab * kSlab, to + i * 1024);
+            copy16(rb, off[i], (uint32_t)slab * kSlab, to + kSide + i * 1024);
+        }
+        if constexpr (kScaled)
+            if ((slab & 3) == 0) copy4(rs, off_s, (uint32_t)slab, base + 2 * kBuffer + wave * 256);
+    }
+    __device__ __forceinline__ i32x8 piece(const uint8_t* side, uint32_t row) const {
+        const uint32_t r = lane & 15, g = lane >> 4;
+        const uint8_t* p = side + (row + r) * kSlab;
+        const i32x4 x = *reinterpret_cast<const i32x4*>(p + ((g ^ (r & 7)) << 4));
+        const i32x4 y = *reinterpret_cast<const i32x4*>(p + (((g + 4) ^ (r & 7)) << 4));
+        return i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    }
+    // Slab `slab` of [.., end), SEL = its number from the first one modulo 4.
+    template <int SEL>
+    __device__ __forceinline__ void step(int slab, int end) {
+        constexpr int buffer = SEL & 1;
+        const uint8_t* side_a = lds + buffer * kBuffer + wm() * 128 * kSlab;
+        const uint8_t* side_b = lds + buffer * kBuffer + kSide + wn() * 64 * kSlab;
+        i32x8 fb[NI], fa[MI / 2];
+        // M1
+        if (wm() == 0 && slab + 1 < end) start_copy(slab + 1, buffer ^ 1);
+        if constexpr (kScaled && SEL == 0) {
+            const int* s = reinterpret_cast<const int*>(lds + 2 * kBuffer) + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) sa[i] = s[wm() * 128 + i * 16];
+#pragma unroll
+            for (int j = 0; j < NI; ++j) sb[j] = s[256 + wn() * 64 + j * 16];
+        }
+#pragma unroll
+        for (int j = 0; j < NI; ++j) fb[j] = piece(side_b, j * 16);
+#pragma unroll
+        for (int i = 0; i < MI / 2; ++i) fa[i] = piece(side_a, i * 16);
+        meet();
+        __builtin_amdgcn_sched_barrier(0);
+        // C1
+        multiply<SEL, 0>(fb, fa);
+        __builtin_amdgcn_sched_barrier(0);
+        meet();
+        __builtin_amdgcn_sched_barrier(0);
+        // M2
+#pragma unroll
+        for (int i = 0; i < MI / 2; ++i) fa[i] = piece(side_a, (MI / 2 + i) * 16);
+        if (wm() == 1) wait_copies();
+        meet();
+        __builtin_amdgcn_sched_barrier(0);
+        // C2
+        if (wm() == 1 && slab + 2 < end) start_copy(slab + 2, buffer);
+        multiply<SEL, MI / 2>(fb, fa);
+        __builtin_amdgcn_sched_barrier(0);
+        if (wm() == 0) wait_copies();
+        meet();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    template <int SEL, int FIRST>
+    __device__ __forceinline__ void multiply(const i32x8 (&fb)[NI], const i32x8 (&fa)[MI / 2]) {
+        __builtin_amdgcn_s_setprio(1);
+        products<KA, KB, SEL, FULL>(acc + FIRST, fa, fb, sa + FIRST, sb);
+        // in this turn, not later: without this the compiler moves the products behind the turn's end
+#pragma unroll
+        for (int i = 0; i < MI / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[FIRST + i][j]));
+        __builtin_amdgcn_s_setprio(0);
+    }
+
+    // Sums slabs [first, end), first < end, first a multiple of 4, of the tile that starts
+    // at row row_a of A and row_b of B (multiples of 256).
+    __device__ __forceinline__ void run(const Operand& a, const Operand& b, int64_t row_a, int64_t row_b, int first,
+                                        int end, uint8_t* shared) {
+        first = (int)scalar((uint32_t)first);
+        end = (int)scalar((uint32_t)end);
+        lds = shared;
+        base = lds_address(shared);
+        lane = threadIdx.x & 63;
+        wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        ra = descriptor(a.data + row_a * a.pitch, (a.rows - row_a) * a.pitch);
+        rb = descriptor(b.data + row_b * b.pitch, (b.rows - row_b) * b.pitch);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t r = wave * 32 + i * 8 + (lane >> 3);
+            off[i] = r * a.pitch + (((lane & 7) ^ (r & 7)) << 4);
+        }
+        if constexpr (kScaled) {
+            const Operand& o = wave < 4 ? a : b;
+            const int64_t row = (wave < 4 ? row_a : row_b) >> o.scale_shift;
+            const int64_t rows = ((o.rows - 1) >> o.scale_shift) + 1;
+            rs = descriptor(o.scale + row * o.scale_pitch, (rows - row) * o.scale_pitch);
+            off_s = (((wave & 3) * 64 + lane) >> o.scale_shift) * o.scale_pitch;
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        start_copy(first, 0);
+        if (wm() == 1 && first + 1 < end) start_copy(first + 1, 1);
+        wait_copies();
+        meet();
+        if (wm() == 1) meet();
+        for (int slab = first; slab < end; slab += 4) {
+            step<0>(slab, end);
+            if (slab + 1 < end) step<1>(slab + 1, end);
+            if (slab + 2 < end) step<2>(slab + 2, end);
+            if (slab + 3 < end) step<3>(slab + 3, end);
+        }
+        if (wm() == 0) meet();
+    }
+    // f(row of A in the tile, first of 4 rows of B in the tile, sums)
+    template <class F>
+    __device__ __forceinline__ void each(F&& f) const {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                f(wm() * 128 + i * 16 + (lane & 15), wn() * 64 + j * 16 + (lane >> 4) * 4, acc[i][j]);
+    }
+};
+
+// The loop of a smaller tile: 4 waves, 2 x 2, each MI * 16 rows of A by NI * 16 of B, two
+// buffers.  Several workgroups of a CU hide each other's waits.
+template <int KA, int KB, int MI_, int NI_, bool FULL = false>
+struct TileSmall {
+    static constexpr int MI = MI_, NI = NI_, BM = 32 * MI, BN = 32 * NI, kThreadsWg = 256;
+    static constexpr int kSideA = BM * kSlab, kSideB = BN * kSlab, kBuffer = kSideA + kSideB;
+    static constexpr bool kScaled = KA != kF16;
+    static constexpr int kScaleBytes = kScaled ? (BM + BN) * 4 : 0;
+    static constexpr int kLds = 2 * kBuffer + kScaleBytes;
+    static_assert(BM + BN <= 256, "one exponent word a thread");
+
+    const uint8_t* lds;
+    uint32_t base, wave, lane;
+    i32x4 ra, rb, rs;
+    uint32_t off_a[MI], off_b[NI], off_s;
+    f32x4 acc[MI][NI];
+    int sa[MI], sb[NI];
+
+    __device__ __forceinline__ uint32_t wm() const { return wave >> 1; }
+    __device__ __forceinline__ uint32_t wn() const { return wave & 1; }
+
+    __device__ __forceinline__ void start_copy(int slab, int buffer) {
+        const uint32_t to = base + buffer * kBuffer;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) copy16(ra, off_a[i], (uint32_t)slab * kSlab, to + (wave * MI + i) * 1024);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) copy16(rb, off_b[j], (uint32_t)slab * kSlab, to + kSideA + (wave * NI + j) * 1024);
+    }
+    __device__ __forceinline__ void start_scales(int slab) {
+        if constexpr (kScaled)
+            if (wave * 64 < BM + BN) copy4(rs, off_s, (uint32_t)slab, base + 2 * kBuffer + wave * 256);
+    }
+    __device__ __forceinline__ i32x8 piece(const uint8_t* side, uint32_t row) const {
+        const uint32_t r = lane & 15, g = lane >> 4;
+        const uint8_t* p = side + (row + r) * kSlab;
+        const i32x4 x = *reinterpret_cast<const i32x4*>(p + ((g ^ (r & 7)) << 4));
+        const i32x4 y = *reinterpret_cast<const i32x4*>(p + (((g + 4) ^ (r & 7)) << 4));
+        return i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    }
+    template <int SEL>
+    __device__ __forceinline__ void step(int slab, int end) {
+        constexpr int buffer = SEL & 1;
+        wait_copies();
+        meet();                               // slab is there, and the other buffer read
+        if constexpr (kScaled && SEL == 0) {
+            const int* s = reinterpret_cast<const int*>(lds + 2 * kBuffer) + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) sa[i] = s[(wm() * MI + i) * 16];
+#pragma unroll
+            for (int j = 0; j < NI; ++j) sb[j] = s[BM + (wn() * NI + j) * 16];
+        }
+        if (slab + 1 < end) {
+            start_copy(slab + 1, buffer ^ 1);
+            if constexpr (SEL == 3) start_scales(slab + 1);
+        }
+        const uint8_t* side_a = lds + buffer * kBuffer + wm() * MI * 16 * kSlab;
+        const uint8_t* side_b = lds + buffer * kBuffer + kSideA + wn() * NI * 16 * kSlab;
+        i32x8 fb[NI], fa[MI];
+#pragma unroll
+        for (int j = 0; j < NI; ++j) fb[j] = piece(side_b, j * 16);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i] = piece(side_a, i * 16);
+        products<KA, KB, SEL, FULL>(acc, fa, fb, sa, sb);
+    }
+    // As Tile256::run; row_a and row_b multiples of BM and BN.
+    __device__ __forceinline__ void run(const Operand& a, const Operand& b, int64_t row_a, int64_t row_b, int first,
+                                        int end, uint8_t* shared) {
+        first = (int)scalar((uint32_t)first);
+        end = (int)scalar((uint32_t)end);
+        lds = shared;
+        base = lds_address(shared);
+        lane = threadIdx.x & 63;
+        wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        ra = descriptor(a.data + row_a * a.pitch, (a.rows - row_a) * a.pitch);
+        rb = descriptor(b.data + row_b * b.pitch, (b.rows - row_b) * b.pitch);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const uint32_t r = (wave * MI + i) * 8 + (lane >> 3);
+            off_a[i] = r * a.pitch + (((lane & 7) ^ (r & 7)) << 4);
+        }
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const uint32_t r = (wave * NI + j) * 8 + (lane >> 3);
+            off_b[j] = r * b.pitch + (((lane & 7) ^ (r & 7)) << 4);
+        }
+        if constexpr (kScaled) {
+            const bool of_a = wave * 64 < BM;
+            const Operand& o = of_a ? a : b;
+            const int64_t row = of_a ? row_a : row_b, within = wave * 64 + lane - (of_a ? 0 : BM);
+            const int64_t first_scale = row >> o.scale_shift, rows = ((o.rows - 1) >> o.scale_shift) + 1;
+            rs = descriptor(o.scale + first_scale * o.scale_pitch, (rows - first_scale) * o.scale_pitch);
+            off_s = (uint32_t)(((row + within) >> o.scale_shift) - first_scale) * o.scale_pitch;
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        start_copy(first, 0);
+        start_scales(first);
+        for (int slab = first; slab < end; slab += 4) {
+            step<0>(slab, end);
+            if (slab + 1 < end) step<1>(slab + 1, end);
+            if (slab + 2 < end) step<2>(slab + 2, end);
+            if (slab + 3 < end) step<3>(slab + 3, end);
+        }
+    }
+    template <class F>
+    __device__ __forceinline__ void each(F&& f) const {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                f((wm() * MI + i) * 16 + (lane & 15), (wn() * NI + j) * 16 + (lane >> 4) * 4, acc[i][j]);
+    }
+};
+
+// Workgroup `id` of `count` to tile (i, j) of rows x columns tiles.  Workgroups go to the 8
+// XCDs in turn, and each XCD has an L2 of its own: the ids of one XCD become consecutive
+// tiles of bands of 8 tile rows, so that the 32 tiles it works on at a time share 8 row and
+// 4 column strips.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t count, uint32_t rows, uint32_t columns, uint32_t& i,
+                                        uint32_t& j) {
+    const uint32_t q = count / 8, r = count % 8, x = id % 8;
+    const uint32_t t = x * q + (x < r ? x : r) + id / 8;
+    const uint32_t band = t / (8 * columns), in = t - band * 8 * columns;
+    const uint32_t high = rows - band * 8 < 8 ? rows - band * 8 : 8;
+    j = in / high;
+    i = band * 8 + (in - j * high);
+}
+
+}  // namespace zpq_matrix
+
+#endif  // ZPQ_MATRIX_H

@@ -342,6 +342,75 @@ zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, c
                               int32_t grad_dtype, int64_t ld_grad, int32_t accumulate,
                               void* workspace, int64_t workspace_bytes, zpq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Matrix products of the step, from 8-bit floating-point blocks.  A rank quantizes
+ * its rows of a weight in tiles (zpq_quant_f8); whole tiles gather by
+ * concatenation as qwZ's codes do, and the products take the gathered buffer as it
+ * is.  (Defined here, as the operators above; the same conventions.)
+ *
+ * A matrix [rows, cols] in 8-bit floating point, quantized along its rows:
+ *   codes   [rows][128 * kb] bytes, kb = ceil(cols / 128): OCP E4M3 or E5M2; codes
+ *           past the last column are 0
+ *   scales  [rows][kb4] exponent bytes, kb4 = kb rounded up to a multiple of 4; those
+ *           past kb are 0.  One for each 128 elements of a row, or in tiles, [ceil(rows / 128)][kb4]:
+ *           one for each 128 x 128.
+ * An element is code * 2^(byte - 127).  With a the block's largest magnitude, byte is
+ * the smallest for which a <= 1.75 * 2^t * 2^(byte - 127), t = 8 for E4M3 and 15 for E5M2
+ * (the format's largest value), at least 0; code = RNE(x * 2^(127 - byte)).  A
+ * block with a value that is not finite has byte 255 and NaNs for codes.
+ * Pointers to codes and scales are 16-byte aligned.  128 * kb at most 2^23.
+ */
+typedef enum { ZPQ_E4M3 = 0, ZPQ_E5M2 = 1 } zpq_f8_kind;
+
+/*
+ * Quantize x, `rows` rows of cols elements of x_dtype, ld apart: along its rows into codes
+ * and scales, along its columns into codes_t [cols][128 * ceil(rows / 128)] and scales_t
+ * (the transposed matrix along its rows), or both at once; each pair may be NULL, not
+ * both (ZPQ_ERR_MODE).  With tile, blocks are 128 x 128, and both pairs hold the same values.
+ * x needs its element's alignment; rows * kb below 2^28, and of tiles and column
+ * blocks below 2^24 squares of 128 x 128.
+ */
+zpq_status zpq_quant_f8(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                        int32_t kind, int32_t tile, uint8_t* codes, uint8_t* scales,
+                        uint8_t* codes_t, uint8_t* scales_t, zpq_stream stream);
+
+/* Values back, rounded to nearest even into y_dtype: y [rows] rows of cols elements, ld apart. */
+zpq_status zpq_dequant_f8(const uint8_t* codes, int32_t kind, const uint8_t* scales, int64_t rows,
+                          int64_t cols, int32_t tile, void* y, int32_t y_dtype, int64_t ld,
+                          zpq_stream stream);
+
+/* The transposed matrix of one in tiles, the same values: [cols][128 * ceil(rows / 128)]. */
+zpq_status zpq_transpose_f8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                            uint8_t* codes_t, uint8_t* scales_t, zpq_stream stream);
+
+typedef struct {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int32_t kind;        /* zpq_f8_kind */
+    int32_t tile;        /* scales of 128 x 128 */
+} zpq_f8_operand;
+
+/*
+ * out = [out +] A * B^T for A [m, k] and B [n, k]:
+ *   out[i][j] = RNE([out[i][j] +] sum over k of a[i][k] * b[j][k])
+ * with exact products and sums in binary32, in an order that depends on the sizes only.
+ * For 16-bit results the matrix core drops what lies more than about 2^-19 below the largest of the
+ * products that it adds at a time (1e-5 of a sum of like values, far below the result's
+ * rounding).  For ZPQ_F32 results elements are multiplied as 16-bit floats of binary32's
+ * range, which holds them exactly, at half the rate and to binary32's precision; there an
+ * element over the largest binary32 is infinite, and one below 2^-126 may count as 0.  With x, dy the input and
+ * output gradient [tokens, .] and w [outputs, inputs]: y = x w^T; dx = dy w takes w's
+ * transposed tiles for B; dw = dy^T x takes both along their columns.
+ *   out [m] rows of n elements of out_dtype, ld apart; read with accumulate only
+ *   workspace: zpq_matmul_f8_bytes bytes of device memory (0 for most sizes),
+ *   16-byte aligned, contents irrelevant
+ * m, n < 2^31, ceil(m / 64) * ceil(n / 64) < 2^23; k = 0 is a sum of nothing.
+ */
+zpq_status zpq_matmul_f8_bytes(int64_t m, int64_t n, int64_t k, int64_t* bytes);
+zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64_t m, int64_t n,
+                         int64_t k, void* out, int32_t out_dtype, int64_t ld, int32_t accumulate,
+                         void* workspace, int64_t workspace_bytes, zpq_stream stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* zpq_status_str(zpq_status s);
 
