@@ -27,6 +27,8 @@ Around the communication path (tensors need their element's alignment only):
   quant_f8(x, tile, along)                   8-bit floats in blocks of 128 along rows, columns or both, or in tiles
   dequant_f8, transpose_f8                   their values; the transposed matrix of tiles
   matmul_f8(a, b)                            a @ b.T of two such matrices
+  orthogonalize(x)                           nearest orthogonal matrices, by Newton-Schulz products
+  Muon(params, grads, ...)                   the optimizer step with orthogonalised updates, for matrices
 """
 import bisect
 import contextlib
@@ -48,7 +50,9 @@ EXPORTS = ("zpq_quant_i8", "zpq_dequant_i8", "zpq_quant_i8_tensor", "zpq_qgz_reo
            "zpq_adamw_step_at",
            "zpq_state8_unpack", "zpq_state8_pack", "zpq_embedding", "zpq_embedding_i8",
            "zpq_embedding_grad_bytes", "zpq_embedding_grad", "zpq_quant_f8", "zpq_dequant_f8",
-           "zpq_transpose_f8", "zpq_matmul_f8_bytes", "zpq_matmul_f8")
+           "zpq_transpose_f8", "zpq_matmul_f8_bytes", "zpq_matmul_f8",
+           "zpq_orthogonalize_bytes", "zpq_orthogonalize", "zpq_muon_plan_bytes", "zpq_muon_plan_make",
+           "zpq_muon_step")
 
 STATE_BLOCK = 256          # elements that share an exponent byte in 8-bit optimizer states
 LIST_FIXED_BYTES = 20736   # ZPQ_LIST_BYTES(0)
@@ -83,6 +87,23 @@ class _AdamwHyper(ctypes.Structure):
 class _F8(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("kind", ctypes.c_int32),
                 ("tile", ctypes.c_int32)]
+
+
+class _MuonMatrix(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+                ("scale", ctypes.c_double)]
+
+
+class _MuonPlan(ctypes.Structure):
+    _fields_ = [("memory", ctypes.c_void_p), ("matrices", ctypes.POINTER(_MuonMatrix)), ("count", ctypes.c_int32),
+                ("p_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32)]
+
+
+class _MuonHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("coeffs", ctypes.POINTER(ctypes.c_double)), ("steps", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32)]
 
 
 class ZpqError(RuntimeError):
@@ -129,12 +150,19 @@ def lib():
         L.zpq_matmul_f8_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
         L.zpq_matmul_f8.argtypes = [ctypes.POINTER(_F8), ctypes.POINTER(_F8), i64, i64, i64, vp, i32, i64, i32, vp,
                                     i64, vp]
+        L.zpq_orthogonalize_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+        L.zpq_orthogonalize.argtypes = [vp, i32, i64, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_double), i32, vp, i32, i64,
+                                        i64, vp, i64, vp]
+        L.zpq_muon_plan_bytes.argtypes = [ctypes.POINTER(_MuonMatrix), i32, ctypes.POINTER(i64)]
+        L.zpq_muon_plan_make.argtypes = [ctypes.POINTER(_MuonMatrix), i32, i32, i32, i32, vp, i64, ctypes.POINTER(_MuonPlan), vp]
+        L.zpq_muon_step.argtypes = [ctypes.POINTER(_MuonPlan), ctypes.POINTER(_MuonHyper), vp, vp]
         for f in (L.zpq_quant_i8, L.zpq_dequant_i8, L.zpq_quant_i8_tensor,
                   L.zpq_qgz_reorder_quant_i4, L.zpq_qgz_dequant_reduce_requant_i4,
                   L.zpq_list_make, L.zpq_grad_sumsq, L.zpq_adamw_plan_make, L.zpq_adamw_step,
                   L.zpq_adamw_step_at, L.zpq_state8_unpack, L.zpq_state8_pack, L.zpq_embedding, L.zpq_embedding_i8,
                   L.zpq_embedding_grad_bytes, L.zpq_embedding_grad, L.zpq_quant_f8, L.zpq_dequant_f8,
-                  L.zpq_transpose_f8, L.zpq_matmul_f8_bytes, L.zpq_matmul_f8):
+                  L.zpq_transpose_f8, L.zpq_matmul_f8_bytes, L.zpq_matmul_f8, L.zpq_orthogonalize_bytes,
+                  L.zpq_orthogonalize, L.zpq_muon_plan_bytes, L.zpq_muon_plan_make, L.zpq_muon_step):
             f.restype = ctypes.c_int
         L.zpq_status_str.argtypes = [ctypes.c_int]
         L.zpq_status_str.restype = ctypes.c_char_p
@@ -955,3 +983,214 @@ def matmul_f8(a, b, out_dtype=None, out=None, accumulate=False, stream=None):
                                    m, n, k, out.data_ptr(), _code(out.dtype), ld, accumulate,
                                    None if ws is None else ws.data_ptr(), need, st), "zpq_matmul_f8")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Orthogonalised updates.
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)      # five times: singular values to between 0.7 and 1.2
+
+
+@functools.lru_cache(maxsize=64)
+def _coeffs(coeffs, steps):
+    """(host array [steps][3], steps): one triple for every step, or one for each."""
+    flat = [c for triple in coeffs for c in triple] if hasattr(coeffs[0], "__len__") else list(coeffs) * steps
+    if len(flat) != 3 * steps:
+        raise ValueError(f"coeffs: need three numbers, or three for each of {steps} steps")
+    return (ctypes.c_double * max(len(flat), 1))(*flat), steps
+
+
+def _coeffs_of(coeffs, steps):
+    return _coeffs(tuple(tuple(c) if hasattr(c, "__len__") else float(c) for c in coeffs), int(steps))
+
+
+@functools.lru_cache(maxsize=256)
+def _orthogonalize_bytes(count, rows, cols):
+    need = ctypes.c_int64()
+    _check(lib().zpq_orthogonalize_bytes(count, rows, cols, ctypes.byref(need)), "zpq_orthogonalize_bytes")
+    return need.value
+
+
+def _stack(t, name, device):
+    """t as matrices: 2-D, or 3-D with equally spaced ones, their rows contiguous (they may lie apart);
+    (count, rows, cols, distance of rows, of matrices)."""
+    if t.dim() == 2:
+        return (1,) + _rows(t, name, device) + (0,)
+    if t.dim() == 3 and t.device == device:
+        count, rows, cols = t.shape
+        apart, ld, step = t.stride()
+        if count == 0 or rows == 0 or cols == 0:
+            return count, rows, cols, cols, rows * cols
+        if step == 1 or cols == 1:
+            ld = cols if rows == 1 else ld
+            span = (rows - 1) * ld + cols
+            if ld >= cols and (count == 1 or apart >= span):
+                return count, rows, cols, ld, apart if count > 1 else span
+        raise ValueError(f"{name}: rows or matrices overlap, or rows are not contiguous (strides {tuple(t.stride())})")
+    raise ValueError(f"{name}: need a 2-D or 3-D tensor on {device}, got {tuple(t.shape)} on {t.device}")
+
+
+def orthogonalize(x, steps=5, coeffs=NEWTON_SCHULZ, out_dtype=None, out=None, stream=None):
+    """x [rows, cols], or [count, rows, cols] of one shape, with its singular values driven towards 1
+    by `steps` Newton-Schulz steps X <- a X + (b A + c A A) X, A = X X^T, from X = x / |x| -> out_dtype
+    (bfloat16 by default, or float16).  coeffs: (a, b, c), or one triple for each step.  Zeros stay
+    zeros; a matrix that is not finite comes out as NaN."""
+    torch = _torch()
+    if not x.is_cuda:
+        raise ValueError(f"x: need a tensor on a GPU, got one on {x.device}")
+    dev = x.device
+    count, rows, cols, ld, apart = _stack(x, "x", dev)
+    c, steps = _coeffs_of(coeffs, steps)
+    need = _orthogonalize_bytes(count, rows, cols)
+    st, ctx = _on(stream, dev)
+    with ctx:
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype or torch.bfloat16, device=dev)
+        elif out.shape != x.shape:
+            raise ValueError(f"out: need {tuple(x.shape)}, got {tuple(out.shape)}")
+        _, _, _, lo, apart_o = _stack(out, "out", dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(lib().zpq_orthogonalize(x.data_ptr(), _code(x.dtype), count, rows, cols, ld, apart, c, steps, out.data_ptr(),
+                                       _code(out.dtype), lo, apart_o, None if ws is None else ws.data_ptr(), need, st),
+               "zpq_orthogonalize")
+    return out
+
+
+class Muon:
+    """The Muon step over many matrices: momentum, orthogonalised by Newton-Schulz products, added
+    to the weights.  For a layer's matrices; its vectors and embeddings are AdamW's.
+
+    params        matrices of one type (float32, or float16 / bfloat16 without a master copy), updated in place
+    grads         their gradients, of one type
+    copies        with float32 params: float16 or bfloat16 tensors that receive the new weights
+    weight_decay  one number, or one per matrix
+    scale         of the orthogonal update, one number or one per matrix; by default
+                  0.2 * sqrt(max(rows, cols)), about the size of an AdamW update at the same lr
+    momenta       existing momenta, float32, one per matrix; zeros are made where not given
+
+    Whole matrices: a rank of a sharded step gives those that it owns.  Tensors are kept and
+    their addresses laid out once, on `stream` (the current one by default; later calls must come
+    after it in stream order): storage must not be replaced meanwhile; set_grads() takes other
+    gradients.  The object's memory, which the steps work in, holds about 12 bytes for each element
+    of its largest matrix, or of 2^26 elements of smaller ones.  A captured graph holds its addresses: keep
+    the object as long as the graph."""
+
+    def __init__(self, params, grads, copies=None, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None,
+                 steps=5, coeffs=NEWTON_SCHULZ, momenta=None, stream=None):
+        torch = _torch()
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("params: need at least one matrix")
+        self.device = _one_device(self.params, "params")
+        for i, p in enumerate(self.params):
+            if p.dim() != 2:
+                raise ValueError(f"params[{i}]: need a matrix, got {tuple(p.shape)}")
+        self._pd = _one_dtype(self.params, "params")
+        self.lr, self.momentum, self.nesterov = lr, momentum, nesterov
+        self._c, self.steps = _coeffs_of(coeffs, steps)
+        count = len(self.params)
+        if scale is None:
+            scale = [0.2 * max(p.shape) ** 0.5 for p in self.params]
+        self.weight_decay, self.scale = (list(v) if hasattr(v, "__len__") else [v] * count for v in (weight_decay, scale))
+        for name in ("weight_decay", "scale"):
+            if len(getattr(self, name)) != count:
+                raise ValueError(f"{name}: need {count} numbers, got {len(getattr(self, name))}")
+        self.copies = None if copies is None else list(copies)
+        self._cd = -1
+        if self.copies is not None:
+            self._match(self.copies, "copies")
+            self._cd = _one_dtype(self.copies, "copies")
+            if self._cd == ZPQ_F32 or self._pd != ZPQ_F32:
+                raise ValueError("copies: need float16 or bfloat16 tensors beside float32 params")
+        self._held = _Held()
+        st, ctx = _on(stream, self.device)
+        with ctx:
+            if momenta is None:
+                self.momenta = [torch.zeros(p.shape, dtype=torch.float32, device=self.device) for p in self.params]
+                self._held.add(self.momenta, st)
+            else:
+                self.momenta = list(momenta)
+                self._match(self.momenta, "momenta")
+                for i, t in enumerate(self.momenta):
+                    _need(t, torch.float32, t.numel(), f"momenta[{i}]", self.device)
+        self._rows = (_MuonMatrix * count)()
+        spans = []                                     # of what the step writes
+        for i, (r, p, m) in enumerate(zip(self._rows, self.params, self.momenta)):
+            written = [p, m] if self.copies is None else [p, m, self.copies[i]]
+            r.p, r.m, (r.rows, r.cols) = p.data_ptr(), m.data_ptr(), p.shape
+            if self.copies is not None:
+                r.copy = self.copies[i].data_ptr()
+            r.weight_decay, r.scale = self.weight_decay[i], self.scale[i]
+            if p.numel():
+                spans += [(a, a + t.numel() * t.element_size()) for t in written for a in (t.data_ptr(),)]
+        spans.sort()
+        self._starts, self._ends = [a for a, _ in spans], [b for _, b in spans]
+        if any(b > a for b, a in zip(self._ends, self._starts[1:])):
+            raise ValueError("params, copies and momenta overlap in memory (tied weights are one matrix)")
+        need = ctypes.c_int64()
+        _check(lib().zpq_muon_plan_bytes(self._rows, count, ctypes.byref(need)), "zpq_muon_plan_bytes")
+        with ctx:
+            self._memory = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        self._held.add([self._memory], st)
+        self._list = None
+        self.set_grads(grads, stream=stream)
+
+    def _match(self, tensors, name):
+        if len(tensors) != len(self.params):
+            raise ValueError(f"{name}: need {len(self.params)} tensors, got {len(tensors)}")
+        for i, (t, p) in enumerate(zip(tensors, self.params)):
+            _gpu(t, f"{name}[{i}]", self.device)
+            if t.shape != p.shape:
+                raise ValueError(f"{name}[{i}]: need {tuple(p.shape)}, got {tuple(t.shape)}")
+
+    def set_grads(self, grads, stream=None):
+        """Take these gradients, of the type of the first ones, from the next call on (in stream order), also
+        in a captured norm or step."""
+        grads = list(grads)
+        self._match(grads, "grads")
+        gd = _one_dtype(grads, "grads")
+        if self._list is not None and gd != self._gd:
+            raise ValueError(f"grads: need {self.grads[0].dtype}, got {grads[0].dtype}")
+        width = grads[0].element_size()
+        starts, ends = self._starts, self._ends
+        for g in grads:
+            a, n = g.data_ptr(), g.numel()
+            j = bisect.bisect_right(starts, a)
+            if n and ((j and ends[j - 1] > a) or (j < len(starts) and starts[j] < a + n * width)):
+                raise ValueError("grads overlap what the step writes")
+        st, ctx = _on(stream, self.device)
+        self._held.used(st, stream, self.device)
+        plan = _MuonPlan()
+        for r, g in zip(self._rows, grads):
+            r.g = g.data_ptr()
+        with ctx:
+            made = self._list
+            if made is None:
+                made = TensorList.__new__(TensorList)
+                made.device = self.device
+                made._allocate(len(grads), stream)
+            _check(lib().zpq_muon_plan_make(self._rows, len(grads), self._pd, gd, self._cd, self._memory.data_ptr(),
+                                            self._memory.numel(), ctypes.byref(plan), st), "zpq_muon_plan_make")
+            made._lay_out([g.data_ptr() for g in grads], [g.numel() for g in grads], gd, stream)
+            made.tensors = grads
+            self._plan, self._ref, self._list, self.grads, self._gd = plan, ctypes.byref(plan), made, grads, gd
+
+    def grad_sumsq(self, out=None, accumulate=False, stream=None):
+        """Sum of squares of the gradients -> float64 [1] (see grad_sumsq)."""
+        return grad_sumsq(self._list, out=out, accumulate=accumulate, stream=stream)
+
+    def step(self, lr=None, grad_scale=1.0, sumsq=None, max_norm=None, stream=None):
+        """One step.  sumsq: float64 [1] on the GPU, the squared norm of the unscaled gradients over all
+        ranks and optimizers; where it is not finite nothing changes.  max_norm: clip the scaled
+        gradients to it (needs sumsq)."""
+        norm = None
+        if sumsq is not None:
+            _need(sumsq, _torch().float64, 1, "sumsq", self.device)
+            norm = sumsq.data_ptr()
+        elif max_norm is not None:
+            raise ValueError("max_norm needs sumsq")
+        h = _MuonHyper(self.lr if lr is None else lr, self.momentum, grad_scale, _INF if max_norm is None else max_norm,
+                       self._c, self.steps, self.nesterov)
+        st, ctx = _on(stream, self.device)
+        self._held.used(st, stream, self.device)
+        with ctx:
+            _check(lib().zpq_muon_step(self._ref, ctypes.byref(h), norm, st), "zpq_muon_step")

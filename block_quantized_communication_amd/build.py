@@ -21,7 +21,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "zpq.hip")
-SOURCES = [SRC] + [os.path.join(HERE, "csrc", f) for f in ("adamw.hip", "embedding.hip", "float8.hip")]
+SOURCES = [SRC] + [os.path.join(HERE, "csrc", f) for f in ("adamw.hip", "embedding.hip", "float8.hip", "muon.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libzpq.so")
 ARCH = "gfx950"

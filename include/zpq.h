@@ -411,6 +411,89 @@ zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64
                          int64_t k, void* out, int32_t out_dtype, int64_t ld, int32_t accumulate,
                          void* workspace, int64_t workspace_bytes, zpq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Orthogonalising updates, and the Muon step of a layer's matrices beside AdamW's of the
+ * rest.  Conventions as above.
+ *
+ * The Newton-Schulz iteration on a matrix U [rows, cols]:
+ *   X = U / |U|_F (0 where the norm is 0), transposed while rows > cols
+ *   for each of `steps` triples (a, b, c) in coeffs [steps][3], a host array:
+ *       A = X X^T;  X = a X + (b A + c A A) X
+ * which drives the singular values that are not 0 to about 1: with (3.4445, -4.7750, 2.0315)
+ * five times, to between 0.7 and 1.2.  Products take 16-bit operands (11 bits), with
+ * sums and X itself in binary32; the result is within about 2e-3 of the exact iteration's, so it
+ * comes in 16 bits.  A matrix with a value that is not finite comes out as NaN.
+ * 1 <= steps <= 32, coefficients at most 64 in size, such that singular values stay under 50.
+ * rows, cols <= 2^22, rows * cols <= 2^34.
+ */
+/*
+ * out_i = iteration(x_i) for `count` matrices of one shape, at most 2^20.
+ *   x     [rows] rows of cols elements of x_dtype, ld_x apart, matrices stride_x apart
+ *   out   likewise; out_dtype ZPQ_F16 or ZPQ_BF16
+ *   workspace: zpq_orthogonalize_bytes bytes of device memory, 256-byte aligned,
+ *   contents irrelevant.  Matrices are worked on about 2^26 elements at a time, which
+ *   bounds it.
+ */
+zpq_status zpq_orthogonalize_bytes(int64_t count, int64_t rows, int64_t cols, int64_t* bytes);
+zpq_status zpq_orthogonalize(const void* x, int32_t x_dtype, int64_t count, int64_t rows,
+                             int64_t cols, int64_t ld_x, int64_t stride_x, const double* coeffs,
+                             int32_t steps, void* out, int32_t out_dtype, int64_t ld_out,
+                             int64_t stride_out, void* workspace, int64_t workspace_bytes,
+                             zpq_stream stream);
+
+/* One matrix of a Muon step, rows * cols consecutive elements each; device
+ * pointers.  The matrices of a plan must not overlap, nor a matrix's own parts. */
+typedef struct {
+    void* p;             /* weights                                        (updated) */
+    const void* g;       /* gradient */
+    void* m;             /* momentum, fp32                                 (updated) */
+    void* copy;          /* the new weights in copy_dtype, or NULL         (written) */
+    int64_t rows, cols;
+    double weight_decay; /* >= 0 */
+    double scale;        /* >= 0: of the orthogonal update; 0.2 * sqrt(max(rows, cols)) gives it
+                            about the size of an AdamW update */
+} zpq_muon_matrix;
+
+typedef struct {
+    void* memory;
+    const zpq_muon_matrix* matrices;   /* the host array, which has to stay as it is */
+    int32_t count, p_dtype, g_dtype, copy_dtype;
+} zpq_muon_plan;
+
+/* Device memory of a plan's table alone; zpq_muon_plan_bytes: with the workspace, which
+ * is bounded as zpq_orthogonalize's. */
+#define ZPQ_MUON_BYTES(count) ((int64_t)(count) * 216 + 64)
+
+/*
+ * Lay out `count` matrices for zpq_muon_step, at most 2^20.  Types as in zpq_adamw_plan_make.  The
+ * table in memory (256-byte aligned) is written by small kernels on `stream`; the rest of the
+ * memory is the step's workspace, so steps of one plan must be ordered.
+ */
+zpq_status zpq_muon_plan_bytes(const zpq_muon_matrix* matrices, int32_t count, int64_t* bytes);
+zpq_status zpq_muon_plan_make(const zpq_muon_matrix* matrices, int32_t count, int32_t p_dtype,
+                              int32_t g_dtype, int32_t copy_dtype, void* memory,
+                              int64_t memory_bytes, zpq_muon_plan* plan, zpq_stream stream);
+
+typedef struct {
+    double lr, momentum;           /* lr >= 0, 0 <= momentum < 1 */
+    double grad_scale, max_norm;   /* as in zpq_adamw_hyper */
+    const double* coeffs;          /* host, [steps][3] */
+    int32_t steps, nesterov;
+} zpq_muon_hyper;
+
+/*
+ * One Muon step of all matrices of a plan:
+ *   g' = g * c, with c from grad_scale, max_norm and sumsq as in zpq_adamw_step
+ *   m' = momentum * m + g'
+ *   u  = nesterov ? g' + momentum * m' : m'
+ *   p' = p * (1 - lr * weight_decay) - lr * scale * iteration(u)
+ * elementwise operations in binary32, one rounding each, the iteration as above; p' is
+ * rounded to nearest even into p_dtype and copy_dtype.  A sumsq that is not finite
+ * leaves every output as it was.
+ */
+zpq_status zpq_muon_step(const zpq_muon_plan* plan, const zpq_muon_hyper* hyper,
+                         const double* sumsq, zpq_stream stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* zpq_status_str(zpq_status s);
 
