@@ -275,30 +275,31 @@ struct Result {
     int32_t slabs, per_split;
 };
 
-template <int DT>
-__device__ __forceinline__ void put4(const Result& o, int64_t row, int64_t col, f32x4 v) {
+// E consecutive results of a row, `have` of them inside.
+template <int DT, int E>
+__device__ __forceinline__ void put(const Result& o, int64_t row, int64_t col, float (&x)[E], int have) {
     const int64_t at = row * o.ld + col;
-    const int have = o.n - col < 4 ? (int)(o.n - col) : 4;
-    Raw<DT, 4> r;
-    float x[4] = {v.x, v.y, v.z, v.w};
+    Raw<DT, E> r;
     if (o.accumulate) {
-        if (have == 4) r.template load<false>(o.out, at);
+        if (have >= E) r.template load<false>(o.out, at);
         else r.load_some(o.out, at, have);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] += r.get(k);
+        for (int k = 0; k < E; ++k) x[k] += r.get(k);
     }
     r.set(x);
-    if (have == 4) r.template store<false>(o.out, at);
+    if (have >= E) r.template store<false>(o.out, at);
     else r.store_some(o.out, at, have);
 }
-__device__ __forceinline__ void put(const Result& o, int64_t row, int64_t col, f32x4 v) {
-    if (o.dtype == ZPQ_F32) put4<ZPQ_F32>(o, row, col, v);
-    else if (o.dtype == ZPQ_F16) put4<ZPQ_F16>(o, row, col, v);
-    else put4<ZPQ_BF16>(o, row, col, v);
+template <int E>
+__device__ __forceinline__ void put(const Result& o, int64_t row, int64_t col, float (&x)[E]) {
+    const int have = o.n - col < E ? (int)(o.n - col) : E;
+    if (o.dtype == ZPQ_F32) put<ZPQ_F32, E>(o, row, col, x, have);
+    else if (o.dtype == ZPQ_F16) put<ZPQ_F16, E>(o, row, col, x, have);
+    else put<ZPQ_BF16, E>(o, row, col, x, have);
 }
 
 template <class TILE>
-__global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_matmul(Operand a, Operand b, Result o) {
+__global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_matmul(Operand a, Operand b, Result o) {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::kLds];
     const uint32_t tiles = o.tiles_m * o.tiles_n, split = blockIdx.x / tiles;
     uint32_t i, j;
@@ -307,19 +308,21 @@ __global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_matmul(Operand a, Opera
     const int first = (int)split * o.per_split;
     TILE t;
     t.run(a, b, row_a, row_b, first, first + o.per_split < o.slabs ? first + o.per_split : o.slabs, shared);
+    const auto none = [](uint32_t, uint32_t, u32x4) {};
     if (o.parts != nullptr) {
         float* part = o.parts + (int64_t)split * o.m * o.n;
-        t.each([&](uint32_t x, uint32_t y, f32x4 v) {
+        t.template finish<false>(shared, [&](uint32_t x, uint32_t y, float (&v)[8]) {
             const int64_t row = row_a + x, col = row_b + y;
-            if (row >= o.m) return;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (col + k < o.n) part[row * o.n + col + k] = v[k];
-        });
+            if (row >= o.m || col >= o.n) return;
+            Raw<ZPQ_F32, 8> r;
+            r.set(v);
+            if (o.n - col >= 8) r.template store<false>(part, row * o.n + col);
+            else r.store_some(part, row * o.n + col, (int)(o.n - col));
+        }, none);
     } else {
-        t.each([&](uint32_t x, uint32_t y, f32x4 v) {
+        t.template finish<false>(shared, [&](uint32_t x, uint32_t y, float (&v)[8]) {
             if (row_a + x < o.m && row_b + y < o.n) put(o, row_a + x, row_b + y, v);
-        });
+        }, none);
     }
 }
 
@@ -328,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void k_join(Result o, int32_t splits) {
     const int64_t per_row = (o.n + 3) / 4, all = o.m * per_row;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kThreads) {
         const int64_t row = i / per_row, col = (i - row * per_row) * 4;
-        f32x4 sum = {0, 0, 0, 0};
+        float sum[4] = {0, 0, 0, 0};
         for (int s = 0; s < splits; ++s) {
             const float* p = o.parts + ((int64_t)s * o.m + row) * o.n + col;
 #pragma unroll
@@ -344,7 +347,8 @@ __global__ __launch_bounds__(kThreads) void k_empty(Result o) {
     const int64_t per_row = (o.n + 3) / 4, all = o.m * per_row;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kThreads) {
         const int64_t row = i / per_row;
-        put(o, row, (i - row * per_row) * 4, f32x4{0, 0, 0, 0});
+        float zero[4] = {0, 0, 0, 0};
+        put(o, row, (i - row * per_row) * 4, zero);
     }
 }
 

@@ -151,20 +151,74 @@ __device__ __forceinline__ void products(f32x4 (*acc)[NB], const i32x8 (&a)[NA],
     }
 }
 
+// What a wave does with its sums when the loop is over.  A lane holds 4 consecutive columns of 16 rows
+// each; through the wave's own part of LDS they become 8 consecutive columns of a row, so that
+// global memory sees whole rows:
+//   f(row, column, v)      the tile's row and first of 8 columns, their sums; may change them
+//   g(column, row, h)      with TURN, what f made of them, rounded to binary16, the other way round: 8 consecutive rows
+//                          of a column
+// Written straight from the sums, 8 bytes a lane and 16 rows an instruction, a 256 x 256 tile's end
+// took 25 us.
+template <int MI, int NI, bool TURN, class F, class G>
+__device__ __forceinline__ void hand_out(const f32x4 (&acc)[MI][NI], uint8_t* shared, uint32_t wave, uint32_t row0, uint32_t col0,
+                                         F&& f, G&& g) {
+    constexpr int COLS = NI * 16, CHUNKS = COLS / 4, LANES = COLS / 8, CALLS = 16 * LANES / 64;
+    constexpr int HIGH = MI < 4 ? MI : 4, ROWS = HIGH * 16;      // rows that are turned at a time
+    constexpr int STAGE = 16 * COLS * 4;
+    meet();                                   // no wave reads operands any more
+    uint32_t lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));            // addresses are made here, not kept in registers through the loop
+    uint8_t* stage = shared + wave * (STAGE + ROWS * COLS * 2);
+    uint8_t* turned = stage + STAGE;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const uint32_t r = lane & 15, q = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+            *reinterpret_cast<f32x4*>(stage + r * (COLS * 4) + (((j * 4 + q) ^ (r & (CHUNKS - 1))) << 4)) = acc[i][j];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < CALLS; ++k) {
+            const uint32_t row = k * (64 / LANES) + lane / LANES, c = lane % LANES;
+            const uint8_t* at = stage + row * (COLS * 4);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(at + (((c * 2) ^ (row & (CHUNKS - 1))) << 4));
+            const f32x4 y = *reinterpret_cast<const f32x4*>(at + (((c * 2 + 1) ^ (row & (CHUNKS - 1))) << 4));
+            float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            f(row0 + i * 16 + row, col0 + c * 8, v);
+            if constexpr (TURN) {
+                const uint32_t high = (i % HIGH) * 16 + row;
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    *reinterpret_cast<_Float16*>(turned + (c * 8 + n) * (ROWS * 2) + (((high >> 3) ^ (c & (ROWS / 8 - 1))) << 4) + (high & 7) * 2) =
+                        (_Float16)v[n];
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if constexpr (TURN) {
+            if (i % HIGH == HIGH - 1) {
+#pragma unroll
+                for (int k = 0; k < COLS * (ROWS / 8) / 64; ++k) {
+                    const uint32_t column = k * (64 / (ROWS / 8)) + lane / (ROWS / 8), c = lane % (ROWS / 8);
+                    g(col0 + column, row0 + (i / HIGH) * ROWS + c * 8,
+                      *reinterpret_cast<const u32x4*>(turned + column * (ROWS * 2) + ((c ^ ((column >> 3) & (ROWS / 8 - 1))) << 4)));
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+        }
+    }
+}
+
 // The loop of a 256 x 256 tile: 8 waves, each 128 rows of A by 64 of B, two waves on a
-// SIMD.  Two buffers of one slab of both operands (128 KB of LDS).  The waves of
-// a SIMD take turns: while one reads its pieces of a slab from LDS (and starts the copy of
-// a later slab), the other one multiplies, so the matrix core is fed without a pause
-// although the LDS needs about three quarters of the time.
-//
-// A turn is half a slab: M1 reads 4 pieces of B and 4 of A, C1 multiplies them, M2 reads the
-// other 4 of A, C2 multiplies.  Waves 4-7 are one turn behind.  Slab k + 2 goes into
-// the buffer of slab k, which both are done with 4 turns after the first began to read it:
-// waves 0-3 start their part of the copy in M1 of slab k + 1, waves 4-7 in C2 of slab k,
-// which is the same turn; it has to be there 4 turns (about 2000 cycles) later.
+// SIMD; two buffers of one slab of both operands (128 KB of LDS), one barrier a slab.  The
+// copy of the next slab starts right after the barrier, into the buffer that all waves have
+// read by then, and has a whole slab's time to arrive.  Pieces of A are read two ahead of
+// their products.
+// Tried and slower: the two waves of a SIMD in turns, one reading and one multiplying (4 barriers a
+// slab); half slabs in four buffers (64 bytes a row keep the address unit busier than the matrix cores);
+// four waves of 128 x 128.
 template <int KA, int KB, bool FULL = false>
 struct Tile256 {
-    static constexpr int BM = 256, BN = 256, kThreadsWg = 512, MI = 8, NI = 4;
+    static constexpr int BM = 256, BN = 256, kThreadsWg = 512, kWaves = 2, MI = 8, NI = 4;   // kWaves: on a SIMD
     static constexpr int kSide = 256 * kSlab, kBuffer = 2 * kSide;
     static constexpr bool kScaled = KA != kF16;
     static constexpr int kLds = 2 * kBuffer + (kScaled ? 2048 : 0);
@@ -202,9 +256,8 @@ struct Tile256 {
         constexpr int buffer = SEL & 1;
         const uint8_t* side_a = lds + buffer * kBuffer + wm() * 128 * kSlab;
         const uint8_t* side_b = lds + buffer * kBuffer + kSide + wn() * 64 * kSlab;
-        i32x8 fb[NI], fa[MI / 2];
-        // M1
-        if (wm() == 0 && slab + 1 < end) start_copy(slab + 1, buffer ^ 1);
+        wait_copies();
+        meet();                               // the slab is there, and the other buffer read
         if constexpr (kScaled && SEL == 0) {
             const int* s = reinterpret_cast<const int*>(lds + 2 * kBuffer) + (lane & 15);
 #pragma unroll
@@ -212,41 +265,39 @@ struct Tile256 {
 #pragma unroll
             for (int j = 0; j < NI; ++j) sb[j] = s[256 + wn() * 64 + j * 16];
         }
+        i32x8 fb[NI], one[2], two[2];
+        one[0] = piece(side_a, 0);
 #pragma unroll
         for (int j = 0; j < NI; ++j) fb[j] = piece(side_b, j * 16);
-#pragma unroll
-        for (int i = 0; i < MI / 2; ++i) fa[i] = piece(side_a, i * 16);
-        meet();
+        one[1] = piece(side_a, 16);
+        if (slab + 1 < end) start_copy(slab + 1, buffer ^ 1);
         __builtin_amdgcn_sched_barrier(0);
-        // C1
-        multiply<SEL, 0>(fb, fa);
+        two[0] = piece(side_a, 32);
+        two[1] = piece(side_a, 48);
+        products<KA, KB, SEL, FULL>(acc, one, fb, sa, sb);
+        pin<0>();
         __builtin_amdgcn_sched_barrier(0);
-        meet();
+        one[0] = piece(side_a, 64);
+        one[1] = piece(side_a, 80);
+        products<KA, KB, SEL, FULL>(acc + 2, two, fb, sa + 2, sb);
+        pin<2>();
         __builtin_amdgcn_sched_barrier(0);
-        // M2
-#pragma unroll
-        for (int i = 0; i < MI / 2; ++i) fa[i] = piece(side_a, (MI / 2 + i) * 16);
-        if (wm() == 1) wait_copies();
-        meet();
+        two[0] = piece(side_a, 96);
+        two[1] = piece(side_a, 112);
+        products<KA, KB, SEL, FULL>(acc + 4, one, fb, sa + 4, sb);
+        pin<4>();
         __builtin_amdgcn_sched_barrier(0);
-        // C2
-        if (wm() == 1 && slab + 2 < end) start_copy(slab + 2, buffer);
-        multiply<SEL, MI / 2>(fb, fa);
-        __builtin_amdgcn_sched_barrier(0);
-        if (wm() == 0) wait_copies();
-        meet();
+        products<KA, KB, SEL, FULL>(acc + 6, two, fb, sa + 6, sb);
+        pin<6>();
         __builtin_amdgcn_sched_barrier(0);
     }
-    template <int SEL, int FIRST>
-    __device__ __forceinline__ void multiply(const i32x8 (&fb)[NI], const i32x8 (&fa)[MI / 2]) {
-        __builtin_amdgcn_s_setprio(1);
-        products<KA, KB, SEL, FULL>(acc + FIRST, fa, fb, sa + FIRST, sb);
-        // in this turn, not later: without this the compiler moves the products behind the turn's end
+    // Here, not later: without this the compiler moves products behind branches and barriers.
+    template <int FIRST>
+    __device__ __forceinline__ void pin() {
 #pragma unroll
-        for (int i = 0; i < MI / 2; ++i)
+        for (int i = FIRST; i < FIRST + 2; ++i)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[FIRST + i][j]));
-        __builtin_amdgcn_s_setprio(0);
+            for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
     }
 
     // Sums slabs [first, end), first < end, first a multiple of 4, of the tile that starts
@@ -278,26 +329,16 @@ struct Tile256 {
 #pragma unroll
             for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
         start_copy(first, 0);
-        if (wm() == 1 && first + 1 < end) start_copy(first + 1, 1);
-        wait_copies();
-        meet();
-        if (wm() == 1) meet();
         for (int slab = first; slab < end; slab += 4) {
             step<0>(slab, end);
             if (slab + 1 < end) step<1>(slab + 1, end);
             if (slab + 2 < end) step<2>(slab + 2, end);
             if (slab + 3 < end) step<3>(slab + 3, end);
         }
-        if (wm() == 0) meet();
     }
-    // f(row of A in the tile, first of 4 rows of B in the tile, sums)
-    template <class F>
-    __device__ __forceinline__ void each(F&& f) const {
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                f(wm() * 128 + i * 16 + (lane & 15), wn() * 64 + j * 16 + (lane >> 4) * 4, acc[i][j]);
+    template <bool TURN, class F, class G>
+    __device__ __forceinline__ void finish(uint8_t* shared, F&& f, G&& g) const {
+        hand_out<MI, NI, TURN>(acc, shared, wave, wm() * 128, wn() * 64, f, g);
     }
 };
 
@@ -305,7 +346,7 @@ struct Tile256 {
 // buffers.  Several workgroups of a CU hide each other's waits.
 template <int KA, int KB, int MI_, int NI_, bool FULL = false>
 struct TileSmall {
-    static constexpr int MI = MI_, NI = NI_, BM = 32 * MI, BN = 32 * NI, kThreadsWg = 256;
+    static constexpr int MI = MI_, NI = NI_, BM = 32 * MI, BN = 32 * NI, kThreadsWg = 256, kWaves = 2;
     static constexpr int kSideA = BM * kSlab, kSideB = BN * kSlab, kBuffer = kSideA + kSideB;
     static constexpr bool kScaled = KA != kF16;
     static constexpr int kScaleBytes = kScaled ? (BM + BN) * 4 : 0;
@@ -407,28 +448,24 @@ struct TileSmall {
             if (slab + 3 < end) step<3>(slab + 3, end);
         }
     }
-    template <class F>
-    __device__ __forceinline__ void each(F&& f) const {
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                f((wm() * MI + i) * 16 + (lane & 15), (wn() * NI + j) * 16 + (lane >> 4) * 4, acc[i][j]);
+    template <bool TURN, class F, class G>
+    __device__ __forceinline__ void finish(uint8_t* shared, F&& f, G&& g) const {
+        hand_out<MI, NI, TURN>(acc, shared, wave, wm() * MI * 16, wn() * NI * 16, f, g);
     }
 };
 
 // Workgroup `id` of `count` to tile (i, j) of rows x columns tiles.  Workgroups go to the 8
 // XCDs in turn, and each XCD has an L2 of its own: the ids of one XCD become consecutive
-// tiles of bands of 8 tile rows, so that the 32 tiles it works on at a time share 8 row and
-// 4 column strips.
+// tiles of bands of 4 tile rows, so that the 32 tiles it works on at a time share 4 row and
+// 8 column strips (bands of 4 measured 5% faster than of 8 or 16, and 15% than no order).
 __device__ __forceinline__ void tile_of(uint32_t id, uint32_t count, uint32_t rows, uint32_t columns, uint32_t& i,
                                         uint32_t& j) {
     const uint32_t q = count / 8, r = count % 8, x = id % 8;
     const uint32_t t = x * q + (x < r ? x : r) + id / 8;
-    const uint32_t band = t / (8 * columns), in = t - band * 8 * columns;
-    const uint32_t high = rows - band * 8 < 8 ? rows - band * 8 : 8;
+    const uint32_t band = t / (4 * columns), in = t - band * 4 * columns;
+    const uint32_t high = rows - band * 4 < 4 ? rows - band * 4 : 4;
     j = in / high;
-    i = band * 8 + (in - j * high);
+    i = band * 4 + (in - j * high);
 }
 
 }  // namespace zpq_matrix

@@ -341,13 +341,6 @@ struct Apply {
 __device__ __forceinline__ Operand operand(const _Float16* p, int64_t rows, uint32_t pitch) {
     return Operand{reinterpret_cast<const uint8_t*>(p), nullptr, rows, pitch * 2, 0, 0};
 }
-__device__ __forceinline__ void store_half4(_Float16* to, f32x4 v) {
-    Raw<ZPQ_F16, 4> r;
-    const float x[4] = {v.x, v.y, v.z, v.w};
-    r.set(x);
-    r.template store<false>(to, 0);
-}
-
 // Tile number k of the lower triangle: row i, column j <= i.
 __device__ __forceinline__ void triangle(uint32_t k, uint32_t& i, uint32_t& j) {
     i = (uint32_t)((sqrtf(8.0f * (float)k + 1.0f) - 1.0f) * 0.5f);
@@ -358,7 +351,7 @@ __device__ __forceinline__ void triangle(uint32_t k, uint32_t& i, uint32_t& j) {
 
 // A = X X^T (SQUARE false) or B = b A + c A A^T (true): tiles on and under the diagonal.
 template <class TILE, bool SQUARE>
-__global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_symmetric(Work w, Apply s) {
+__global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_symmetric(Work w, Apply s) {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::kLds];
     uint32_t id = blockIdx.x;
     const Entry& e = entry_of(w, id);
@@ -373,56 +366,53 @@ __global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_symmetric(Work w, Apply
     t.run(x, x, row0, col0, 0, (int)(x.pitch / kSlab), shared);
     const int pitch = (int)e.pitch_a;
     _Float16* to = SQUARE ? e.b16 : e.a16;
-    t.each([&](uint32_t dr, uint32_t dc, f32x4 v) {
+    t.template finish<true>(shared, [&](uint32_t dr, uint32_t dc, float (&v)[8]) {
         const int r = row0 + (int)dr, c = col0 + (int)dc;
-        if (r >= pitch || c >= pitch) return;
-        v *= 1.0f / kScale;
-        if constexpr (SQUARE) {
-            if (r < small) {
-                Raw<ZPQ_F16, 4> a;
-                a.template load<false>(e.a16, (int64_t)r * pitch + c);
-                v = f32x4{s.b * a.get(0), s.b * a.get(1), s.b * a.get(2), s.b * a.get(3)} + v * s.c;
-            }
-        }
+        const bool in = r < small && c < pitch;
+        Raw<ZPQ_F16, 8> a;
+        if (SQUARE && in) a.template load<false>(e.a16, (int64_t)r * pitch + c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = r < small && c + k < small ? v[k] : 0.0f;
-        if (r < small) store_half4(to + (int64_t)r * pitch + c, v);
-        if (i != j) {                          // tiles on the right edge bring the zeros up to the pitch
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (c + k < small) to[(int64_t)(c + k) * pitch + r] = (_Float16)v[k];
+        for (int k = 0; k < 8; ++k) {
+            float x = v[k] * (1.0f / kScale);
+            if constexpr (SQUARE) x = fmaf(s.b, in ? a.get(k) : 0.0f, s.c * x);
+            v[k] = in && c + k < small ? x : 0.0f;
         }
+        a.set(v);
+        if (in) a.template store<false>(to, (int64_t)r * pitch + c);
+    }, [&](uint32_t dc, uint32_t dr, u32x4 h) {   // tiles on the right edge bring the zeros up to the pitch
+        const int r = row0 + (int)dr, c = col0 + (int)dc;
+        if (i != j && c < small && r < pitch) *reinterpret_cast<u32x4*>(to + (int64_t)c * pitch + r) = h;
     });
 }
 
 template <int DT>
-__device__ __forceinline__ void put_row(void* to, int64_t at, const float (&x)[4], int have) {
-    Raw<DT, 4> r;
+__device__ __forceinline__ void put_row(void* to, int64_t at, const float (&x)[8], int have) {
+    Raw<DT, 8> r;
     r.set(x);
-    if (have >= 4) r.template store<false>(to, at);
+    if (have >= 8) r.template store<false>(to, at);
     else r.store_some(to, at, have);
 }
-__device__ __forceinline__ void put_row(int32_t dtype, void* to, int64_t at, const float (&x)[4], int have) {
+__device__ __forceinline__ void put_row(int32_t dtype, void* to, int64_t at, const float (&x)[8], int have) {
     if (dtype == ZPQ_F32) put_row<ZPQ_F32>(to, at, x, have);
     else if (dtype == ZPQ_F16) put_row<ZPQ_F16>(to, at, x, have);
     else put_row<ZPQ_BF16>(to, at, x, have);
 }
-__device__ __forceinline__ void get_row(int32_t dtype, const void* from, int64_t at, float (&x)[4], int have) {
+__device__ __forceinline__ void get_row(int32_t dtype, const void* from, int64_t at, float (&x)[8], int have) {
     const auto get = [&](auto r) {
-        if (have >= 4) r.template load<false>(from, at);
+        if (have >= 8) r.template load<false>(from, at);
         else r.load_some(from, at, have);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = r.get(k);
+        for (int k = 0; k < 8; ++k) x[k] = r.get(k);
     };
-    if (dtype == ZPQ_F32) get(Raw<ZPQ_F32, 4>{});
-    else if (dtype == ZPQ_F16) get(Raw<ZPQ_F16, 4>{});
-    else get(Raw<ZPQ_BF16, 4>{});
+    if (dtype == ZPQ_F32) get(Raw<ZPQ_F32, 8>{});
+    else if (dtype == ZPQ_F16) get(Raw<ZPQ_F16, 8>{});
+    else get(Raw<ZPQ_BF16, 8>{});
 }
 
 // X' = a X + B X in X's own layout; the last step's goes to the output, or into the weights:
 // p' = p (1 - lr decay) - lr scale X'.
 template <class TILE, bool MUON>
-__global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_update(Work w, Apply s, const double* __restrict__ sumsq) {
+__global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_update(Work w, Apply s, const double* __restrict__ sumsq) {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::kLds];
     if (MUON && stopped(sumsq)) return;
     uint32_t id = blockIdx.x;
@@ -445,46 +435,58 @@ __global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_update(Work w, Apply s,
     t.run(wide ? b : x, wide ? x : b, row0, col0, 0, (int)(b.pitch / kSlab), shared);
     const double inv = s.first ? *e.inv : 1.0;
     const float keep = (float)(1.0 - (double)s.lr * e.decay), rate = s.lr * e.rate;
-    t.each([&](uint32_t dr, uint32_t dc, f32x4 v) {
-        const int r = row0 + (int)dr, c = col0 + (int)dc, have = e.cols - c;
-        const bool in = r < e.rows && have > 0;
-        float x[4] = {0, 0, 0, 0};
-        if (in) {
-            Raw<ZPQ_F32, 4> old;
-            const int64_t at = (int64_t)r * e.cols + c;
-            if (have >= 4) old.template load<false>(e.x32, at);
-            else old.load_some(e.x32, at, have);
+    const auto sum = [&](int r, int c, float (&v)[8]) {         // X'
+        const int have = e.cols - c;
+        Raw<ZPQ_F32, 8> old;
+        const int64_t at = (int64_t)r * e.cols + c;
+        if (have >= 8) old.template load<false>(e.x32, at);
+        else old.load_some(e.x32, at, have);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float o = s.first ? (float)(old.get(k) * inv) : old.get(k);
-                x[k] = k < have ? fmaf(v[k], 1.0f / (kScale * kScale), s.a * o) : 0.0f;
-            }
-            if (!s.last) {
-                old.set(x);
-                if (have >= 4) old.template store<false>(e.x32, at);
-                else old.store_some(e.x32, at, have);
-            }
+        for (int k = 0; k < 8; ++k) {
+            const float o = s.first ? (float)(old.get(k) * inv) : old.get(k);
+            v[k] = k < have ? fmaf(v[k], 1.0f / (kScale * kScale), s.a * o) : 0.0f;
         }
-        if (s.last) {
-            if (!in) return;
+    };
+    if (s.last) {
+        t.template finish<false>(shared, [&](uint32_t dr, uint32_t dc, float (&v)[8]) {
+            const int r = row0 + (int)dr, c = col0 + (int)dc, have = e.cols - c;
+            if (r >= e.rows || have <= 0) return;
+            sum(r, c, v);
             const int64_t at = (int64_t)r * e.ld_p + c;
             if constexpr (MUON) {
-                float p[4];
+                float p[8];
                 get_row(s.out_dtype, e.p, at, p, have);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = p[k] * keep - rate * x[k];
-                if (s.copy_dtype >= 0) put_row(s.copy_dtype, e.copy, at, x, have);
+                for (int k = 0; k < 8; ++k) v[k] = p[k] * keep - rate * v[k];
+                if (s.copy_dtype >= 0) put_row(s.copy_dtype, e.copy, at, v, have);
             }
-            put_row(s.out_dtype, e.p, at, x, have);
-            return;
-        }
-        const f32x4 y = f32x4{x[0], x[1], x[2], x[3]} * kScale;
-        if (r < e.rows && c < (int)e.pitch_x) store_half4(x16 + (int64_t)r * e.pitch_x + c, y);
-        if (r < (int)e.pitch_t) {
+            put_row(s.out_dtype, e.p, at, v, have);
+        }, [](uint32_t, uint32_t, u32x4) {});
+        return;
+    }
+    t.template finish<true>(shared, [&](uint32_t dr, uint32_t dc, float (&v)[8]) {
+        const int r = row0 + (int)dr, c = col0 + (int)dc, have = e.cols - c;
+        if (r >= e.rows || have <= 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < have) t16[(int64_t)(c + k) * e.pitch_t + r] = (_Float16)y[k];
+            for (int k = 0; k < 8; ++k) v[k] = 0;
+        } else {
+            sum(r, c, v);
+            Raw<ZPQ_F32, 8> x;
+            x.set(v);
+            const int64_t at = (int64_t)r * e.cols + c;
+            if (have >= 8) x.template store<false>(e.x32, at);
+            else x.store_some(e.x32, at, have);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= kScale;
         }
+        if (r < e.rows && c < (int)e.pitch_x) {
+            Raw<ZPQ_F16, 8> h;
+            h.set(v);
+            h.template store<false>(x16, (int64_t)r * e.pitch_x + c);
+        }
+    }, [&](uint32_t dc, uint32_t dr, u32x4 h) {
+        const int r = row0 + (int)dr, c = col0 + (int)dc;
+        if (c < e.cols && r < (int)e.pitch_t) *reinterpret_cast<u32x4*>(t16 + (int64_t)c * e.pitch_t + r) = h;
     });
 }
 
@@ -511,9 +513,9 @@ __global__ __launch_bounds__(kThreads) void k_update_few(Work w, Apply s, const 
 #pragma unroll
         for (int k = 0; k < kFew; ++k) y = fmaf(poly[i][k], x[k], y);
         const int64_t at = wide ? i * e.ld_p + j : j * e.ld_p + i;
-        float v[4] = {y, 0, 0, 0};
+        float v[8] = {y};
         if constexpr (MUON) {
-            float p[4];
+            float p[8];
             get_row(s.out_dtype, e.p, at, p, 1);
             v[0] = p[0] * keep - rate * y;
             if (s.copy_dtype >= 0) put_row(s.copy_dtype, e.copy, at, v, 1);
