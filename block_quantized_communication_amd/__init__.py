@@ -849,20 +849,26 @@ def _f8_shapes(rows, cols, tile):
     return (rows, kb * F8_BLOCK), (-(-rows // F8_BLOCK) if tile else rows, -(-kb // 4) * 4)
 
 
+@functools.lru_cache(maxsize=4096)
+def _f8_shape(shape, dtype, scales, scales_dtype, name):
+    """(kind, rows, blocks of a row, tile) of codes and scales of these shapes and types."""
+    kind = _kind(dtype, f"{name} codes")
+    if len(shape) != 2 or shape[1] % F8_BLOCK or len(scales) != 2 or scales_dtype != _torch().uint8:
+        raise ValueError(f"{name}: need codes [rows, 128 * blocks] and uint8 scales [rows, blocks4], got "
+                         f"{tuple(shape)} and {tuple(scales)} of {scales_dtype}")
+    rows, width = shape
+    of_rows, of_tiles = _f8_shapes(rows, width, False)[1], _f8_shapes(rows, width, True)[1]
+    if tuple(scales) not in (of_rows, of_tiles):
+        raise ValueError(f"{name} scales: need {of_rows} or, of tiles, {of_tiles}, got {tuple(scales)}")
+    return kind, rows, width // F8_BLOCK, tuple(scales) != of_rows
+
+
 def _f8_pair(pair, name, device=None):
     """Checks codes and scales; (device, kind, rows, blocks of a row, tile)."""
     codes, scales = pair
     dev = _gpu(codes, f"{name} codes", device)
-    kind = _kind(codes.dtype, f"{name} codes")
     _gpu(scales, f"{name} scales", dev)
-    if codes.dim() != 2 or codes.shape[1] % F8_BLOCK or scales.dim() != 2 or scales.dtype != _torch().uint8:
-        raise ValueError(f"{name}: need codes [rows, 128 * blocks] and uint8 scales [rows, blocks4], got "
-                         f"{tuple(codes.shape)} and {tuple(scales.shape)} of {scales.dtype}")
-    rows, width = codes.shape
-    of_rows, of_tiles = _f8_shapes(rows, width, False)[1], _f8_shapes(rows, width, True)[1]
-    if tuple(scales.shape) not in (of_rows, of_tiles):
-        raise ValueError(f"{name} scales: need {of_rows} or, of tiles, {of_tiles}, got {tuple(scales.shape)}")
-    return dev, kind, rows, width // F8_BLOCK, tuple(scales.shape) != of_rows
+    return (dev,) + _f8_shape(codes.shape, codes.dtype, scales.shape, scales.dtype, name)
 
 
 def _f8_cols(cols, blocks, name):

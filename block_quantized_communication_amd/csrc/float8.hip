@@ -1,6 +1,8 @@
 // float8.hip -- 8-bit floating-point blocks of 128 with a power-of-two scale (quantizing along
 // rows, along columns and in tiles; back to floats; transposing tiles) and the products of
 // such operands.  Definitions: zpq.h.
+#include <type_traits>
+
 #include "matrix.h"
 
 namespace {
@@ -309,9 +311,10 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_matmul(Opera
     TILE t;
     t.run(a, b, row_a, row_b, first, first + o.per_split < o.slabs ? first + o.per_split : o.slabs, shared);
     const auto none = [](uint32_t, uint32_t, u32x4) {};
+    const auto nothing = [](uint32_t, uint32_t) { return 0; };
     if (o.parts != nullptr) {
         float* part = o.parts + (int64_t)split * o.m * o.n;
-        t.template finish<false>(shared, [&](uint32_t x, uint32_t y, float (&v)[8]) {
+        t.template finish<false>(shared, nothing, [&](uint32_t x, uint32_t y, float (&v)[8], int) {
             const int64_t row = row_a + x, col = row_b + y;
             if (row >= o.m || col >= o.n) return;
             Raw<ZPQ_F32, 8> r;
@@ -320,9 +323,99 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_matmul(Opera
             else r.store_some(part, row * o.n + col, (int)(o.n - col));
         }, none);
     } else {
-        t.template finish<false>(shared, [&](uint32_t x, uint32_t y, float (&v)[8]) {
-            if (row_a + x < o.m && row_b + y < o.n) put(o, row_a + x, row_b + y, v);
+        // binary32 results that are added to, whole pieces of a row: loaded ahead
+        const bool ahead = o.accumulate && o.dtype == ZPQ_F32;
+        t.template finish<false>(shared, [&](uint32_t x, uint32_t y) {
+            Raw<ZPQ_F32, 8> old = {};
+            if (ahead && row_a + x < o.m && row_b + y + 8 <= o.n)
+                old.template load<false>(o.out, (row_a + x) * o.ld + row_b + y);
+            return old;
+        }, [&](uint32_t x, uint32_t y, float (&v)[8], const Raw<ZPQ_F32, 8>& old) {
+            const int64_t row = row_a + x, col = row_b + y;
+            if (row >= o.m || col >= o.n) return;
+            if (ahead && col + 8 <= o.n) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += old.get(k);
+                Raw<ZPQ_F32, 8> sum;
+                sum.set(v);
+                sum.template store<false>(o.out, row * o.ld + col);
+            } else {
+                put(o, row, col, v);
+            }
         }, none);
+    }
+}
+
+// Few rows of A (up to 16 * MI): the weight streams past once.  A workgroup has 16 rows of B; its 8 waves take
+// four slabs (one exponent word) each in turn, straight from memory into registers, and add
+// up in LDS.  Nothing is shared, so nothing goes through LDS on the way in.
+constexpr int kFewWaves = 8;
+template <int KA, int KB, bool FULL, int MI>
+__global__ __launch_bounds__(kFewWaves * 64) void k_matmul_few(Operand a, Operand b, Result o) {
+    __shared__ f32x4 sums[kFewWaves][MI][64];
+    const uint32_t lane = threadIdx.x & 63, wave = scalar(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const uint32_t split = blockIdx.x / o.tiles_n;
+    const int64_t col0 = (int64_t)(blockIdx.x - split * o.tiles_n) * 16;
+    const int first = (int)split * o.per_split, end = first + o.per_split < o.slabs ? first + o.per_split : o.slabs;
+    const int64_t row_b = col0 + r < o.n ? col0 + r : o.n - 1;             // rows past the end: the last one again
+    const uint8_t *pb = b.data + row_b * b.pitch + g * 16, *sb = b.scale + (row_b >> b.scale_shift) * b.scale_pitch;
+    const uint8_t *pa[MI], *sa[MI];
+    f32x4 acc[1][1], all[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int64_t row = i * 16 + r < o.m ? i * 16 + r : o.m - 1;
+        pa[i] = a.data + row * a.pitch + g * 16;
+        sa[i] = a.scale + (row >> a.scale_shift) * a.scale_pitch;
+        all[i] = f32x4{0, 0, 0, 0};
+    }
+    const auto piece = [](const uint8_t* p) {
+        const i32x4 x = *reinterpret_cast<const i32x4*>(p), y = *reinterpret_cast<const i32x4*>(p + 64);
+        return i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    };
+    const auto one = [&](auto sel, const i32x8& fa, const i32x8& fb, int wa, int wb, f32x4& to) {
+        const i32x8 x[1] = {fa}, y[1] = {fb};
+        const int ya[1] = {wa}, yb[1] = {wb};
+        acc[0][0] = to;
+        products<KA, KB, decltype(sel)::value, FULL>(acc, x, y, ya, yb);
+        to = acc[0][0];
+    };
+    for (int slab = first + (int)wave * 4; slab < end; slab += kFewWaves * 4) {
+        const int wb = *reinterpret_cast<const int*>(sb + slab);
+        int wa[MI];
+        i32x8 fb[4], fa[MI][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t at = (int64_t)(slab + k < end ? slab + k : slab) * kSlab;
+            fb[k] = piece(pb + at);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) fa[i][k] = piece(pa[i] + at);
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            wa[i] = *reinterpret_cast<const int*>(sa[i] + slab);
+            one(std::integral_constant<int, 0>{}, fa[i][0], fb[0], wa[i], wb, all[i]);
+            if (slab + 1 < end) one(std::integral_constant<int, 1>{}, fa[i][1], fb[1], wa[i], wb, all[i]);
+            if (slab + 2 < end) one(std::integral_constant<int, 2>{}, fa[i][2], fb[2], wa[i], wb, all[i]);
+            if (slab + 3 < end) one(std::integral_constant<int, 3>{}, fa[i][3], fb[3], wa[i], wb, all[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sums[wave][i][lane] = all[i];
+    __syncthreads();
+    if (wave >= MI) return;
+    f32x4 sum = sums[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) sum += sums[w][wave][lane];
+    const int64_t row = wave * 16 + r, col = col0 + g * 4;
+    if (row >= o.m || col >= o.n) return;
+    float v[4] = {sum.x, sum.y, sum.z, sum.w};
+    if (o.parts == nullptr) {
+        put(o, row, col, v);
+    } else {
+        float* part = o.parts + ((int64_t)split * o.m + row) * o.n + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (col + k < o.n) part[k] = v[k];
     }
 }
 
@@ -405,6 +498,16 @@ struct Cut { int side; int64_t splits; int32_t per_split; };
 inline Cut cut_of(int64_t m, int64_t n, int64_t slabs) {
     const auto tiles = [&](int64_t s) { return ((m + s - 1) / s) * ((n + s - 1) / s); };
     Cut c{256, 1, (int32_t)slabs};
+    if (m <= 32) {                             // 8 waves of 16 columns; 512 workgroups, but a turn of 32 slabs each
+        c.side = 16;
+        int64_t want = 512 / ((n + 15) / 16 > 0 ? (n + 15) / 16 : 1);
+        if (want > slabs / 32) want = slabs / 32;
+        if (want > 1) {
+            c.per_split = (int32_t)(((slabs + want - 1) / want + 3) / 4 * 4);
+            c.splits = (slabs + c.per_split - 1) / c.per_split;
+        }
+        return c;
+    }
     if (tiles(256) < 192) c.side = 128;
     if (c.side == 128 && tiles(128) < 256) c.side = 64;
     int64_t want = 512 / (tiles(c.side) > 0 ? tiles(c.side) : 1);
@@ -419,7 +522,12 @@ inline Cut cut_of(int64_t m, int64_t n, int64_t slabs) {
 
 template <int KA, int KB, bool FULL>
 void launch_matmul(const Operand& a, const Operand& b, Result o, const Cut& c, hipStream_t st) {
-    if (c.side == 256) launch_tiles<Tile256<KA, KB, FULL>>(a, b, o, c.splits, st);
+    if (c.side == 16) {
+        o.tiles_n = (uint32_t)((o.n + 15) / 16);
+        const dim3 grid((uint32_t)(o.tiles_n * c.splits)), wg(kFewWaves * 64);
+        if (o.m <= 16) hipLaunchKernelGGL((k_matmul_few<KA, KB, FULL, 1>), grid, wg, 0, st, a, b, o);
+        else hipLaunchKernelGGL((k_matmul_few<KA, KB, FULL, 2>), grid, wg, 0, st, a, b, o);
+    } else if (c.side == 256) launch_tiles<Tile256<KA, KB, FULL>>(a, b, o, c.splits, st);
     else if (c.side == 128) launch_tiles<TileSmall<KA, KB, 4, 4, FULL>>(a, b, o, c.splits, st);
     else launch_tiles<TileSmall<KA, KB, 2, 2, FULL>>(a, b, o, c.splits, st);
     if (c.splits > 1) {
@@ -520,7 +628,7 @@ static zpq_status matmul_sizes(int64_t m, int64_t n, int64_t k) {
     if (m < 0 || n < 0 || k < 0 || m > 0x7FFFFFFF || n > 0x7FFFFFFF || k > kMaxRow) return ZPQ_ERR_SIZE;
     if (m > 0 && (n > kMaxElems / m || k > kMaxElems / m)) return ZPQ_ERR_SIZE;
     if (n > 0 && k > kMaxElems / n) return ZPQ_ERR_SIZE;
-    if (((m + 63) / 64) * ((n + 63) / 64) > 0x7FFFFF) return ZPQ_ERR_SIZE;
+    if (((m + 63) / 64) * ((n + 63) / 64) > 0x7FFFFF || n > (1 << 26)) return ZPQ_ERR_SIZE;
     return ZPQ_OK;
 }
 

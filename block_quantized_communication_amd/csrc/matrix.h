@@ -154,14 +154,15 @@ __device__ __forceinline__ void products(f32x4 (*acc)[NB], const i32x8 (&a)[NA],
 // What a wave does with its sums when the loop is over.  A lane holds 4 consecutive columns of 16 rows
 // each; through the wave's own part of LDS they become 8 consecutive columns of a row, so that
 // global memory sees whole rows:
-//   f(row, column, v)      the tile's row and first of 8 columns, their sums; may change them
+//   l(row, column)         loads what f will need there, a group of 16 rows ahead of it
+//   f(row, column, v, l)   the tile's row and first of 8 columns, their sums, what l loaded; may change the sums
 //   g(column, row, h)      with TURN, what f made of them, rounded to binary16, the other way round: 8 consecutive rows
 //                          of a column
 // Written straight from the sums, 8 bytes a lane and 16 rows an instruction, a 256 x 256 tile's end
 // took 25 us.
-template <int MI, int NI, bool TURN, class F, class G>
+template <int MI, int NI, bool TURN, class L, class F, class G>
 __device__ __forceinline__ void hand_out(const f32x4 (&acc)[MI][NI], uint8_t* shared, uint32_t wave, uint32_t row0, uint32_t col0,
-                                         F&& f, G&& g) {
+                                         L&& l, F&& f, G&& g) {
     constexpr int COLS = NI * 16, CHUNKS = COLS / 4, LANES = COLS / 8, CALLS = 16 * LANES / 64;
     constexpr int HIGH = MI < 4 ? MI : 4, ROWS = HIGH * 16;      // rows that are turned at a time
     constexpr int STAGE = 16 * COLS * 4;
@@ -170,8 +171,17 @@ __device__ __forceinline__ void hand_out(const f32x4 (&acc)[MI][NI], uint8_t* sh
     asm volatile("" : "+v"(lane));            // addresses are made here, not kept in registers through the loop
     uint8_t* stage = shared + wave * (STAGE + ROWS * COLS * 2);
     uint8_t* turned = stage + STAGE;
+    decltype(l(0u, 0u)) here[CALLS], ahead[CALLS];
+    const auto load = [&](int i, auto& to) {
+#pragma unroll
+        for (int k = 0; k < CALLS; ++k) to[k] = l(row0 + i * 16 + k * (64 / LANES) + lane / LANES, col0 + lane % LANES * 8);
+    };
+    load(0, ahead);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
+#pragma unroll
+        for (int k = 0; k < CALLS; ++k) here[k] = ahead[k];
+        if (i + 1 < MI) load(i + 1, ahead);
         const uint32_t r = lane & 15, q = lane >> 4;
 #pragma unroll
         for (int j = 0; j < NI; ++j)
@@ -184,7 +194,7 @@ __device__ __forceinline__ void hand_out(const f32x4 (&acc)[MI][NI], uint8_t* sh
             const f32x4 x = *reinterpret_cast<const f32x4*>(at + (((c * 2) ^ (row & (CHUNKS - 1))) << 4));
             const f32x4 y = *reinterpret_cast<const f32x4*>(at + (((c * 2 + 1) ^ (row & (CHUNKS - 1))) << 4));
             float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            f(row0 + i * 16 + row, col0 + c * 8, v);
+            f(row0 + i * 16 + row, col0 + c * 8, v, here[k]);
             if constexpr (TURN) {
                 const uint32_t high = (i % HIGH) * 16 + row;
 #pragma unroll
@@ -336,9 +346,9 @@ struct Tile256 {
             if (slab + 3 < end) step<3>(slab + 3, end);
         }
     }
-    template <bool TURN, class F, class G>
-    __device__ __forceinline__ void finish(uint8_t* shared, F&& f, G&& g) const {
-        hand_out<MI, NI, TURN>(acc, shared, wave, wm() * 128, wn() * 64, f, g);
+    template <bool TURN, class L, class F, class G>
+    __device__ __forceinline__ void finish(uint8_t* shared, L&& l, F&& f, G&& g) const {
+        hand_out<MI, NI, TURN>(acc, shared, wave, wm() * 128, wn() * 64, l, f, g);
     }
 };
 
@@ -448,9 +458,9 @@ struct TileSmall {
             if (slab + 3 < end) step<3>(slab + 3, end);
         }
     }
-    template <bool TURN, class F, class G>
-    __device__ __forceinline__ void finish(uint8_t* shared, F&& f, G&& g) const {
-        hand_out<MI, NI, TURN>(acc, shared, wave, wm() * MI * 16, wn() * NI * 16, f, g);
+    template <bool TURN, class L, class F, class G>
+    __device__ __forceinline__ void finish(uint8_t* shared, L&& l, F&& f, G&& g) const {
+        hand_out<MI, NI, TURN>(acc, shared, wave, wm() * MI * 16, wn() * NI * 16, l, f, g);
     }
 };
 

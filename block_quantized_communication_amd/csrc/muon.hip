@@ -27,10 +27,12 @@ using namespace zpq_matrix;
 
 constexpr float kScale = 1024.0f;             // of 16-bit operands
 constexpr int kCut = 128;                     // side of the elementwise kernels' tiles
+constexpr int kGatherRows = 32;               // and of the gathering ones' tiles, 128 wide
 constexpr int kMaxSteps = 32;
 constexpr int64_t kMaxSide = 1 << 22;         // a row of 16-bit operands is at most 2^23 bytes
 constexpr int kFew = 32;                      // sides that go by one small matrix
 constexpr int kLong = 256;                    // of the other side, what a workgroup takes then
+constexpr int kOneSide = 64, kOneLong = 256;  // matrices that one workgroup works on, in LDS
 constexpr int64_t kGroup = 1 << 26;           // elements that are worked on at a time
 
 struct Entry {
@@ -50,16 +52,21 @@ struct Entry {
     float decay, rate;                        // Muon: weight_decay, scale
     double* gram;                             // a side up to kFew: parts of A, [longs][kFew][kFew]
     float* poly;                              // and P, [kFew][kFew]
-    uint32_t cuts, longs;
-    uint32_t start_cut, start_sym, start_full, start_long;
+    uint32_t parts, longs;                    // parts: tiles of k_gather
+    uint32_t start_part, start_cut, start_sym, start_full, start_long;
 };
+__host__ __device__ __forceinline__ bool one_workgroup(int64_t rows, int64_t cols) {
+    const int64_t side = rows < cols ? rows : cols;
+    return side > kFew && side <= kOneSide && rows + cols - side <= kOneLong;
+}
+__device__ __forceinline__ bool one_workgroup(const Entry& e) { return one_workgroup(e.rows, e.cols); }
 __device__ __forceinline__ bool few(const Entry& e) { return (e.rows < e.cols ? e.rows : e.cols) <= kFew; }
-constexpr int kFill = 18;
+constexpr int kFill = 17;
 struct Fill { Entry entry[kFill]; };
 static_assert(sizeof(Fill) < 3800, "kernel arguments");
 
 __global__ __launch_bounds__(64) void k_fill(Fill f, int32_t first, int32_t count, Entry* entries, uint32_t* cut,
-                                             uint32_t* sym, uint32_t* full, uint32_t* along) {
+                                             uint32_t* sym, uint32_t* full, uint32_t* along, uint32_t* part) {
     const int i = threadIdx.x;
     if (i >= count) return;
     entries[first + i] = f.entry[i];
@@ -67,6 +74,7 @@ __global__ __launch_bounds__(64) void k_fill(Fill f, int32_t first, int32_t coun
     sym[first + i] = f.entry[i].start_sym;
     full[first + i] = f.entry[i].start_full;
     along[first + i] = f.entry[i].start_long;
+    part[first + i] = f.entry[i].start_part;
 }
 
 // What a launch works on: `count` consecutive entries and where their shares of workgroups start.
@@ -90,15 +98,16 @@ struct Hyper {
 // A norm that is not finite leaves everything as it was.
 __device__ __forceinline__ bool stopped(const double* sumsq) { return sumsq != nullptr && !(*sumsq < INFINITY); }
 
-// u = [momentum and] gradient as binary32, and the sum of its squares; a 128 x 128 tile a workgroup, a
-// lane 8 consecutive elements of 8 rows.
+// u = [momentum and] gradient as binary32, and the sum of its squares; a 32 x 128 tile a workgroup, a
+// lane 8 consecutive elements of 2 rows (of 8 rows: 35 us instead of 19 for three layers of hidden 250, too few
+// workgroups).
 template <int GT, bool MUON>
 __global__ __launch_bounds__(kThreads) void k_gather(Work w, Hyper h, const double* __restrict__ sumsq) {
     if (MUON && stopped(sumsq)) return;
     uint32_t id = blockIdx.x;
     const Entry& e = entry_of(w, id);
     const uint32_t across = (uint32_t)(e.cols + kCut - 1) / kCut, t = threadIdx.x;
-    const int row = (int)(id / across) * kCut + (t >> 4) * 8, col = (int)(id % across) * kCut + (t & 15) * 8;
+    const int row = (int)(id / across) * kGatherRows + (t >> 4), col = (int)(id % across) * kCut + (t & 15) * 8;
     const int have = e.cols - col;
     float c = 1.0f;
     if (MUON) {
@@ -107,9 +116,9 @@ __global__ __launch_bounds__(kThreads) void k_gather(Work w, Hyper h, const doub
         c = (float)s;
     }
     double sum = 0;
-#pragma unroll 2
-    for (int p = 0; p < 8; ++p) {
-        if (row + p >= e.rows || have <= 0) break;
+#pragma unroll
+    for (int p = 0; p < kGatherRows; p += 16) {
+        if (row + p >= e.rows || have <= 0) continue;
         const int64_t at = (int64_t)(row + p) * e.cols + col, at_g = (int64_t)(row + p) * e.ld_g + col;
         Raw<GT, 8> g;
         if (have >= 8) g.load(e.g, at_g);
@@ -150,9 +159,9 @@ __global__ __launch_bounds__(kThreads) void k_gather(Work w, Hyper h, const doub
 // 1 / norm of each matrix; 0 for a matrix of zeros, NaN for one that is not finite.
 __global__ __launch_bounds__(kThreads) void k_norms(const Entry* __restrict__ entries) {
     const Entry& e = entries[blockIdx.x];
-    if (e.cuts == 0 || few(e)) return;         // (cuts: an empty matrix)
+    if (e.parts == 0 || few(e) || one_workgroup(e)) return;     // (cuts: an empty matrix)
     double sum = 0;
-    for (uint32_t i = threadIdx.x; i < e.cuts; i += kThreads) sum += e.part[i];
+    for (uint32_t i = threadIdx.x; i < e.parts; i += kThreads) sum += e.part[i];
     __shared__ double part[kThreads / 64];
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
@@ -169,7 +178,6 @@ __global__ __launch_bounds__(kThreads) void k_halves(Work w) {
     __shared__ u32x4 turned[kCut * 16];
     uint32_t id = blockIdx.x;
     const Entry& e = entry_of(w, id);
-    if (few(e)) return;
     const uint32_t across = (uint32_t)(e.cols + kCut - 1) / kCut, t = threadIdx.x, c = t & 15, r = t >> 4;
     const int row0 = (int)(id / across) * kCut, col0 = (int)(id % across) * kCut;
     const int row = row0 + r * 8, col = col0 + c * 8, have = e.cols - col;
@@ -366,15 +374,18 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_symmetric(Wo
     t.run(x, x, row0, col0, 0, (int)(x.pitch / kSlab), shared);
     const int pitch = (int)e.pitch_a;
     _Float16* to = SQUARE ? e.b16 : e.a16;
-    t.template finish<true>(shared, [&](uint32_t dr, uint32_t dc, float (&v)[8]) {
+    t.template finish<true>(shared, [&](uint32_t dr, uint32_t dc) {
+        const int r = row0 + (int)dr, c = col0 + (int)dc;
+        Raw<ZPQ_F16, 8> a = {};
+        if (SQUARE && r < small && c < pitch) a.template load<false>(e.a16, (int64_t)r * pitch + c);
+        return a;
+    }, [&](uint32_t dr, uint32_t dc, float (&v)[8], Raw<ZPQ_F16, 8> a) {
         const int r = row0 + (int)dr, c = col0 + (int)dc;
         const bool in = r < small && c < pitch;
-        Raw<ZPQ_F16, 8> a;
-        if (SQUARE && in) a.template load<false>(e.a16, (int64_t)r * pitch + c);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             float x = v[k] * (1.0f / kScale);
-            if constexpr (SQUARE) x = fmaf(s.b, in ? a.get(k) : 0.0f, s.c * x);
+            if constexpr (SQUARE) x = fmaf(s.b, a.get(k), s.c * x);
             v[k] = in && c + k < small ? x : 0.0f;
         }
         a.set(v);
@@ -435,12 +446,14 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_update(Work 
     t.run(wide ? b : x, wide ? x : b, row0, col0, 0, (int)(b.pitch / kSlab), shared);
     const double inv = s.first ? *e.inv : 1.0;
     const float keep = (float)(1.0 - (double)s.lr * e.decay), rate = s.lr * e.rate;
-    const auto sum = [&](int r, int c, float (&v)[8]) {         // X'
-        const int have = e.cols - c;
-        Raw<ZPQ_F32, 8> old;
-        const int64_t at = (int64_t)r * e.cols + c;
-        if (have >= 8) old.template load<false>(e.x32, at);
-        else old.load_some(e.x32, at, have);
+    const auto load = [&](uint32_t dr, uint32_t dc) {              // X
+        const int r = row0 + (int)dr, c = col0 + (int)dc, have = e.cols - c;
+        Raw<ZPQ_F32, 8> old = {};
+        if (r < e.rows && have >= 8) old.template load<false>(e.x32, (int64_t)r * e.cols + c);
+        else if (r < e.rows && have > 0) old.load_some(e.x32, (int64_t)r * e.cols + c, have);
+        return old;
+    };
+    const auto sum = [&](int have, float (&v)[8], const Raw<ZPQ_F32, 8>& old) {     // X'
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float o = s.first ? (float)(old.get(k) * inv) : old.get(k);
@@ -448,10 +461,10 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_update(Work 
         }
     };
     if (s.last) {
-        t.template finish<false>(shared, [&](uint32_t dr, uint32_t dc, float (&v)[8]) {
+        t.template finish<false>(shared, load, [&](uint32_t dr, uint32_t dc, float (&v)[8], const Raw<ZPQ_F32, 8>& old) {
             const int r = row0 + (int)dr, c = col0 + (int)dc, have = e.cols - c;
             if (r >= e.rows || have <= 0) return;
-            sum(r, c, v);
+            sum(have, v, old);
             const int64_t at = (int64_t)r * e.ld_p + c;
             if constexpr (MUON) {
                 float p[8];
@@ -464,13 +477,13 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_update(Work 
         }, [](uint32_t, uint32_t, u32x4) {});
         return;
     }
-    t.template finish<true>(shared, [&](uint32_t dr, uint32_t dc, float (&v)[8]) {
+    t.template finish<true>(shared, load, [&](uint32_t dr, uint32_t dc, float (&v)[8], const Raw<ZPQ_F32, 8>& old) {
         const int r = row0 + (int)dr, c = col0 + (int)dc, have = e.cols - c;
         if (r >= e.rows || have <= 0) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = 0;
         } else {
-            sum(r, c, v);
+            sum(have, v, old);
             Raw<ZPQ_F32, 8> x;
             x.set(v);
             const int64_t at = (int64_t)r * e.cols + c;
@@ -488,6 +501,111 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_update(Work 
         const int r = row0 + (int)dr, c = col0 + (int)dc;
         if (c < e.cols && r < (int)e.pitch_t) *reinterpret_cast<u32x4*>(t16 + (int64_t)c * e.pitch_t + r) = h;
     });
+}
+
+// The whole iteration of a matrix of up to 64 x 256 on one workgroup, where launches would take far longer
+// than the products: the same operands and sums as above, in LDS, X itself in registers.  8 waves;
+// X' in tiles of 16 x 16, tile t of 4 down and 16 across is wave t / 8's.
+template <bool MUON>
+__global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, Coeffs k, Apply s, const double* __restrict__ sumsq) {
+    constexpr int PX = kOneLong + 8, PA = kOneSide + 8;        // pitches that spread rows over the banks
+    __shared__ __attribute__((aligned(16))) _Float16 x16[kOneSide * PX], t16[kOneLong * PA], a16[kOneSide * PA], b16[kOneSide * PA];
+    const Entry& e = entries[blockIdx.x];
+    if (e.parts == 0 || !one_workgroup(e)) return;
+    if (MUON && stopped(sumsq)) return;
+    const Few f(e);
+    const bool wide = e.rows <= e.cols;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    double size = 0;
+    for (uint32_t i = 0; i < e.parts; ++i) size += e.part[i];
+    const double inv = size == 0.0 ? 0.0 : size < INFINITY ? 1.0 / sqrt(size) : NAN;
+    const int down = (f.side + 15) / 16, across = (f.length + 15) / 16, deep = (f.length + 31) / 32;
+    float x[8][4];
+    const auto row_of = [&](int n) { return ((wave * 8 + n) & 3) * 16 + r; };
+    const auto col_of = [&](int n) { return ((wave * 8 + n) >> 2) * 16 + g * 4; };
+    const auto keep16 = [&]() {                                // X both ways round, zeros outside
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int i = row_of(n), j = col_of(n);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const _Float16 h = (_Float16)(x[n][q] * kScale);
+                x16[i * PX + j + q] = h;
+                t16[(j + q) * PA + i] = h;
+            }
+        }
+    };
+    const auto piece = [&](const _Float16* from, int pitch, int row, int step) {
+        return *reinterpret_cast<const f16x8*>(from + (row + r) * pitch + step * 32 + g * 8);
+    };
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const int i = row_of(n), j = col_of(n);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            x[n][q] = i < f.side && j + q < f.length ? (float)(e.x32[i * f.step_i + (j + q) * f.step_j] * inv) : 0.0f;
+    }
+    for (int step = 0; step < k.steps; ++step) {
+        const float a = k.abc[3 * step], b = k.abc[3 * step + 1], c = k.abc[3 * step + 2];
+        keep16();
+        __syncthreads();
+        // A and B: tile t of 4 x 4 is wave t / 2's; lane: rows 4 g .. + 3 of column r, symmetric
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int ti = (wave * 2 + n) >> 2, tj = (wave * 2 + n) & 3;
+            f32x4 acc = {0, 0, 0, 0};
+            if (ti < down && tj < down)
+                for (int d = 0; d < deep; ++d)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(x16, PX, ti * 16, d), piece(x16, PX, tj * 16, d), acc, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) a16[(tj * 16 + r) * PA + ti * 16 + g * 4 + q] = (_Float16)(acc[q] * (1.0f / kScale));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int ti = (wave * 2 + n) >> 2, tj = (wave * 2 + n) & 3;
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(a16, PA, ti * 16, d), piece(a16, PA, tj * 16, d), acc, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int at = (tj * 16 + r) * PA + ti * 16 + g * 4 + q;
+                b16[at] = (_Float16)fmaf(b, (float)a16[at], c * (acc[q] * (1.0f / kScale)));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int ti = (wave * 8 + n) & 3, tj = (wave * 8 + n) >> 2;
+            f32x4 acc = {0, 0, 0, 0};
+            if (ti < down && tj < across)
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(t16, PA, tj * 16, d), piece(b16, PA, ti * 16, d), acc, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[n][q] = fmaf(acc[q], 1.0f / (kScale * kScale), a * x[n][q]);
+        }
+        __syncthreads();                       // before x16 and t16 are written again
+    }
+    const float keep = (float)(1.0 - (double)s.lr * e.decay), rate = s.lr * e.rate;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const int i = row_of(n), j = col_of(n);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (i >= f.side || j + q >= f.length) continue;
+            const int64_t at = wide ? i * e.ld_p + j + q : (j + q) * e.ld_p + i;
+            float v[8] = {x[n][q]};
+            if constexpr (MUON) {
+                float p[8];
+                get_row(s.out_dtype, e.p, at, p, 1);
+                v[0] = p[0] * keep - rate * x[n][q];
+                if (s.copy_dtype >= 0) put_row(s.copy_dtype, e.copy, at, v, 1);
+            }
+            put_row(s.out_dtype, e.p, at, v, 1);
+        }
+    }
 }
 
 // The result of matrices with a side up to kFew: P X, a lane one place of the long side.
@@ -532,20 +650,22 @@ inline int64_t div_up(int64_t n, int64_t by) { return (n + by - 1) / by; }
 struct Shape { int64_t rows, cols; };
 inline int64_t small_of(Shape s) { return s.rows < s.cols ? s.rows : s.cols; }
 inline int64_t cuts_of(Shape s) { return div_up(s.rows, kCut) * div_up(s.cols, kCut); }
+inline int64_t parts_of(Shape s) { return div_up(s.rows, kGatherRows) * div_up(s.cols, kCut); }
 inline bool few(Shape s) { return small_of(s) <= kFew; }
+inline bool tiled(Shape s) { return !few(s) && !one_workgroup(s.rows, s.cols); }
 inline int64_t longs_of(Shape s) { return few(s) ? div_up(s.rows < s.cols ? s.cols : s.rows, kLong) : 0; }
 inline int64_t triangle_of(Shape s, int64_t side) {
-    if (few(s)) return 0;
+    if (!tiled(s)) return 0;
     const int64_t t = div_up(small_of(s), side);
     return t * (t + 1) / 2;
 }
-inline int64_t tiles_of(Shape s, int64_t side) { return few(s) ? 0 : div_up(s.rows, side) * div_up(s.cols, side); }
+inline int64_t tiles_of(Shape s, int64_t side) { return tiled(s) ? div_up(s.rows, side) * div_up(s.cols, side) : 0; }
 inline bool shape_ok(Shape s) { return s.rows >= 0 && s.cols >= 0 && s.rows <= kMaxSide && s.cols <= kMaxSide && s.rows * s.cols <= (1LL << 34); }
 
 // Bytes of a matrix's part of the workspace, and the addresses in it.
 inline int64_t place(Shape s, char* at, Entry* e) {
-    const int64_t px = up(s.cols, 64), pt = up(s.rows, 64), pa = up(small_of(s), 64), cuts = cuts_of(s), longs = longs_of(s);
-    const int64_t halves = few(s) ? 0 : 2;
+    const int64_t px = up(s.cols, 64), pt = up(s.rows, 64), pa = up(small_of(s), 64), parts = parts_of(s), longs = longs_of(s);
+    const int64_t halves = tiled(s) ? 2 : 0;
     int64_t used = 0;
     const auto take = [&](int64_t bytes) {
         char* p = at ? at + used : nullptr;
@@ -555,7 +675,7 @@ inline int64_t place(Shape s, char* at, Entry* e) {
     char *x32 = take(s.rows * s.cols * 4), *x16 = take(s.rows * px * halves), *t16 = take(s.cols * pt * halves);
     char* other = take((s.rows <= s.cols ? s.cols * pt : s.rows * px) * halves);
     char *a16 = take(small_of(s) * pa * halves), *b16 = take(small_of(s) * pa * halves);
-    char *part = take(cuts * 8), *inv = take(16), *gram = take(longs * kFew * kFew * 8), *poly = take(longs ? kFew * kFew * 4 : 0);
+    char *part = take(parts * 8), *inv = take(16), *gram = take(longs * kFew * kFew * 8), *poly = take(longs ? kFew * kFew * 4 : 0);
     if (e) {
         e->x32 = reinterpret_cast<float*>(x32);
         e->x16 = reinterpret_cast<_Float16*>(x16);
@@ -570,7 +690,7 @@ inline int64_t place(Shape s, char* at, Entry* e) {
         e->pitch_x = (uint32_t)px;
         e->pitch_t = (uint32_t)pt;
         e->pitch_a = (uint32_t)pa;
-        e->cuts = (uint32_t)cuts;
+        e->parts = (uint32_t)parts;
         e->longs = (uint32_t)longs;
         e->gram = reinterpret_cast<double*>(gram);
         e->poly = reinterpret_cast<float*>(poly);
@@ -580,7 +700,7 @@ inline int64_t place(Shape s, char* at, Entry* e) {
 
 // Matrices that are worked on at a time: consecutive ones up to kGroup elements, one at least.
 struct Group {
-    int64_t first, end, bytes, cuts, sym, full, longs;
+    int64_t first, end, bytes, parts, cuts, sym, full, longs, ones;
     int side_sym, side_full;
 };
 // The largest tile that leaves the chip's 256 CUs enough workgroups.
@@ -589,7 +709,7 @@ inline int side_of(COUNT count) { return count(256) >= 192 ? 256 : count(128) >=
 
 template <class SHAPES>
 Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
-    Group g{first, first, 0, 0, 0, 0, 0, 0, 0};
+    Group g{first, first, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     int64_t elems = 0;
     while (g.end < count) {
         const Shape s = shape(g.end);
@@ -597,8 +717,10 @@ Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
         elems += s.rows * s.cols;
         if (s.rows > 0 && s.cols > 0) {
             g.bytes += place(s, nullptr, nullptr);
-            g.cuts += cuts_of(s);
+            g.parts += parts_of(s);
+            g.cuts += tiled(s) ? cuts_of(s) : 0;
             g.longs += longs_of(s);
+            g.ones += one_workgroup(s.rows, s.cols);
         }
         ++g.end;
     }
@@ -617,7 +739,7 @@ Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
 // The table: entries, then where each one's workgroups start, for the three kinds of launches.
 struct Table {
     Entry* entries;
-    uint32_t *cut, *sym, *full, *along;
+    uint32_t *cut, *sym, *full, *along, *part;
 };
 inline Table table_of(void* at, int64_t count) {
     Table t;
@@ -626,9 +748,10 @@ inline Table table_of(void* at, int64_t count) {
     t.sym = t.cut + count;
     t.full = t.sym + count;
     t.along = t.full + count;
+    t.part = t.along + count;
     return t;
 }
-static_assert(sizeof(Entry) + 16 <= ZPQ_MUON_BYTES(1) - ZPQ_MUON_BYTES(0), "ZPQ_MUON_BYTES");
+static_assert(sizeof(Entry) + 20 <= ZPQ_MUON_BYTES(1) - ZPQ_MUON_BYTES(0), "ZPQ_MUON_BYTES");
 
 // Fills the table; `entry(i, Entry&)` sets what place() does not.
 template <class SHAPES, class ENTRY>
@@ -637,7 +760,7 @@ void fill_table(const SHAPES& shape, const ENTRY& entry, int64_t count, void* ta
     for (int64_t first = 0; first < count;) {
         const Group g = group_at(shape, first, count);
         int64_t used = 0;
-        uint32_t cut = 0, sym = 0, full = 0, along = 0;
+        uint32_t cut = 0, sym = 0, full = 0, along = 0, part = 0;
         for (int64_t i = g.first; i < g.end; i += kFill) {
             Fill f = {};
             const int32_t some = (int32_t)(g.end - i < kFill ? g.end - i : kFill);
@@ -648,16 +771,18 @@ void fill_table(const SHAPES& shape, const ENTRY& entry, int64_t count, void* ta
                 e.start_sym = sym;
                 e.start_full = full;
                 e.start_long = along;
+                e.start_part = part;
                 if (s.rows == 0 || s.cols == 0) continue;
                 used += place(s, static_cast<char*>(workspace) + used, &e);
                 entry(i + k, e);
-                cut += (uint32_t)cuts_of(s);
+                cut += (uint32_t)(tiled(s) ? cuts_of(s) : 0);
+                part += (uint32_t)parts_of(s);
                 sym += (uint32_t)triangle_of(s, g.side_sym);
                 full += (uint32_t)tiles_of(s, g.side_full);
                 along += (uint32_t)longs_of(s);
             }
             hipLaunchKernelGGL(k_fill, dim3(1), dim3(64), 0, st, f, (int32_t)i, some, t.entries, t.cut, t.sym, t.full,
-                               t.along);
+                               t.along, t.part);
         }
         first = g.end;
     }
@@ -674,24 +799,26 @@ void launch_symmetric(const Work& w, const Apply& s, const Group& g, hipStream_t
 template <bool MUON>
 void launch_group(const Table& t, const Group& g, int32_t g_dtype, const Hyper& h, Apply s, const float* coeffs, int32_t steps,
                   const double* sumsq, hipStream_t st) {
-    if (g.cuts == 0) return;
+    if (g.parts == 0) return;
     const Entry* entries = t.entries + g.first;
     const uint32_t count = (uint32_t)(g.end - g.first);
     const Work cut{entries, t.cut + g.first, count}, sym{entries, t.sym + g.first, count}, full{entries, t.full + g.first, count};
-    const dim3 cuts((uint32_t)g.cuts), wg(kThreads);
-    if (g_dtype == ZPQ_F32) hipLaunchKernelGGL((k_gather<ZPQ_F32, MUON>), cuts, wg, 0, st, cut, h, sumsq);
-    else if (g_dtype == ZPQ_F16) hipLaunchKernelGGL((k_gather<ZPQ_F16, MUON>), cuts, wg, 0, st, cut, h, sumsq);
-    else hipLaunchKernelGGL((k_gather<ZPQ_BF16, MUON>), cuts, wg, 0, st, cut, h, sumsq);
+    const Work part{entries, t.part + g.first, count};
+    const dim3 cuts((uint32_t)g.cuts), parts((uint32_t)g.parts), wg(kThreads);
+    if (g_dtype == ZPQ_F32) hipLaunchKernelGGL((k_gather<ZPQ_F32, MUON>), parts, wg, 0, st, part, h, sumsq);
+    else if (g_dtype == ZPQ_F16) hipLaunchKernelGGL((k_gather<ZPQ_F16, MUON>), parts, wg, 0, st, part, h, sumsq);
+    else hipLaunchKernelGGL((k_gather<ZPQ_BF16, MUON>), parts, wg, 0, st, part, h, sumsq);
+    Coeffs k;
+    for (int32_t i = 0; i < 3 * steps; ++i) k.abc[i] = coeffs[i];
+    k.steps = steps;
     if (g.longs > 0) {
         const Work along{entries, t.along + g.first, count};
         const dim3 longs((uint32_t)g.longs);
-        Coeffs k;
-        for (int32_t i = 0; i < 3 * steps; ++i) k.abc[i] = coeffs[i];
-        k.steps = steps;
         hipLaunchKernelGGL(k_gram, longs, wg, 0, st, along);
         hipLaunchKernelGGL(k_poly, dim3(count), wg, 0, st, entries, k);
         hipLaunchKernelGGL((k_update_few<MUON>), longs, wg, 0, st, along, s, sumsq);
     }
+    if (g.ones > 0) hipLaunchKernelGGL((k_one<MUON>), dim3(count), dim3(512), 0, st, entries, k, s, sumsq);
     if (g.full == 0) return;
     hipLaunchKernelGGL(k_norms, dim3(count), wg, 0, st, entries);
     hipLaunchKernelGGL(k_halves, cuts, wg, 0, st, cut);

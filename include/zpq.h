@@ -404,7 +404,7 @@ typedef struct {
  *   out [m] rows of n elements of out_dtype, ld apart; read with accumulate only
  *   workspace: zpq_matmul_f8_bytes bytes of device memory (0 for most sizes),
  *   16-byte aligned, contents irrelevant
- * m, n < 2^31, ceil(m / 64) * ceil(n / 64) < 2^23; k = 0 is a sum of nothing.
+ * m < 2^31, n <= 2^26, ceil(m / 64) * ceil(n / 64) < 2^23; k = 0 is a sum of nothing.
  */
 zpq_status zpq_matmul_f8_bytes(int64_t m, int64_t n, int64_t k, int64_t* bytes);
 zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64_t m, int64_t n,
@@ -462,7 +462,7 @@ typedef struct {
 
 /* Device memory of a plan's table alone; zpq_muon_plan_bytes: with the workspace, which
  * is bounded as zpq_orthogonalize's. */
-#define ZPQ_MUON_BYTES(count) ((int64_t)(count) * 216 + 64)
+#define ZPQ_MUON_BYTES(count) ((int64_t)(count) * 232 + 64)
 
 /*
  * Lay out `count` matrices for zpq_muon_step, at most 2^20.  Types as in zpq_adamw_plan_make.  The

@@ -164,6 +164,17 @@ def test_matmul_whole_numbers(m, n, k, ka, kb, ta, tb):
         assert torch.equal(zpq.matmul_f8(a, b, out_dtype=dtype), want.float().to(dtype))
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 40, 40000), (15, 17, 9000), (16, 1, 20000), (17, 100, 8300), (32, 33, 12800), (33, 32, 12800)])
+def test_matmul_few_rows_and_long_sums(m, n, k):
+    """Up to 32 rows, sums split over workgroups: whole numbers, below 2^24 (40000 * 16 * 16)."""
+    for tile in (False, True):
+        a, av = whole(m, k, "e4m3", False, 3)
+        b, bv = whole(n, k, "e4m3", tile, 4)
+        want = av @ bv.t()
+        for dtype in (torch.float32, torch.bfloat16):
+            assert torch.equal(zpq.matmul_f8(a, b, out_dtype=dtype), want.float().to(dtype))
+
+
 @pytest.mark.parametrize("out", list(DT))
 @pytest.mark.parametrize("m,n,k", [(1, 700, 3000), (33, 500, 4000), (300, 700, 1500), (2700, 4900, 600)])
 def test_matmul_error(m, n, k, out):

@@ -60,6 +60,15 @@ def test_orthogonalize(rows, cols, kind):
         close(zpq.orthogonalize(x, out_dtype=DT[out]), want, HALF[out])
 
 
+@pytest.mark.parametrize("rows,cols", [(33, 33), (33, 256), (256, 40), (48, 47), (64, 256), (256, 64), (64, 257), (32, 33), (50, 200)])
+def test_orthogonalize_one_workgroup(rows, cols):
+    """Sizes at and around what one workgroup takes, each in every orientation."""
+    for kind in ("plain", "strong", "rank"):
+        x = matrix(rows, cols, kind, 11)
+        for out in HALF:
+            close(zpq.orthogonalize(x, out_dtype=DT[out]), iterate(x), HALF[out])
+
+
 @pytest.mark.parametrize("rows,cols", [(2048, 9000), (3700, 3650), (5000, 5100)])
 def test_orthogonalize_large(rows, cols):
     x = matrix(rows, cols, "strong").bfloat16()
@@ -124,7 +133,7 @@ def test_orthogonalize_repeats_bit_for_bit():
 
 
 # ------------------------------------------------------------------------------------------- Muon
-LAYER = [(96, 32), (32, 32), (128, 32), (32, 128), (1, 50), (77, 3), (200, 333)]
+LAYER = [(96, 32), (32, 32), (128, 32), (32, 128), (1, 50), (77, 3), (200, 333), (64, 192), (200, 48)]
 
 
 def make(shapes, p="f32", g="bf16", copy=None, seed=0, **options):
