@@ -310,7 +310,7 @@ struct Tile256 {
             for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
     }
 
-    // Sums slabs [first, end), first < end, first a multiple of 4, of the tile that starts
+    // Sums slabs [first, end), none or some, first a multiple of 4 with scales, of the tile that starts
     // at row row_a of A and row_b of B (multiples of 256).
     __device__ __forceinline__ void run(const Operand& a, const Operand& b, int64_t row_a, int64_t row_b, int first,
                                         int end, uint8_t* shared) {
@@ -334,10 +334,8 @@ struct Tile256 {
             rs = descriptor(o.scale + row * o.scale_pitch, (rows - row) * o.scale_pitch);
             off_s = (((wave & 3) * 64 + lane) >> o.scale_shift) * o.scale_pitch;
         }
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        clear();
+        if (first >= end) return;
         start_copy(first, 0);
         for (int slab = first; slab < end; slab += 4) {
             step<0>(slab, end);
@@ -345,6 +343,12 @@ struct Tile256 {
             if (slab + 2 < end) step<2>(slab + 2, end);
             if (slab + 3 < end) step<3>(slab + 3, end);
         }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     }
     template <bool TURN, class L, class F, class G>
     __device__ __forceinline__ void finish(uint8_t* shared, L&& l, F&& f, G&& g) const {

@@ -45,6 +45,7 @@ struct Entry {
     _Float16 *x16, *t16;                      // [rows][pitch_x], [cols][pitch_t]
     _Float16* other;                          // of the one that X' is a product with, the next step's
     _Float16 *a16, *b16;                      // [small][pitch_a]
+    float* pieces;                            // of A's sums that are split: [tile][split][256][256]
     double* part;                             // partial sums of squares
     double* inv;                              // 1 / norm, which binary32 cannot hold for subnormal matrices
     int32_t rows, cols;
@@ -53,7 +54,7 @@ struct Entry {
     double* gram;                             // a side up to kFew: parts of A, [longs][kFew][kFew]
     float* poly;                              // and P, [kFew][kFew]
     uint32_t parts, longs;                    // parts: tiles of k_gather
-    uint32_t start_part, start_cut, start_sym, start_full, start_long;
+    uint32_t start_part, start_cut, start_sym, start_full, start_long, start_large;
 };
 __host__ __device__ __forceinline__ bool one_workgroup(int64_t rows, int64_t cols) {
     const int64_t side = rows < cols ? rows : cols;
@@ -61,12 +62,12 @@ __host__ __device__ __forceinline__ bool one_workgroup(int64_t rows, int64_t col
 }
 __device__ __forceinline__ bool one_workgroup(const Entry& e) { return one_workgroup(e.rows, e.cols); }
 __device__ __forceinline__ bool few(const Entry& e) { return (e.rows < e.cols ? e.rows : e.cols) <= kFew; }
-constexpr int kFill = 17;
+constexpr int kFill = 16;
 struct Fill { Entry entry[kFill]; };
 static_assert(sizeof(Fill) < 3800, "kernel arguments");
 
 __global__ __launch_bounds__(64) void k_fill(Fill f, int32_t first, int32_t count, Entry* entries, uint32_t* cut,
-                                             uint32_t* sym, uint32_t* full, uint32_t* along, uint32_t* part) {
+                                             uint32_t* sym, uint32_t* full, uint32_t* along, uint32_t* part, uint32_t* large) {
     const int i = threadIdx.x;
     if (i >= count) return;
     entries[first + i] = f.entry[i];
@@ -75,6 +76,7 @@ __global__ __launch_bounds__(64) void k_fill(Fill f, int32_t first, int32_t coun
     full[first + i] = f.entry[i].start_full;
     along[first + i] = f.entry[i].start_long;
     part[first + i] = f.entry[i].start_part;
+    large[first + i] = f.entry[i].start_large;
 }
 
 // What a launch works on: `count` consecutive entries and where their shares of workgroups start.
@@ -396,6 +398,78 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_symmetric(Wo
     });
 }
 
+// A = X X^T with each tile's sum over the long side in `splits` pieces: few large tiles leave part of the chip
+// idle (136 of 256 CUs for a side of 4096), small ones cannot feed the matrix cores. 4096 x 16,384: 469 us in tiles of
+// 128, 296 + 42 us to join 3 pieces.
+template <class TILE>
+__global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_symmetric_split(Work w, uint32_t tiles, int32_t splits) {
+    __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::kLds];
+    const uint32_t split = blockIdx.x / tiles;
+    uint32_t id = blockIdx.x - split * tiles;
+    const Entry& e = entry_of(w, id);
+    const bool wide = e.rows <= e.cols;
+    const Operand x = wide ? operand(e.x16, e.rows, e.pitch_x) : operand(e.t16, e.cols, e.pitch_t);
+    uint32_t i, j;
+    triangle(id, i, j);
+    const int slabs = (int)(x.pitch / kSlab), per = (slabs + splits - 1) / splits, first = (int)split * per;
+    TILE t;
+    t.run(x, x, (int64_t)i * TILE::BM, (int64_t)j * TILE::BN, first, first + per < slabs ? first + per : slabs, shared);
+    float* to = e.pieces + ((int64_t)id * splits + split) * (TILE::BM * TILE::BN);
+    t.template finish<false>(shared, [](uint32_t, uint32_t) { return 0; }, [&](uint32_t r, uint32_t c, float (&v)[8], int) {
+        Raw<ZPQ_F32, 8> x;
+        x.set(v);
+        x.template store<false>(to, r * TILE::BN + c);
+    }, [](uint32_t, uint32_t, u32x4) {});
+}
+
+// The pieces added up, in order, into A and its mirror image; a 64 x 64 part of a tile a workgroup.
+constexpr int kPart = 64;
+template <int SIDE>
+__global__ __launch_bounds__(kThreads) void k_symmetric_join(Work w, int32_t splits) {
+    __shared__ __attribute__((aligned(16))) _Float16 turned[kPart * kPart];
+    constexpr uint32_t along = SIDE / kPart, each = along * along;
+    const uint32_t quarter = blockIdx.x % each, t = threadIdx.x;
+    uint32_t id = blockIdx.x / each;
+    const Entry& e = entry_of(w, id);
+    const int small = e.rows <= e.cols ? e.rows : e.cols, pitch = (int)e.pitch_a;
+    uint32_t i, j;
+    triangle(id, i, j);
+    const int in_row = (int)(quarter / along) * kPart, in_col = (int)(quarter % along) * kPart;
+    const int row0 = (int)i * SIDE + in_row, col0 = (int)j * SIDE + in_col;
+    if (row0 >= pitch || col0 >= pitch) return;                // the same in all lanes
+    const float* from = e.pieces + (int64_t)id * splits * (SIDE * SIDE);
+    const uint32_t c = t & 7;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const uint32_t r = p * 32 + (t >> 3);
+        float v[8] = {};
+        for (int k = 0; k < splits; ++k) {
+            Raw<ZPQ_F32, 8> x;
+            x.template load<false>(from, (int64_t)k * (SIDE * SIDE) + (in_row + r) * SIDE + in_col + c * 8);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) v[n] += x.get(n);
+        }
+        const int row = row0 + (int)r, col = col0 + (int)c * 8;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            v[n] = row < small && col + n < small ? v[n] * (1.0f / kScale) : 0.0f;
+            turned[(c * 8 + n) * kPart + (((r >> 3) ^ c) << 3) + (r & 7)] = (_Float16)v[n];
+        }
+        Raw<ZPQ_F16, 8> h;
+        h.set(v);
+        if (row < small) h.template store<false>(e.a16, (int64_t)row * pitch + col);
+    }
+    if (i == j) return;
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const uint32_t column = p * 32 + (t >> 3);
+        if (col0 + (int)column < small)
+            *reinterpret_cast<u32x4*>(e.a16 + (int64_t)(col0 + (int)column) * pitch + row0 + c * 8) =
+                *reinterpret_cast<const u32x4*>(&turned[column * kPart + ((c ^ (column >> 3)) << 3)]);
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ void put_row(void* to, int64_t at, const float (&x)[8], int have) {
     Raw<DT, 8> r;
@@ -663,7 +737,7 @@ inline int64_t tiles_of(Shape s, int64_t side) { return tiled(s) ? div_up(s.rows
 inline bool shape_ok(Shape s) { return s.rows >= 0 && s.cols >= 0 && s.rows <= kMaxSide && s.cols <= kMaxSide && s.rows * s.cols <= (1LL << 34); }
 
 // Bytes of a matrix's part of the workspace, and the addresses in it.
-inline int64_t place(Shape s, char* at, Entry* e) {
+inline int64_t place(Shape s, int splits, char* at, Entry* e) {
     const int64_t px = up(s.cols, 64), pt = up(s.rows, 64), pa = up(small_of(s), 64), parts = parts_of(s), longs = longs_of(s);
     const int64_t halves = tiled(s) ? 2 : 0;
     int64_t used = 0;
@@ -676,6 +750,7 @@ inline int64_t place(Shape s, char* at, Entry* e) {
     char* other = take((s.rows <= s.cols ? s.cols * pt : s.rows * px) * halves);
     char *a16 = take(small_of(s) * pa * halves), *b16 = take(small_of(s) * pa * halves);
     char *part = take(parts * 8), *inv = take(16), *gram = take(longs * kFew * kFew * 8), *poly = take(longs ? kFew * kFew * 4 : 0);
+    char* pieces = take(splits > 1 ? triangle_of(s, 256) * splits * (256 * 256 * 4) : 0);
     if (e) {
         e->x32 = reinterpret_cast<float*>(x32);
         e->x16 = reinterpret_cast<_Float16*>(x16);
@@ -690,6 +765,7 @@ inline int64_t place(Shape s, char* at, Entry* e) {
         e->pitch_x = (uint32_t)px;
         e->pitch_t = (uint32_t)pt;
         e->pitch_a = (uint32_t)pa;
+        e->pieces = reinterpret_cast<float*>(pieces);
         e->parts = (uint32_t)parts;
         e->longs = (uint32_t)longs;
         e->gram = reinterpret_cast<double*>(gram);
@@ -700,25 +776,49 @@ inline int64_t place(Shape s, char* at, Entry* e) {
 
 // Matrices that are worked on at a time: consecutive ones up to kGroup elements, one at least.
 struct Group {
-    int64_t first, end, bytes, parts, cuts, sym, full, longs, ones;
-    int side_sym, side_full;
+    int64_t first, end, bytes, parts, cuts, sym, large, full, longs, ones;
+    int side_sym, side_full, splits;          // of square products (B), of X', pieces of A's sums (tiles of 256)
 };
 // The largest tile that leaves the chip's 256 CUs enough workgroups.
 template <class COUNT>
 inline int side_of(COUNT count) { return count(256) >= 192 ? 256 : count(128) >= 256 ? 128 : 64; }
 
+// Pieces of A's sums with tiles of 256 (1: none, and tiles of side_sym). Time in slabs of a tile of 256: rounds of the
+// 256 CUs by slabs of a piece; writing and reading a piece costs a CU about as much as 10 slabs (measured: 256 KB
+// twice, 1.4 us a slab). For matrices of one length only: sums of different length even out by themselves (a layer's
+// four matrices: 163 us without, 190 with). A slab of a 128 tile takes 2/3 of it, two at a time on a CU, of a 64 one 2/5, four at a time.
+inline int splits_of(int64_t large, int64_t tiles, int side, int64_t longest) {
+    const int64_t slabs = div_up(longest, 64);
+    const double now = side == 256 ? (double)div_up(tiles, 256) * slabs
+                     : side == 128 ? (double)div_up(tiles, 512) * slabs * 2 / 3 : (double)div_up(tiles, 1024) * slabs * 2 / 5;
+    double best = now * 0.85;                 // worth its memory
+    int splits = 1;
+    for (int s = 2; s <= 8 && large > 0; ++s) {
+        const double rounds = (double)div_up(large * s, 256), t = rounds * (div_up(slabs, s) + 10);
+        if (t < best) {
+            best = t;
+            splits = s;
+        }
+    }
+    return splits;
+}
+
 template <class SHAPES>
 Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
-    Group g{first, first, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    int64_t elems = 0;
+    Group g{first, first, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    int64_t elems = 0, longest = 0, shortest = kMaxSide;
     while (g.end < count) {
         const Shape s = shape(g.end);
         if (elems > 0 && elems + s.rows * s.cols > kGroup) break;
         elems += s.rows * s.cols;
         if (s.rows > 0 && s.cols > 0) {
-            g.bytes += place(s, nullptr, nullptr);
             g.parts += parts_of(s);
             g.cuts += tiled(s) ? cuts_of(s) : 0;
+            if (tiled(s)) {
+                const int64_t length = s.rows > s.cols ? s.rows : s.cols;
+                longest = length > longest ? length : longest;
+                shortest = length < shortest ? length : shortest;
+            }
             g.longs += longs_of(s);
             g.ones += one_workgroup(s.rows, s.cols);
         }
@@ -732,6 +832,10 @@ Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
     g.side_sym = side_of([&](int64_t side) { return sum(triangle_of, side); });
     g.side_full = side_of([&](int64_t side) { return sum(tiles_of, side); });
     g.sym = sum(triangle_of, g.side_sym);
+    g.large = sum(triangle_of, 256);
+    g.splits = longest == shortest ? splits_of(g.large, g.sym, g.side_sym, longest) : 1;
+    for (int64_t i = g.first; i < g.end; ++i)
+        if (shape(i).rows > 0 && shape(i).cols > 0) g.bytes += place(shape(i), g.splits, nullptr, nullptr);
     g.full = sum(tiles_of, g.side_full);
     return g;
 }
@@ -739,7 +843,7 @@ Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
 // The table: entries, then where each one's workgroups start, for the three kinds of launches.
 struct Table {
     Entry* entries;
-    uint32_t *cut, *sym, *full, *along, *part;
+    uint32_t *cut, *sym, *full, *along, *part, *large;
 };
 inline Table table_of(void* at, int64_t count) {
     Table t;
@@ -749,9 +853,10 @@ inline Table table_of(void* at, int64_t count) {
     t.full = t.sym + count;
     t.along = t.full + count;
     t.part = t.along + count;
+    t.large = t.part + count;
     return t;
 }
-static_assert(sizeof(Entry) + 20 <= ZPQ_MUON_BYTES(1) - ZPQ_MUON_BYTES(0), "ZPQ_MUON_BYTES");
+static_assert(sizeof(Entry) + 24 <= ZPQ_MUON_BYTES(1) - ZPQ_MUON_BYTES(0), "ZPQ_MUON_BYTES");
 
 // Fills the table; `entry(i, Entry&)` sets what place() does not.
 template <class SHAPES, class ENTRY>
@@ -760,7 +865,7 @@ void fill_table(const SHAPES& shape, const ENTRY& entry, int64_t count, void* ta
     for (int64_t first = 0; first < count;) {
         const Group g = group_at(shape, first, count);
         int64_t used = 0;
-        uint32_t cut = 0, sym = 0, full = 0, along = 0, part = 0;
+        uint32_t cut = 0, sym = 0, full = 0, along = 0, part = 0, large = 0;
         for (int64_t i = g.first; i < g.end; i += kFill) {
             Fill f = {};
             const int32_t some = (int32_t)(g.end - i < kFill ? g.end - i : kFill);
@@ -772,17 +877,19 @@ void fill_table(const SHAPES& shape, const ENTRY& entry, int64_t count, void* ta
                 e.start_full = full;
                 e.start_long = along;
                 e.start_part = part;
+                e.start_large = large;
                 if (s.rows == 0 || s.cols == 0) continue;
-                used += place(s, static_cast<char*>(workspace) + used, &e);
+                used += place(s, g.splits, static_cast<char*>(workspace) + used, &e);
                 entry(i + k, e);
                 cut += (uint32_t)(tiled(s) ? cuts_of(s) : 0);
                 part += (uint32_t)parts_of(s);
+                large += (uint32_t)triangle_of(s, 256);
                 sym += (uint32_t)triangle_of(s, g.side_sym);
                 full += (uint32_t)tiles_of(s, g.side_full);
                 along += (uint32_t)longs_of(s);
             }
             hipLaunchKernelGGL(k_fill, dim3(1), dim3(64), 0, st, f, (int32_t)i, some, t.entries, t.cut, t.sym, t.full,
-                               t.along, t.part);
+                               t.along, t.part, t.large);
         }
         first = g.end;
     }
@@ -829,7 +936,14 @@ void launch_group(const Table& t, const Group& g, int32_t g_dtype, const Hyper& 
         s.first = i == 0;
         s.last = i == steps - 1;
         s.odd = i & 1;
-        launch_symmetric<false>(sym, s, g, st);
+        if (g.splits > 1) {
+            const Work large{entries, t.large + g.first, count};
+            hipLaunchKernelGGL((k_symmetric_split<Tile256<kF16, kF16>>), dim3((uint32_t)(g.large * g.splits)), dim3(512), 0, st, large,
+                               (uint32_t)g.large, g.splits);
+            hipLaunchKernelGGL((k_symmetric_join<256>), dim3((uint32_t)(g.large * 16)), wg, 0, st, large, g.splits);
+        } else {
+            launch_symmetric<false>(sym, s, g, st);
+        }
         launch_symmetric<true>(sym, s, g, st);
         const dim3 grid((uint32_t)g.full);
         if (g.side_full == 256) hipLaunchKernelGGL((k_update<Tile256<kF16, kF16>, MUON>), grid, dim3(512), 0, st, full, s, sumsq);

@@ -462,7 +462,7 @@ typedef struct {
 
 /* Device memory of a plan's table alone; zpq_muon_plan_bytes: with the workspace, which
  * is bounded as zpq_orthogonalize's. */
-#define ZPQ_MUON_BYTES(count) ((int64_t)(count) * 232 + 64)
+#define ZPQ_MUON_BYTES(count) ((int64_t)(count) * 248 + 64)
 
 /*
  * Lay out `count` matrices for zpq_muon_step, at most 2^20.  Types as in zpq_adamw_plan_make.  The
