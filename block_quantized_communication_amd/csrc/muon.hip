@@ -260,6 +260,7 @@ __global__ __launch_bounds__(kThreads) void k_gram(Work w) {
         for (int q = 0; q < 2; ++q) to[(r + p) * kFew + c + q] = s[p][q];
 }
 
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 struct Coeffs {
     float abc[3 * kMaxSteps];
     int32_t steps;
@@ -482,6 +483,14 @@ __device__ __forceinline__ void put_row(int32_t dtype, void* to, int64_t at, con
     else if (dtype == ZPQ_F16) put_row<ZPQ_F16>(to, at, x, have);
     else put_row<ZPQ_BF16>(to, at, x, have);
 }
+__device__ __forceinline__ float get_one(int32_t dtype, const void* from, int64_t at) {
+    return dtype == ZPQ_F32 ? load1<ZPQ_F32>(from, at) : dtype == ZPQ_F16 ? load1<ZPQ_F16>(from, at) : load1<ZPQ_BF16>(from, at);
+}
+__device__ __forceinline__ void put_one(int32_t dtype, void* to, int64_t at, float x) {
+    if (dtype == ZPQ_F32) store1<ZPQ_F32>(to, at, x);
+    else if (dtype == ZPQ_F16) store1<ZPQ_F16>(to, at, x);
+    else store1<ZPQ_BF16>(to, at, x);
+}
 __device__ __forceinline__ void get_row(int32_t dtype, const void* from, int64_t at, float (&x)[8], int have) {
     const auto get = [&](auto r) {
         if (have >= 8) r.template load<false>(from, at);
@@ -593,7 +602,7 @@ __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, 
     double size = 0;
     for (uint32_t i = 0; i < e.parts; ++i) size += e.part[i];
     const double inv = size == 0.0 ? 0.0 : size < INFINITY ? 1.0 / sqrt(size) : NAN;
-    const int down = (f.side + 15) / 16, across = (f.length + 15) / 16, deep = (f.length + 31) / 32;
+    const bool deep = f.length > kOneLong / 2;
     float x[8][4];
     const auto row_of = [&](int n) { return ((wave * 8 + n) & 3) * 16 + r; };
     const auto col_of = [&](int n) { return ((wave * 8 + n) >> 2) * 16 + g * 4; };
@@ -601,12 +610,12 @@ __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, 
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const int i = row_of(n), j = col_of(n);
+            f16x4 h;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const _Float16 h = (_Float16)(x[n][q] * kScale);
-                x16[i * PX + j + q] = h;
-                t16[(j + q) * PA + i] = h;
-            }
+            for (int q = 0; q < 4; ++q) h[q] = (_Float16)(x[n][q] * kScale);
+            *reinterpret_cast<f16x4*>(x16 + i * PX + j) = h;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) t16[(j + q) * PA + i] = h[q];
         }
     };
     const auto piece = [&](const _Float16* from, int pitch, int row, int step) {
@@ -615,9 +624,20 @@ __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, 
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         const int i = row_of(n), j = col_of(n);
+        if (wide && i < f.side && j + 4 <= f.length) {
+            Raw<ZPQ_F32, 4> u;
+            u.load<false>(e.x32, i * f.step_i + j);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            x[n][q] = i < f.side && j + q < f.length ? (float)(e.x32[i * f.step_i + (j + q) * f.step_j] * inv) : 0.0f;
+            for (int q = 0; q < 4; ++q) x[n][q] = u.get(q);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[n][q] = i < f.side && j + q < f.length ? e.x32[i * f.step_i + (j + q) * f.step_j] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[n][q] = x[n][q] == 0.0f ? 0.0f : (float)(x[n][q] * inv);
     }
     for (int step = 0; step < k.steps; ++step) {
         const float a = k.abc[3 * step], b = k.abc[3 * step + 1], c = k.abc[3 * step + 2];
@@ -628,11 +648,19 @@ __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, 
         for (int n = 0; n < 2; ++n) {
             const int ti = (wave * 2 + n) >> 2, tj = (wave * 2 + n) & 3;
             f32x4 acc = {0, 0, 0, 0};
-            if (ti < down && tj < down)
-                for (int d = 0; d < deep; ++d)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(x16, PX, ti * 16, d), piece(x16, PX, tj * 16, d), acc, 0, 0, 0);
+            const auto add = [&](int d) {
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(x16, PX, ti * 16, d), piece(x16, PX, tj * 16, d), acc, 0, 0, 0);
+            };
 #pragma unroll
-            for (int q = 0; q < 4; ++q) a16[(tj * 16 + r) * PA + ti * 16 + g * 4 + q] = (_Float16)(acc[q] * (1.0f / kScale));
+            for (int d = 0; d < kOneLong / 64; ++d) add(d);
+            if (deep) {
+#pragma unroll
+                for (int d = kOneLong / 64; d < kOneLong / 32; ++d) add(d);
+            }
+            f16x4 h;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[q] = (_Float16)(acc[q] * (1.0f / kScale));
+            *reinterpret_cast<f16x4*>(a16 + (tj * 16 + r) * PA + ti * 16 + g * 4) = h;
         }
         __syncthreads();
 #pragma unroll
@@ -642,21 +670,20 @@ __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, 
 #pragma unroll
             for (int d = 0; d < 2; ++d)
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(a16, PA, ti * 16, d), piece(a16, PA, tj * 16, d), acc, 0, 0, 0);
+            const int at = (tj * 16 + r) * PA + ti * 16 + g * 4;
+            f16x4 h = *reinterpret_cast<const f16x4*>(a16 + at);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int at = (tj * 16 + r) * PA + ti * 16 + g * 4 + q;
-                b16[at] = (_Float16)fmaf(b, (float)a16[at], c * (acc[q] * (1.0f / kScale)));
-            }
+            for (int q = 0; q < 4; ++q) h[q] = (_Float16)fmaf(b, (float)h[q], c * (acc[q] * (1.0f / kScale)));
+            *reinterpret_cast<f16x4*>(b16 + at) = h;
         }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const int ti = (wave * 8 + n) & 3, tj = (wave * 8 + n) >> 2;
             f32x4 acc = {0, 0, 0, 0};
-            if (ti < down && tj < across)
 #pragma unroll
-                for (int d = 0; d < 2; ++d)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(t16, PA, tj * 16, d), piece(b16, PA, ti * 16, d), acc, 0, 0, 0);
+            for (int d = 0; d < 2; ++d)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(piece(t16, PA, tj * 16, d), piece(b16, PA, ti * 16, d), acc, 0, 0, 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) x[n][q] = fmaf(acc[q], 1.0f / (kScale * kScale), a * x[n][q]);
         }
@@ -670,14 +697,12 @@ __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, 
         for (int q = 0; q < 4; ++q) {
             if (i >= f.side || j + q >= f.length) continue;
             const int64_t at = wide ? i * e.ld_p + j + q : (j + q) * e.ld_p + i;
-            float v[8] = {x[n][q]};
+            float y = x[n][q];
             if constexpr (MUON) {
-                float p[8];
-                get_row(s.out_dtype, e.p, at, p, 1);
-                v[0] = p[0] * keep - rate * x[n][q];
-                if (s.copy_dtype >= 0) put_row(s.copy_dtype, e.copy, at, v, 1);
+                y = get_one(s.out_dtype, e.p, at) * keep - rate * y;
+                if (s.copy_dtype >= 0) put_one(s.copy_dtype, e.copy, at, y);
             }
-            put_row(s.out_dtype, e.p, at, v, 1);
+            put_one(s.out_dtype, e.p, at, y);
         }
     }
 }
@@ -705,14 +730,11 @@ __global__ __launch_bounds__(kThreads) void k_update_few(Work w, Apply s, const 
 #pragma unroll
         for (int k = 0; k < kFew; ++k) y = fmaf(poly[i][k], x[k], y);
         const int64_t at = wide ? i * e.ld_p + j : j * e.ld_p + i;
-        float v[8] = {y};
         if constexpr (MUON) {
-            float p[8];
-            get_row(s.out_dtype, e.p, at, p, 1);
-            v[0] = p[0] * keep - rate * y;
-            if (s.copy_dtype >= 0) put_row(s.copy_dtype, e.copy, at, v, 1);
+            y = get_one(s.out_dtype, e.p, at) * keep - rate * y;
+            if (s.copy_dtype >= 0) put_one(s.copy_dtype, e.copy, at, y);
         }
-        put_row(s.out_dtype, e.p, at, v, 1);
+        put_one(s.out_dtype, e.p, at, y);
     }
 }
 
