@@ -495,7 +495,11 @@ inline dim3 grid_of_quads(int64_t m, int64_t n) {
 // How a product is cut: the tile's side and the parts of its sum.
 struct Cut { int side; int64_t splits; int32_t per_split; };
 
-inline Cut cut_of(int64_t m, int64_t n, int64_t slabs) {
+// 16-bit results: tiles of 256 where they keep half of the 256 CUs busy (3000 x 3000 x 8192, 144 tiles: 86 us, 118 with
+// tiles of 64; 95 with 128), else of 64 (2048 x 2048 x 2048, 64 tiles of 256: 28 us, 16 with 64; 29 with 128).
+// Binary32 ones spend twice the time on a slab, which tiles of 128 suffice for (3000 x 3300 x 2000: 48 us, 55 with
+// 256, 52 with 64).
+inline Cut cut_of(int64_t m, int64_t n, int64_t slabs, bool full) {
     const auto tiles = [&](int64_t s) { return ((m + s - 1) / s) * ((n + s - 1) / s); };
     Cut c{256, 1, (int32_t)slabs};
     if (m <= 32) {                             // 8 waves of 16 columns; 512 workgroups, but a turn of 32 slabs each
@@ -508,8 +512,7 @@ inline Cut cut_of(int64_t m, int64_t n, int64_t slabs) {
         }
         return c;
     }
-    if (tiles(256) < 192) c.side = 128;
-    if (c.side == 128 && tiles(128) < 256) c.side = 64;
+    if (full ? tiles(256) < 192 : tiles(256) < 128) c.side = full && tiles(128) >= 256 ? 128 : 64;
     int64_t want = 512 / (tiles(c.side) > 0 ? tiles(c.side) : 1);
     if (c.side == 256 || want < 2) want = 1;
     int64_t per = (slabs + want - 1) / want;
@@ -528,7 +531,7 @@ void launch_matmul(const Operand& a, const Operand& b, Result o, const Cut& c, h
         if (o.m <= 16) hipLaunchKernelGGL((k_matmul_few<KA, KB, FULL, 1>), grid, wg, 0, st, a, b, o);
         else hipLaunchKernelGGL((k_matmul_few<KA, KB, FULL, 2>), grid, wg, 0, st, a, b, o);
     } else if (c.side == 256) launch_tiles<Tile256<KA, KB, FULL>>(a, b, o, c.splits, st);
-    else if (c.side == 128) launch_tiles<TileSmall<KA, KB, 4, 4, FULL>>(a, b, o, c.splits, st);
+    else if (FULL && c.side == 128) launch_tiles<TileSmall<KA, KB, 4, 4, true>>(a, b, o, c.splits, st);
     else launch_tiles<TileSmall<KA, KB, 2, 2, FULL>>(a, b, o, c.splits, st);
     if (c.splits > 1) {
         hipLaunchKernelGGL(k_join, grid_of_quads(o.m, o.n), dim3(kThreads), 0, st, o, (int32_t)c.splits);
@@ -636,8 +639,9 @@ zpq_status zpq_matmul_f8_bytes(int64_t m, int64_t n, int64_t k, int64_t* bytes) 
     if (!bytes) return ZPQ_ERR_NULL;
     const zpq_status s = matmul_sizes(m, n, k);
     if (s != ZPQ_OK) return s;
-    const Cut c = cut_of(m, n, blocks_of(k));
-    *bytes = c.splits > 1 ? c.splits * m * n * 4 : 0;
+    const int64_t a = cut_of(m, n, blocks_of(k), false).splits, b = cut_of(m, n, blocks_of(k), true).splits;
+    const int64_t splits = a > b ? a : b;
+    *bytes = splits > 1 ? splits * m * n * 4 : 0;
     return ZPQ_OK;
 }
 
@@ -653,7 +657,7 @@ zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64
     if (m == 0 || n == 0) return ZPQ_OK;
     if (!out || (k > 0 && (!a->codes || !a->scales || !b->codes || !b->scales))) return ZPQ_ERR_NULL;
     const int64_t slabs = blocks_of(k), pitch = slabs * kBlock, kb4 = blocks4_of(k);
-    const Cut c = cut_of(m, n, slabs);
+    const Cut c = cut_of(m, n, slabs, out_dtype == ZPQ_F32);
     const int64_t need = c.splits > 1 ? c.splits * m * n * 4 : 0;
     if (need > 0 && !workspace) return ZPQ_ERR_NULL;
     if (workspace_bytes < need) return ZPQ_ERR_SIZE;

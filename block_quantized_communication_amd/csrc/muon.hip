@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void k_gram(Work w) {
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 struct Coeffs {
     float abc[3 * kMaxSteps];
-    int32_t steps;
+    int32_t steps, g_dtype;
 };
 typedef double Square[kFew][kFew + 1];
 
@@ -588,20 +588,17 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_update(Work 
 
 // The whole iteration of a matrix of up to 64 x 256 on one workgroup, where launches would take far longer
 // than the products: the same operands and sums as above, in LDS, X itself in registers.  8 waves;
-// X' in tiles of 16 x 16, tile t of 4 down and 16 across is wave t / 8's.
+// X' in tiles of 16 x 16, tile t of 4 down and 16 across is wave t / 8's.  Without a momentum it takes the input itself.
 template <bool MUON>
 __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, Coeffs k, Apply s, const double* __restrict__ sumsq) {
     constexpr int PX = kOneLong + 8, PA = kOneSide + 8;        // pitches that spread rows over the banks
     __shared__ __attribute__((aligned(16))) _Float16 x16[kOneSide * PX], t16[kOneLong * PA], a16[kOneSide * PA], b16[kOneSide * PA];
     const Entry& e = entries[blockIdx.x];
-    if (e.parts == 0 || !one_workgroup(e)) return;
+    if (!one_workgroup(e)) return;             // an empty matrix neither
     if (MUON && stopped(sumsq)) return;
     const Few f(e);
     const bool wide = e.rows <= e.cols;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    double size = 0;
-    for (uint32_t i = 0; i < e.parts; ++i) size += e.part[i];
-    const double inv = size == 0.0 ? 0.0 : size < INFINITY ? 1.0 / sqrt(size) : NAN;
     const bool deep = f.length > kOneLong / 2;
     float x[8][4];
     const auto row_of = [&](int n) { return ((wave * 8 + n) & 3) * 16 + r; };
@@ -624,16 +621,42 @@ __global__ __launch_bounds__(512) void k_one(const Entry* __restrict__ entries, 
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         const int i = row_of(n), j = col_of(n);
-        if (wide && i < f.side && j + 4 <= f.length) {
-            Raw<ZPQ_F32, 4> u;
-            u.load<false>(e.x32, i * f.step_i + j);
+        if constexpr (MUON) {
+            if (wide && i < f.side && j + 4 <= f.length) {
+                Raw<ZPQ_F32, 4> u;
+                u.load<false>(e.x32, i * f.step_i + j);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[n][q] = u.get(q);
+                for (int q = 0; q < 4; ++q) x[n][q] = u.get(q);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[n][q] = i < f.side && j + q < f.length ? e.x32[i * f.step_i + (j + q) * f.step_j] : 0.0f;
+            }
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[n][q] = i < f.side && j + q < f.length ? e.x32[i * f.step_i + (j + q) * f.step_j] : 0.0f;
+            for (int q = 0; q < 4; ++q) {
+                const int64_t at = wide ? i * e.ld_g + j + q : (j + q) * e.ld_g + i;
+                x[n][q] = i < f.side && j + q < f.length ? get_one(k.g_dtype, e.g, at) : 0.0f;
+            }
         }
     }
+    double size = 0;
+    if constexpr (MUON) {
+        for (uint32_t i = 0; i < e.parts; ++i) size += e.part[i];
+    } else {
+        __shared__ double sums[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) size = fma((double)x[n][q], (double)x[n][q], size);
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) size += __shfl_xor(size, d);
+        if (lane == 0) sums[wave] = size;
+        __syncthreads();
+        size = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) size += sums[i];
+    }
+    const double inv = size == 0.0 ? 0.0 : size < INFINITY ? 1.0 / sqrt(size) : NAN;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
 #pragma unroll
@@ -934,12 +957,14 @@ void launch_group(const Table& t, const Group& g, int32_t g_dtype, const Hyper& 
     const Work cut{entries, t.cut + g.first, count}, sym{entries, t.sym + g.first, count}, full{entries, t.full + g.first, count};
     const Work part{entries, t.part + g.first, count};
     const dim3 cuts((uint32_t)g.cuts), parts((uint32_t)g.parts), wg(kThreads);
-    if (g_dtype == ZPQ_F32) hipLaunchKernelGGL((k_gather<ZPQ_F32, MUON>), parts, wg, 0, st, part, h, sumsq);
+    if (!MUON && g.ones > 0) {                 // of one shape: all of them
+    } else if (g_dtype == ZPQ_F32) hipLaunchKernelGGL((k_gather<ZPQ_F32, MUON>), parts, wg, 0, st, part, h, sumsq);
     else if (g_dtype == ZPQ_F16) hipLaunchKernelGGL((k_gather<ZPQ_F16, MUON>), parts, wg, 0, st, part, h, sumsq);
     else hipLaunchKernelGGL((k_gather<ZPQ_BF16, MUON>), parts, wg, 0, st, part, h, sumsq);
     Coeffs k;
     for (int32_t i = 0; i < 3 * steps; ++i) k.abc[i] = coeffs[i];
     k.steps = steps;
+    k.g_dtype = g_dtype;
     if (g.longs > 0) {
         const Work along{entries, t.along + g.first, count};
         const dim3 longs((uint32_t)g.longs);

@@ -423,7 +423,8 @@ zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64
  * five times, to between 0.7 and 1.2.  Products take 16-bit operands (11 bits), with
  * sums and X itself in binary32; the result is within about 2e-3 of the exact iteration's, so it
  * comes in 16 bits.  A matrix with a value that is not finite comes out as NaN.
- * 1 <= steps <= 32, coefficients at most 64 in size, such that singular values stay under 50.
+ * 1 <= steps <= 32, coefficients at most 64 in size, such that the entries of A and of
+ * b A + c A A stay under 60 (binary16 at the operands' scale; over it results are not finite).
  * rows, cols <= 2^22, rows * cols <= 2^34.
  */
 /*
