@@ -532,6 +532,8 @@ void launch_matmul(const Operand& a, const Operand& b, Result o, const Cut& c, h
         else hipLaunchKernelGGL((k_matmul_few<KA, KB, FULL, 2>), grid, wg, 0, st, a, b, o);
     } else if (c.side == 256) launch_tiles<Tile256<KA, KB, FULL>>(a, b, o, c.splits, st);
     else if (FULL && c.side == 128) launch_tiles<TileSmall<KA, KB, 4, 4, true>>(a, b, o, c.splits, st);
+    else if (((o.m + 63) / 64) * ((o.n + 63) / 64) * c.splits <= kFewWorkgroups)
+        launch_tiles<TileSmall<KA, KB, 2, 2, FULL, 4>>(a, b, o, c.splits, st);
     else launch_tiles<TileSmall<KA, KB, 2, 2, FULL>>(a, b, o, c.splits, st);
     if (c.splits > 1) {
         hipLaunchKernelGGL(k_join, grid_of_quads(o.m, o.n), dim3(kThreads), 0, st, o, (int32_t)c.splits);

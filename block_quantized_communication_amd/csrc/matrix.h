@@ -66,7 +66,9 @@ __device__ __forceinline__ void copy4(i32x4 from, uint32_t lane_offset, uint32_t
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :: "s"(scalar(to)), "v"(lane_offset), "s"(from), "s"(scalar(offset)) : "memory");
 }
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Until at most LEFT of the wave's memory accesses, the latest ones, are under way.
+template <int LEFT = 0>
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LEFT) : "memory"); }
 // Own LDS reads done, then all waves here.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -356,15 +358,18 @@ struct Tile256 {
     }
 };
 
-// The loop of a smaller tile: 4 waves, 2 x 2, each MI * 16 rows of A by NI * 16 of B, two
-// buffers.  Several workgroups of a CU hide each other's waits.
-template <int KA, int KB, int MI_, int NI_, bool FULL = false>
+// The loop of a smaller tile: 4 waves, 2 x 2, each MI * 16 rows of A by NI * 16 of B.  Several
+// workgroups of a CU hide each other's waits. BUFFERS: 2, or 4 where there are few workgroups and a copy's
+// way is what takes time (1024 x 1024 orthogonalised: 196 -> 149 us; but 999 x 4004 x 1001, 1008 tiles, 10.3 -> 11.4,
+// since only two workgroups of four buffers fit a CU).
+template <int KA, int KB, int MI_, int NI_, bool FULL = false, int BUFFERS = 2>
 struct TileSmall {
     static constexpr int MI = MI_, NI = NI_, BM = 32 * MI, BN = 32 * NI, kThreadsWg = 256, kWaves = 2;
     static constexpr int kSideA = BM * kSlab, kSideB = BN * kSlab, kBuffer = kSideA + kSideB;
     static constexpr bool kScaled = KA != kF16;
     static constexpr int kScaleBytes = kScaled ? (BM + BN) * 4 : 0;
-    static constexpr int kLds = 2 * kBuffer + kScaleBytes;
+    static constexpr int kBuffers = BUFFERS, kCopies = MI + NI;       // copies of a slab, of a wave
+    static constexpr int kLds = kBuffers * kBuffer + kScaleBytes;
     static_assert(BM + BN <= 256, "one exponent word a thread");
 
     const uint8_t* lds;
@@ -377,6 +382,9 @@ struct TileSmall {
     __device__ __forceinline__ uint32_t wm() const { return wave >> 1; }
     __device__ __forceinline__ uint32_t wn() const { return wave & 1; }
 
+    // Waves past the exponent words' rows bring the others' again, so that all wait for the same number.
+    __device__ __forceinline__ uint32_t scale_wave() const { return wave % ((BM + BN) / 64); }
+
     __device__ __forceinline__ void start_copy(int slab, int buffer) {
         const uint32_t to = base + buffer * kBuffer;
 #pragma unroll
@@ -386,7 +394,7 @@ struct TileSmall {
     }
     __device__ __forceinline__ void start_scales(int slab) {
         if constexpr (kScaled)
-            if (wave * 64 < BM + BN) copy4(rs, off_s, (uint32_t)slab, base + 2 * kBuffer + wave * 256);
+            copy4(rs, off_s, (uint32_t)slab, base + kBuffers * kBuffer + scale_wave() * 256);
     }
     __device__ __forceinline__ i32x8 piece(const uint8_t* side, uint32_t row) const {
         const uint32_t r = lane & 15, g = lane >> 4;
@@ -397,19 +405,26 @@ struct TileSmall {
     }
     template <int SEL>
     __device__ __forceinline__ void step(int slab, int end) {
-        constexpr int buffer = SEL & 1;
-        wait_copies();
-        meet();                               // slab is there, and the other buffer read
+        constexpr int buffer = SEL & (kBuffers - 1), freed = (SEL + kBuffers - 1) & (kBuffers - 1);
+        // copies of the slabs between this one and those that are not started yet may be under way
+        if constexpr (kBuffers == 2) {
+            wait_copies();
+        } else {
+            if (slab + 2 < end) wait_copies<2 * kCopies + (kScaled && SEL >= 2)>();
+            else if (slab + 1 < end) wait_copies<kCopies + (kScaled && SEL == 3)>();
+            else wait_copies();
+        }
+        meet();                               // slab is there, and the buffer of the one before read
         if constexpr (kScaled && SEL == 0) {
-            const int* s = reinterpret_cast<const int*>(lds + 2 * kBuffer) + (lane & 15);
+            const int* s = reinterpret_cast<const int*>(lds + kBuffers * kBuffer) + (lane & 15);
 #pragma unroll
             for (int i = 0; i < MI; ++i) sa[i] = s[(wm() * MI + i) * 16];
 #pragma unroll
             for (int j = 0; j < NI; ++j) sb[j] = s[BM + (wn() * NI + j) * 16];
         }
-        if (slab + 1 < end) {
-            start_copy(slab + 1, buffer ^ 1);
-            if constexpr (SEL == 3) start_scales(slab + 1);
+        if (slab + kBuffers - 1 < end) {
+            if constexpr (((SEL + kBuffers - 1) & 3) == 0) start_scales(slab + kBuffers - 1);
+            start_copy(slab + kBuffers - 1, freed);
         }
         const uint8_t* side_a = lds + buffer * kBuffer + wm() * MI * 16 * kSlab;
         const uint8_t* side_b = lds + buffer * kBuffer + kSideA + wn() * NI * 16 * kSlab;
@@ -442,9 +457,9 @@ struct TileSmall {
             off_b[j] = r * b.pitch + (((lane & 7) ^ (r & 7)) << 4);
         }
         if constexpr (kScaled) {
-            const bool of_a = wave * 64 < BM;
+            const bool of_a = scale_wave() * 64 < BM;
             const Operand& o = of_a ? a : b;
-            const int64_t row = of_a ? row_a : row_b, within = wave * 64 + lane - (of_a ? 0 : BM);
+            const int64_t row = of_a ? row_a : row_b, within = scale_wave() * 64 + lane - (of_a ? 0 : BM);
             const int64_t first_scale = row >> o.scale_shift, rows = ((o.rows - 1) >> o.scale_shift) + 1;
             rs = descriptor(o.scale + first_scale * o.scale_pitch, (rows - first_scale) * o.scale_pitch);
             off_s = (uint32_t)(((row + within) >> o.scale_shift) - first_scale) * o.scale_pitch;
@@ -453,8 +468,10 @@ struct TileSmall {
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        start_copy(first, 0);
         start_scales(first);
+#pragma unroll
+        for (int i = 0; i < kBuffers - 1; ++i)
+            if (first + i < end) start_copy(first + i, i);
         for (int slab = first; slab < end; slab += 4) {
             step<0>(slab, end);
             if (slab + 1 < end) step<1>(slab + 1, end);
@@ -481,6 +498,8 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t count, uint32_t ro
     j = in / high;
     i = band * 4 + (in - j * high);
 }
+
+constexpr int64_t kFewWorkgroups = 512;       // two a CU: up to here four buffers
 
 }  // namespace zpq_matrix
 

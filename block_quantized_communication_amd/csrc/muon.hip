@@ -945,6 +945,8 @@ void launch_symmetric(const Work& w, const Apply& s, const Group& g, hipStream_t
     const dim3 grid((uint32_t)g.sym);
     if (g.side_sym == 256) hipLaunchKernelGGL((k_symmetric<Tile256<kF16, kF16>, SQUARE>), grid, dim3(512), 0, st, w, s);
     else if (g.side_sym == 128) hipLaunchKernelGGL((k_symmetric<TileSmall<kF16, kF16, 4, 4>, SQUARE>), grid, dim3(256), 0, st, w, s);
+    else if (g.sym <= kFewWorkgroups)
+        hipLaunchKernelGGL((k_symmetric<TileSmall<kF16, kF16, 2, 2, false, 4>, SQUARE>), grid, dim3(256), 0, st, w, s);
     else hipLaunchKernelGGL((k_symmetric<TileSmall<kF16, kF16, 2, 2>, SQUARE>), grid, dim3(256), 0, st, w, s);
 }
 
@@ -995,6 +997,8 @@ void launch_group(const Table& t, const Group& g, int32_t g_dtype, const Hyper& 
         const dim3 grid((uint32_t)g.full);
         if (g.side_full == 256) hipLaunchKernelGGL((k_update<Tile256<kF16, kF16>, MUON>), grid, dim3(512), 0, st, full, s, sumsq);
         else if (g.side_full == 128) hipLaunchKernelGGL((k_update<TileSmall<kF16, kF16, 4, 4>, MUON>), grid, dim3(256), 0, st, full, s, sumsq);
+        else if (g.full <= kFewWorkgroups)
+            hipLaunchKernelGGL((k_update<TileSmall<kF16, kF16, 2, 2, false, 4>, MUON>), grid, dim3(256), 0, st, full, s, sumsq);
         else hipLaunchKernelGGL((k_update<TileSmall<kF16, kF16, 2, 2>, MUON>), grid, dim3(256), 0, st, full, s, sumsq);
     }
 }
