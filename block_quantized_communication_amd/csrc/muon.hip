@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void k_gather(Work w, Hyper h, const doub
 // 1 / norm of each matrix; 0 for a matrix of zeros, NaN for one that is not finite.
 __global__ __launch_bounds__(kThreads) void k_norms(const Entry* __restrict__ entries) {
     const Entry& e = entries[blockIdx.x];
-    if (e.parts == 0 || few(e) || one_workgroup(e)) return;     // (cuts: an empty matrix)
+    if (e.parts == 0 || few(e) || one_workgroup(e)) return;     // (no parts: an empty matrix)
     double sum = 0;
     for (uint32_t i = threadIdx.x; i < e.parts; i += kThreads) sum += e.part[i];
     __shared__ double part[kThreads / 64];
