@@ -824,9 +824,12 @@ struct Group {
     int64_t first, end, bytes, parts, cuts, sym, large, full, longs, ones;
     int side_sym, side_full, splits;          // of square products (B), of X', pieces of A's sums (tiles of 256)
 };
-// The largest tile that leaves the chip's 256 CUs enough workgroups.
+// Tiles of 256 where they keep half of the 256 CUs busy (4096 x 4096: 1603 us, with tiles of 128 for the
+// symmetric products 1892), of 128 where they fill them once, else of 64.  For A of matrices of different lengths
+// three quarters: the longest sum decides (a layer's four matrices: 177 us, 164 with tiles of 128).
+constexpr int64_t kHalfBusy = 128;
 template <class COUNT>
-inline int side_of(COUNT count) { return count(256) >= 192 ? 256 : count(128) >= 256 ? 128 : 64; }
+inline int side_of(COUNT count, int64_t least) { return count(256) >= least ? 256 : count(128) >= 256 ? 128 : 64; }
 
 // Pieces of A's sums with tiles of 256 (1: none, and tiles of side_sym). Time in slabs of a tile of 256: rounds of the
 // 256 CUs by slabs of a piece; writing and reading a piece costs a CU about as much as 10 slabs (measured: 256 KB
@@ -874,8 +877,8 @@ Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
         for (int64_t i = g.first; i < g.end; ++i) n += shape(i).rows > 0 && shape(i).cols > 0 ? of(shape(i), side) : 0;
         return n;
     };
-    g.side_sym = side_of([&](int64_t side) { return sum(triangle_of, side); });
-    g.side_full = side_of([&](int64_t side) { return sum(tiles_of, side); });
+    g.side_sym = side_of([&](int64_t side) { return sum(triangle_of, side); }, longest == shortest ? kHalfBusy : 192);
+    g.side_full = side_of([&](int64_t side) { return sum(tiles_of, side); }, kHalfBusy);
     g.sym = sum(triangle_of, g.side_sym);
     g.large = sum(triangle_of, 256);
     g.splits = longest == shortest ? splits_of(g.large, g.sym, g.side_sym, longest) : 1;
@@ -993,7 +996,10 @@ void launch_group(const Table& t, const Group& g, int32_t g_dtype, const Hyper& 
         } else {
             launch_symmetric<false>(sym, s, g, st);
         }
-        launch_symmetric<true>(sym, s, g, st);
+        if (g.large >= kHalfBusy)
+            hipLaunchKernelGGL((k_symmetric<Tile256<kF16, kF16>, true>), dim3((uint32_t)g.large), dim3(512), 0, st,
+                               Work{entries, t.large + g.first, count}, s);
+        else launch_symmetric<true>(sym, s, g, st);
         const dim3 grid((uint32_t)g.full);
         if (g.side_full == 256) hipLaunchKernelGGL((k_update<Tile256<kF16, kF16>, MUON>), grid, dim3(512), 0, st, full, s, sumsq);
         else if (g.side_full == 128) hipLaunchKernelGGL((k_update<TileSmall<kF16, kF16, 4, 4>, MUON>), grid, dim3(256), 0, st, full, s, sumsq);
