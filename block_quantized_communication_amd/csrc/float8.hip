@@ -495,9 +495,9 @@ inline dim3 grid_of_quads(int64_t m, int64_t n) {
 // How a product is cut: the tile's side and the parts of its sum.
 struct Cut { int side; int64_t splits; int32_t per_split; };
 
-// 16-bit results: tiles of 256 where they keep half of the 256 CUs busy (3000 x 3000 x 8192, 144 tiles: 86 us, 118 with
+// bf16 results: tiles of 256 where they keep half of the 256 CUs busy (3000 x 3000 x 8192, 144 tiles: 86 us, 118 with
 // tiles of 64; 95 with 128), else of 64 (2048 x 2048 x 2048, 64 tiles of 256: 28 us, 16 with 64; 29 with 128).
-// Binary32 ones spend twice the time on a slab, which tiles of 128 suffice for (3000 x 3300 x 2000: 48 us, 55 with
+// Others (full) spend twice the time on a slab, which tiles of 128 suffice for (3000 x 3300 x 2000: 48 us, 55 with
 // 256, 52 with 64).
 inline Cut cut_of(int64_t m, int64_t n, int64_t slabs, bool full) {
     const auto tiles = [&](int64_t s) { return ((m + s - 1) / s) * ((n + s - 1) / s); };
@@ -540,9 +540,14 @@ void launch_matmul(const Operand& a, const Operand& b, Result o, const Cut& c, h
     }
 }
 
+// Which results get sums to binary32's precision (matrix.h, products). What the 8-bit instructions drop is, as a root mean
+// square over activations with one column in a hundred 30 (1000) times as large, 5e-5 (9e-5) of the result: far
+// below bf16's rounding, 1.7e-3, but a quarter (two fifths) of binary16's, 2.1e-4.
+inline bool full_sums(int32_t dtype) { return dtype != ZPQ_BF16; }
+
 template <int KA, int KB>
 void launch_matmul(const Operand& a, const Operand& b, const Result& o, const Cut& c, hipStream_t st) {
-    if (o.dtype == ZPQ_F32) launch_matmul<KA, KB, true>(a, b, o, c, st);
+    if (full_sums(o.dtype)) launch_matmul<KA, KB, true>(a, b, o, c, st);
     else launch_matmul<KA, KB, false>(a, b, o, c, st);
 }
 
@@ -659,7 +664,7 @@ zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64
     if (m == 0 || n == 0) return ZPQ_OK;
     if (!out || (k > 0 && (!a->codes || !a->scales || !b->codes || !b->scales))) return ZPQ_ERR_NULL;
     const int64_t slabs = blocks_of(k), pitch = slabs * kBlock, kb4 = blocks4_of(k);
-    const Cut c = cut_of(m, n, slabs, out_dtype == ZPQ_F32);
+    const Cut c = cut_of(m, n, slabs, full_sums(out_dtype));
     const int64_t need = c.splits > 1 ? c.splits * m * n * 4 : 0;
     if (need > 0 && !workspace) return ZPQ_ERR_NULL;
     if (workspace_bytes < need) return ZPQ_ERR_SIZE;

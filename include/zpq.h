@@ -393,14 +393,18 @@ typedef struct {
 /*
  * out = [out +] A * B^T for A [m, k] and B [n, k]:
  *   out[i][j] = RNE([out[i][j] +] sum over k of a[i][k] * b[j][k])
- * with exact products and sums in binary32, in an order that depends on the sizes only.
- * For 16-bit results the matrix core drops what lies more than about 2^-19 below the largest of the
- * products that it adds at a time (1e-5 of a sum of like values, far below the result's
- * rounding).  For ZPQ_F32 results elements are multiplied as 16-bit floats of binary32's
- * range, which holds them exactly, at half the rate and to binary32's precision; there an
- * element over the largest binary32 is infinite, and one below 2^-126 may count as 0.  With x, dy the input and
- * output gradient [tokens, .] and w [outputs, inputs]: y = x w^T; dx = dy w takes w's
- * transposed tiles for B; dw = dy^T x takes both along their columns.
+ * with exact products and sums in binary32, in an order that depends on the sizes and on
+ * whether results are bf16 only.
+ *   ZPQ_F32 and ZPQ_F16 results: elements are multiplied as 16-bit floats of binary32's range,
+ *   which holds them exactly, at half the rate; a binary16 result is the binary32 one rounded.  An
+ *   element over the largest binary32 is infinite there, and one below 2^-126 may count as 0.
+ *   ZPQ_BF16 results: the 8-bit matrix instructions drop what lies more than about 2^-19 below the
+ *   largest of the products that they add at a time, whether that cancels or not: at most 2^-18 of a
+ *   block's largest product for each of its elements; as a root mean square 1e-5 of a sum of like
+ *   values, 5e-5 (9e-5) with one element in a hundred 30 (1000) times as large, far below the
+ *   result's rounding, 1.7e-3.
+ * With x, dy the input and output gradient [tokens, .] and w [outputs, inputs]: y = x w^T;
+ * dx = dy w takes w's transposed tiles for B; dw = dy^T x takes both along their columns.
  *   out [m] rows of n elements of out_dtype, ld apart; read with accumulate only
  *   workspace: zpq_matmul_f8_bytes bytes of device memory (0 for most sizes),
  *   16-byte aligned, contents irrelevant
