@@ -1078,9 +1078,10 @@ class Muon:
     Whole matrices: a rank of a sharded step gives those that it owns.  Tensors are kept and
     their addresses laid out once, on `stream` (the current one by default; later calls must come
     after it in stream order): storage must not be replaced meanwhile; set_grads() takes other
-    gradients.  The object's memory, which the steps work in, holds about 12 bytes for each element
-    of its largest matrix, or of 2^26 elements of smaller ones.  A captured graph holds its addresses: keep
-    the object as long as the graph."""
+    gradients.  The object's memory, which the steps work in, holds about 14 bytes for each element
+    of the matrices that are worked on at a time: its largest one, or consecutive ones up to 2^26
+    elements and 1 GiB; and up to 0.5 GiB for parts of long sums (zpq.h).  A captured graph holds
+    its addresses: keep the object as long as the graph."""
 
     def __init__(self, params, grads, copies=None, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None,
                  steps=5, coeffs=NEWTON_SCHULZ, momenta=None, stream=None):

@@ -33,7 +33,8 @@ constexpr int64_t kMaxSide = 1 << 22;         // a row of 16-bit operands is at 
 constexpr int kFew = 32;                      // sides that go by one small matrix
 constexpr int kLong = 256;                    // of the other side, what a workgroup takes then
 constexpr int kOneSide = 64, kOneLong = 256;  // matrices that one workgroup works on, in LDS
-constexpr int64_t kGroup = 1 << 26;           // elements that are worked on at a time
+constexpr int64_t kGroup = 1 << 26;           // elements that are worked on at a time,
+constexpr int64_t kGroupBytes = 1 << 30;      // and bytes of workspace: 14 an element, more for small matrices
 
 struct Entry {
     const void* g;                            // input
@@ -819,7 +820,8 @@ inline int64_t place(Shape s, int splits, char* at, Entry* e) {
     return used;
 }
 
-// Matrices that are worked on at a time: consecutive ones up to kGroup elements, one at least.
+// Matrices that are worked on at a time: consecutive ones up to kGroup elements and kGroupBytes (without pieces), one at
+// least.
 struct Group {
     int64_t first, end, bytes, parts, cuts, sym, large, full, longs, ones;
     int side_sym, side_full, splits;          // of square products (B), of X', pieces of A's sums (tiles of 256)
@@ -854,11 +856,13 @@ inline int splits_of(int64_t large, int64_t tiles, int side, int64_t longest) {
 template <class SHAPES>
 Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
     Group g{first, first, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    int64_t elems = 0, longest = 0, shortest = kMaxSide;
+    int64_t elems = 0, bytes = 0, longest = 0, shortest = kMaxSide;
     while (g.end < count) {
         const Shape s = shape(g.end);
-        if (elems > 0 && elems + s.rows * s.cols > kGroup) break;
+        const int64_t more = s.rows > 0 && s.cols > 0 ? place(s, 1, nullptr, nullptr) : 0;
+        if (elems > 0 && (elems + s.rows * s.cols > kGroup || bytes + more > kGroupBytes)) break;
         elems += s.rows * s.cols;
+        bytes += more;
         if (s.rows > 0 && s.cols > 0) {
             g.parts += parts_of(s);
             g.cuts += tiled(s) ? cuts_of(s) : 0;

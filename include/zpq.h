@@ -436,8 +436,10 @@ zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64
  *   x     [rows] rows of cols elements of x_dtype, ld_x apart, matrices stride_x apart
  *   out   likewise; out_dtype ZPQ_F16 or ZPQ_BF16
  *   workspace: zpq_orthogonalize_bytes bytes of device memory, 256-byte aligned,
- *   contents irrelevant.  Matrices are worked on about 2^26 elements at a time, which
- *   bounds it.
+ *   contents irrelevant: ZPQ_MUON_BYTES(count), and room for the matrices that are worked on at a
+ *   time, consecutive ones up to 2^26 elements and 2^30 bytes, one at least, with up to 2^29 bytes
+ *   for parts of long sums.  A matrix takes about 14 bytes an element; one with a side up to
+ *   32 takes 4, and 32 for each element of the other side, 13 KB at least.
  */
 zpq_status zpq_orthogonalize_bytes(int64_t count, int64_t rows, int64_t cols, int64_t* bytes);
 zpq_status zpq_orthogonalize(const void* x, int32_t x_dtype, int64_t count, int64_t rows,
