@@ -119,7 +119,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(Quant q, int64_t count)
 template <int DT, int KIND, bool TILE, bool ROWS, bool COLS>
 __global__ __launch_bounds__(kThreads) void k_quant_tile(Quant q) {
     __shared__ uint32_t most_of[TILE ? 4 : 4 * kBlock];
-    __shared__ u32x2 turned[COLS ? kBlock * 16 : 1];
+    __shared__ __attribute__((aligned(16))) u32x2 turned[COLS ? kBlock * 16 : 1];
+    static_assert(__alignof__(turned) >= alignof(u32x4), "read 16 bytes at a time");
     const uint32_t t = threadIdx.x, c = t & 15, r = t >> 4, wave = t >> 6;
     const uint32_t cb = blockIdx.x % q.blocks, rb = blockIdx.x / q.blocks;
     const int64_t row = (int64_t)rb * kBlock + r * 8, col = (int64_t)cb * kBlock + c * 8;
@@ -196,7 +197,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_tile(Quant q) {
 
 // Codes of tiles the other way round, as k_quant_tile writes both.
 __global__ __launch_bounds__(kThreads) void k_transpose(Quant q) {
-    __shared__ u32x2 turned[kBlock * 16];
+    __shared__ __attribute__((aligned(16))) u32x2 turned[kBlock * 16];
+    static_assert(__alignof__(turned) >= alignof(u32x4), "read 16 bytes at a time");
     const uint32_t t = threadIdx.x, c = t & 15, r = t >> 4;
     const uint32_t cb = blockIdx.x % q.blocks, rb = blockIdx.x / q.blocks;
     const int64_t row = (int64_t)rb * kBlock + r * 8;
