@@ -57,14 +57,14 @@ __device__ __forceinline__ uint32_t scalar(uint32_t x) { return (uint32_t)__buil
 // lane.  Not the builtin: the compiler waits for it before any later LDS read.  These
 // have no result register; whoever reads the bytes waits by wait_copies() and a barrier.
 // `offset` and `to` are the same in all lanes.  (Five wait states: a scalar register that a vector
-// instruction has written may be an operand.)  Nothing else in these kernels uses m0.
+// instruction has written may be an operand.)
 __device__ __forceinline__ void copy16(i32x4 from, uint32_t lane_offset, uint32_t offset, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(scalar(to)), "v"(lane_offset), "s"(from), "s"(scalar(offset)) : "memory");
+                 :: "s"(scalar(to)), "v"(lane_offset), "s"(from), "s"(scalar(offset)) : "m0", "memory");
 }
 __device__ __forceinline__ void copy4(i32x4 from, uint32_t lane_offset, uint32_t offset, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :: "s"(scalar(to)), "v"(lane_offset), "s"(from), "s"(scalar(offset)) : "memory");
+                 :: "s"(scalar(to)), "v"(lane_offset), "s"(from), "s"(scalar(offset)) : "m0", "memory");
 }
 // Until at most LEFT of the wave's memory accesses, the latest ones, are under way.
 template <int LEFT = 0>
