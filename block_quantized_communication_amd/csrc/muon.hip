@@ -402,7 +402,7 @@ __global__ __launch_bounds__(TILE::kThreadsWg, TILE::kWaves) void k_symmetric(Wo
 
 // A = X X^T with each tile's sum over the long side in `splits` pieces: few large tiles leave part of the chip
 // idle (136 of 256 CUs for a side of 4096), small ones cannot feed the matrix cores. 4096 x 16,384: 469 us in tiles of
-// 128, 296 + 42 us to join 3 pieces.
+// 128, 277 + 28 us to join 3 pieces, 274 + 41 with 5.
 template <class TILE>
 __global__ __launch_bounds__(TILE::kThreadsWg, 2) void k_symmetric_split(Work w, uint32_t tiles, int32_t splits) {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::kLds];
@@ -828,15 +828,19 @@ struct Group {
 };
 // Tiles of 256 where they keep half of the 256 CUs busy (4096 x 4096: 1603 us, with tiles of 128 for the
 // symmetric products 1892), of 128 where they fill them once, else of 64.  For A of matrices of different lengths
-// three quarters: the longest sum decides (a layer's four matrices: 177 us, 164 with tiles of 128).
+// three quarters, measured at one set only: the four matrices of a layer of hidden 2048, 144 large tiles whose longest sums
+// decide (177 us, 164 with tiles of 128).
 constexpr int64_t kHalfBusy = 128;
 template <class COUNT>
 inline int side_of(COUNT count, int64_t least) { return count(256) >= least ? 256 : count(128) >= 256 ? 128 : 64; }
 
 // Pieces of A's sums with tiles of 256 (1: none, and tiles of side_sym). Time in slabs of a tile of 256: rounds of the
 // 256 CUs by slabs of a piece; writing and reading a piece costs a CU about as much as 10 slabs (measured: 256 KB
-// twice, 1.4 us a slab). For matrices of one length only: sums of different length even out by themselves (a layer's
-// four matrices: 163 us without, 190 with). A slab of a 128 tile takes 2/3 of it, two at a time on a CU, of a 64 one 2/5, four at a time.
+// twice, 1.4 us a slab), up to 23 where all CUs do. So pieces, and each further one, have to be better by more than
+// that error: without the 0.95, 4096 x 16,384 took 5 pieces (5649 us as a whole, with 3 5563, a twelfth less memory),
+// 2043 x 3411 7 (592, without 539), 498 x 3061 8 (244, without 193); what it loses is 6502 x 13,571 (11,317 with 2, without
+// 11,584). For matrices of one length only: a layer's four matrices take 163 us without, 190 with. A slab of a 128 tile takes
+// 2/3 of it, two at a time on a CU, of a 64 one 2/5, four at a time.
 inline int splits_of(int64_t large, int64_t tiles, int side, int64_t longest) {
     const int64_t slabs = div_up(longest, 64);
     const double now = side == 256 ? (double)div_up(tiles, 256) * slabs
@@ -845,7 +849,7 @@ inline int splits_of(int64_t large, int64_t tiles, int side, int64_t longest) {
     int splits = 1;
     for (int s = 2; s <= 8 && large > 0; ++s) {
         const double rounds = (double)div_up(large * s, 256), t = rounds * (div_up(slabs, s) + 10);
-        if (t < best) {
+        if (t < best * 0.95) {
             best = t;
             splits = s;
         }
@@ -892,7 +896,7 @@ Group group_at(const SHAPES& shape, int64_t first, int64_t count) {
     return g;
 }
 
-// The table: entries, then where each one's workgroups start, for the three kinds of launches.
+// The table: entries, then where each one's workgroups start, for the six kinds of launches.
 struct Table {
     Entry* entries;
     uint32_t *cut, *sym, *full, *along, *part, *large;

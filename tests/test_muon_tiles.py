@@ -13,7 +13,7 @@ TILES = [(2047, 2050),           # 128; 64 with two buffers
          (2050, 2047),
          (1024, 4096),           # 128; 256, its sums in pieces
          (4095, 1030),
-         (2901, 3099),           # 256; 256, in pieces
+         (2901, 3099),           # 256; 128
          (4500, 4600)]           # 256; 256
 
 

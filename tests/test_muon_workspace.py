@@ -27,6 +27,17 @@ def test_bytes_of_an_element(rows, cols, each):
     assert need.value <= TABLE(1) + each * rows * cols
 
 
+@pytest.mark.parametrize("rows,cols,pieces", [(4096, 16384, 3), (4096, 8192, 0), (2043, 3411, 0), (498, 3061, 0)])
+def test_pieces_are_worth_their_memory(rows, cols, pieces):
+    """Room for at most so many parts of A's sums, binary32 in 256 x 256 tiles on and under the diagonal, beside X, its
+    three copies in 16 bits, A and B: sides to 64, and 64 KB of the rest."""
+    up = lambda n: -(-n // 64) * 64  # noqa: E731
+    need, t = ctypes.c_int64(), -(-rows // 256)
+    assert zpq.lib().zpq_orthogonalize_bytes(1, rows, cols, ctypes.byref(need)) == 0
+    room = rows * cols * 4 + rows * up(cols) * 2 + 2 * cols * up(rows) * 2 + 2 * rows * up(rows) * 2
+    assert need.value <= room + rows * cols // 256 + 65536 + pieces * t * (t + 1) // 2 * (256 * 256 * 4)
+
+
 def test_plan():
     need = ctypes.c_int64()
     for shapes in ([(1 + i % 7, 1 + i % 5) for i in range(200000)], [(1, 0)] * 1000 + [(2, 3)] * 150000):
