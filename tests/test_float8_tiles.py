@@ -13,6 +13,7 @@ SIZES = [(5, 200, 700),          # few rows
          (70, 130, 700),         # 64, four buffers; the same
          (999, 4004, 1001),      # 64, two buffers; 128
          (1500, 1601, 1100),     # 64, two buffers; the same
+         (999, 4004, 4100),      # 64, two buffers; 128, the sum in two parts
          (3000, 3300, 700),      # 256; 128
          (2816, 4864, 700)]      # 256; 256
 
