@@ -425,8 +425,11 @@ zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64
  *       A = X X^T;  X = a X + (b A + c A A) X
  * which drives the singular values that are not 0 to about 1: with (3.4445, -4.7750, 2.0315)
  * five times, to between 0.7 and 1.2.  Products take 16-bit operands (11 bits), with
- * sums and X itself in binary32; the result is within about 2e-3 of the exact iteration's, so it
- * comes in 16 bits.  A matrix with a value that is not finite comes out as NaN.
+ * sums and X itself in binary32.  As a root mean square the result is within 2e-3 of the exact
+ * iteration's for dense matrices of full rank, 1e-3 for those of low rank, and within 3.5e-3 where only a few
+ * rows or columns differ or are not 0, so that roundings add up; so it comes in 16 bits.  A side up to
+ * 32 goes in 64 bits, to the result's own rounding.  A matrix with a value that is not finite comes
+ * out as NaN.
  * 1 <= steps <= 32, coefficients at most 64 in size, such that the entries of A and of
  * b A + c A A stay under 60 (binary16 at the operands' scale; over it results are not finite).
  * rows, cols <= 2^22, rows * cols <= 2^34.
