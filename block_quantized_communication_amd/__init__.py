@@ -968,7 +968,9 @@ def matmul_f8(a, b, out_dtype=None, out=None, accumulate=False, stream=None):
     type, along rows or in tiles) -> [m, n] of out_dtype (bfloat16 by default), or
     out, added to it with accumulate.  Sums are in binary32 for float32 and float16 results.  For
     bfloat16 ones, at twice the rate, the matrix core drops low bits beside large elements: up to 9e-5
-    of the result as a root mean square, where its rounding is 1.7e-3 (zpq.h).  With x, dy [tokens, .]
+    of the result as a root mean square, where its rounding is 1.7e-3 (zpq.h).  A pair says its
+    columns in whole blocks only: a and b need as many blocks, and the shorter one counts as padded
+    with the zeros that it is quantized with.  With x, dy [tokens, .]
     and w [outputs, inputs]: y = x w^T; dx = dy w = matmul_f8(dy, transpose_f8(*w)); dw = dy^T x, of
     both along their columns."""
     torch = _torch()
@@ -1190,7 +1192,9 @@ class Muon:
     def step(self, lr=None, grad_scale=1.0, sumsq=None, max_norm=None, stream=None):
         """One step.  sumsq: float64 [1] on the GPU, the squared norm of the unscaled gradients over all
         ranks and optimizers; where it is not finite nothing changes.  max_norm: clip the scaled
-        gradients to it (needs sumsq)."""
+        gradients to it (needs sumsq).  lr, momentum, grad_scale and max_norm are numbers of this call: a
+        captured step goes on with those it was captured with (there is no DeviceHyper for it; capture it
+        again to change them), while sumsq and the gradients are read at each replay."""
         norm = None
         if sumsq is not None:
             _need(sumsq, _torch().float64, 1, "sumsq", self.device)

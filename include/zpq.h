@@ -350,7 +350,7 @@ zpq_status zpq_embedding_grad(const void* dy, int32_t dy_dtype, int64_t ld_dy, c
  *
  * A matrix [rows, cols] in 8-bit floating point, quantized along its rows:
  *   codes   [rows][128 * kb] bytes, kb = ceil(cols / 128): OCP E4M3 or E5M2; codes
- *           past the last column are 0
+ *           past the last column are 0 (0 or NaN in a block with a value that is not finite)
  *   scales  [rows][kb4] exponent bytes, kb4 = kb rounded up to a multiple of 4; those
  *           past kb are 0.  One for each 128 elements of a row, or in tiles, [ceil(rows / 128)][kb4]:
  *           one for each 128 x 128.
@@ -408,7 +408,8 @@ typedef struct {
  *   out [m] rows of n elements of out_dtype, ld apart; read with accumulate only
  *   workspace: zpq_matmul_f8_bytes bytes of device memory (0 for most sizes),
  *   16-byte aligned, contents irrelevant
- * m < 2^31, n <= 2^26, ceil(m / 64) * ceil(n / 64) < 2^23; k = 0 is a sum of nothing.
+ * m < 2^31, n <= 2^26, ceil(m / 64) * ceil(n / 64) < 2^23; k = 0 is a sum of nothing.  Whole
+ * blocks are summed: codes past k count, and are 0 as quantized.
  */
 zpq_status zpq_matmul_f8_bytes(int64_t m, int64_t n, int64_t k, int64_t* bytes);
 zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64_t m, int64_t n,
@@ -425,11 +426,10 @@ zpq_status zpq_matmul_f8(const zpq_f8_operand* a, const zpq_f8_operand* b, int64
  *       A = X X^T;  X = a X + (b A + c A A) X
  * which drives the singular values that are not 0 to about 1: with (3.4445, -4.7750, 2.0315)
  * five times, to between 0.7 and 1.2.  Products take 16-bit operands (11 bits), with
- * sums and X itself in binary32.  As a root mean square the result is within 2e-3 of the exact
- * iteration's for dense matrices of full rank, 1e-3 for those of low rank, and within 3.5e-3 where only a few
- * rows or columns differ or are not 0, so that roundings add up; so it comes in 16 bits.  A side up to
- * 32 goes in 64 bits, to the result's own rounding.  A matrix with a value that is not finite comes
- * out as NaN.
+ * sums and X itself in binary32.  As a root mean square the result is within 2.5e-3 of the exact
+ * iteration's (less for large matrices and low ranks), 3.5e-3 where only a few rows or columns
+ * differ or are not 0, so that roundings add up; so it comes in 16 bits.  A side up to 32 goes in
+ * 64 bits, to the result's own rounding.  A matrix with a value that is not finite comes out as NaN.
  * 1 <= steps <= 32, coefficients at most 64 in size, such that the entries of A and of
  * b A + c A A stay under 60 (binary16 at the operands' scale; over it results are not finite).
  * rows, cols <= 2^22, rows * cols <= 2^34.
