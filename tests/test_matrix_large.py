@@ -37,14 +37,16 @@ def test_quantizing(tile):
 
 
 def test_product_of_a_large_operand():
-    """A of 4.4e9 codes, and a binary32 result of 4.4e9 values, by its last rows."""
+    """A of 4.4e9 codes, by its last rows, within what bfloat16 results lose (zpq.h) and their rounding; a binary32 result of
+    4.4e9 values."""
     b = zpq.quant_f8(randn(70, COLS, seed=1))
     a = zpq.quant_f8(randn(ROWS, COLS))
     got = zpq.matmul_f8(a, b, out_dtype=torch.bfloat16)
     last = ROWS - 1000
     av, bv = (zpq.dequant_f8(*p, dtype=torch.float32).double() for p in ((a[0][last:].clone(), a[1][last:].clone()), b))
-    want, size = av @ bv.t(), av.abs().amax(1)[:, None] * bv.abs().amax(1)[None, :]
-    assert ((got[last:].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2 * COLS * 2.0 ** -18 * size).all()
+    want, most = av @ bv.t(), [v.abs().view(v.shape[0], -1, 8).amax(2) for v in (av, bv)]
+    cut = 7 * 2.0 ** -13 * (most[0] @ most[1].t()) + COLS * 2.0 ** -23 * (av.abs() @ bv.abs().t())
+    assert ((got[last:].double() - want).abs() <= cut + 2.0 ** -8 * (want.abs() + cut)).all()
     del a, got
     one, two = (torch.randint(-4, 5, (n, 128), generator=torch.Generator(device="cuda").manual_seed(n), device="cuda").float() for n in (ROWS, COLS))
     pair = lambda v: (v.to(torch.float8_e4m3fn), torch.tensor([[127, 0, 0, 0]], dtype=torch.uint8, device="cuda").repeat(v.shape[0], 1))  # noqa: E731
