@@ -400,10 +400,10 @@ typedef struct {
  *   element over the largest binary32 is infinite there, and one below 2^-126 may count as 0.
  *   ZPQ_BF16 results: the 8-bit matrix instructions add the products of 8 consecutive elements
  *   (0 to 7, 8 to 15, ...) in units of 2^-13 of the largest's power of two, cutting off what lies
- *   below, also where the large ones cancel: at most 7 * 2^-13 of the largest product of each
- *   8, of which quantizing has already changed 2^-4 (E5M2: 2^-3).  As a root mean square that is 1e-5 of a sum of like
- *   values, 5e-5 (9e-5) with one element in a hundred 30 (1000) times as large; the result's
- *   rounding is 1.7e-3.
+ *   below, also where the large ones cancel: at most 7 * 2^-13 of the largest product of each 8
+ *   (quantizing changes an element by up to 2^-4 of it, E5M2 2^-3).  As a root mean square that is
+ *   1e-5 of a sum of like values, 5e-5 (9e-5) with one element in a hundred 30 (1000) times as
+ *   large; the result's rounding is 1.7e-3.
  * With x, dy the input and output gradient [tokens, .] and w [outputs, inputs]: y = x w^T;
  * dx = dy w takes w's transposed tiles for B; dw = dy^T x takes both along their columns.
  *   out [m] rows of n elements of out_dtype, ld apart; read with accumulate only
